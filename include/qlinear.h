@@ -314,6 +314,91 @@ ql_status qlinear_apply_experts_noalloc(ql_format fmt, const void* w0, const voi
                                         const void* x, ql_dtype x_dtype, int64_t pos_per_row, void* y,
                                         ql_dtype y_dtype, void* stream);
 
+/* ---- Attention side of a decoder layer: what runs between the q, k and v products and the output
+ * product, over a paged cache.  These follow no page; the formulas are stated here.
+ *
+ * Tensors of heads are [t, heads, d] in a 16-bit dtype with d contiguous and any token and head
+ * stride (ELEMENTS, multiples of 8), so that q, k and v may be parts of one fused product or head-
+ * major; pointers 16-byte aligned.  An output may be its own input (the same pointer and strides),
+ * otherwise outputs overlap nothing. */
+
+/* A paged cache: k and v are two arrays of n_pages pages of page_size slots, hk heads of d values
+ * each, with the same strides in ELEMENTS (multiples of 8): token-major pages [page_size, hk, d],
+ * head-major ones [hk, page_size, d] or parts of a larger array.  Slot s is place s % page_size of
+ * page s / page_size.  n_pages * page_size < 2^31. */
+typedef struct {
+  void* k;
+  void* v;
+  int64_t n_pages, page_size, hk, d;
+  int64_t page_stride, token_stride, head_stride;
+} ql_paged_cache;
+
+/* Norm and rotation shared by qlinear_qk_norm_rope and qlinear_kv_append.  For a row x (one head of
+ * one token of q or k), in fp32 and rounded once at the end:
+ *   norm:      y = x * w / sqrt(mean(x^2) + eps), w = q_weight or k_weight [d] in w_dtype (any
+ *              ql_dtype, 16-byte aligned), each NULL for no norm;
+ *   rotation:  for i < rot/2, with (a, b) = (i, i + rot/2), or (2i, 2i+1) when interleaved != 0,
+ *              (c, s) = (cos_sin[p][i], cos_sin[p][rot/2 + i]) and p = positions[token]:
+ *              (y_a c - y_b s, y_b c + y_a s); values from rot on stay.  cos_sin is fp32 [max_pos, rot],
+ *              16-byte aligned; positions int64 [t], 8-byte aligned.  rot = 0: no rotation (both
+ *              unused).  A position outside [0, max_pos) gives zero rows of q and k.
+ * d a multiple of 8 up to 512; rot a multiple of 16, 0 <= rot <= d. */
+typedef struct {
+  const void* q_weight;
+  const void* k_weight;
+  ql_dtype w_dtype;
+  float eps;
+  const int64_t* positions;
+  const float* cos_sin;
+  int64_t max_pos, rot;
+  int interleaved;
+} ql_norm_rope;
+
+/* Heads of a tensor: pointer, head count, strides in elements. */
+typedef struct {
+  void* p;
+  int64_t heads, token_stride, head_stride;
+} ql_heads;
+
+/* q_out = norm_rope(q), k_out = norm_rope(k): the rows of t tokens, both in one launch.  q or k may
+ * have 0 heads (its pointers are then unused).  q_out and k_out have q's and k's head counts. */
+ql_status qlinear_qk_norm_rope(const ql_heads* q, const ql_heads* q_out, const ql_heads* k, const ql_heads* k_out,
+                               ql_dtype dtype, int64_t t, int64_t d, const ql_norm_rope* nr, void* stream);
+
+/* Append to a paged cache: cache.k[slots[i]] = norm_rope(k[i]), cache.v[slots[i]] = v[i], and, where q
+ * has heads, q_out[i] = norm_rope(q[i]), in one launch.  slots: int64 [t], 8-byte aligned; a slot
+ * outside [0, n_pages * page_size) stores nothing (padding tokens); the others must be distinct.
+ * k and v have cache.hk heads; every tensor and the cache share dtype (QL_F16 or QL_BF16). */
+ql_status qlinear_kv_append(const ql_heads* q, const ql_heads* q_out, const ql_heads* k, const ql_heads* v,
+                            const ql_paged_cache* cache, const int64_t* slots, ql_dtype dtype, int64_t t,
+                            const ql_norm_rope* nr, void* stream);
+
+/* Causal attention of new tokens over a paged cache that already holds their keys and values.
+ * Sequence s owns the query tokens [cu_q[s], cu_q[s+1]) of q and the cached positions [0, kv_lens[s]),
+ * its new tokens the last ones: query i of n is at position p = kv_lens[s] - n + i and sees the
+ * positions j <= p, with j > p - window where window > 0.  Position j lies in page
+ * block_table[s][j / page_size], place j % page_size; positions in a page outside [0, n_pages) are not
+ * seen, and neither are unused slots' values, whatever they hold.
+ *   out = sum_j e^(scale q.k_j) v_j / (sum_j e^(scale q.k_j) + e^(sinks[h]))
+ * per query head h (sinks: fp32 [hq] or NULL for no such term); kv head h / (hq / hk).  A row that
+ * sees nothing is zero.  Scores, softmax sums and the output are accumulated in fp32; the softmax
+ * weights enter the product with v rounded to the 16-bit dtype.
+ * cu_q int32 [n_seqs + 1] (not decreasing, from 0), kv_lens int32 [n_seqs] and block_table int32 [n_seqs]
+ * rows of max_pages entries, table_stride apart, are DEVICE memory (4-byte aligned) and not known to the
+ * host: max_q is the host's bound on a sequence's new tokens, t the rows of q and out.  Whatever the
+ * device values, nothing outside the arrays is touched: lengths are cut to t, max_q and
+ * max_pages * page_size (below 2^30, as is t * hq / hk).  Rows of out that belong to no sequence are left as they are.
+ * d in {64, 128, 256}; hq a multiple of cache.hk; scale finite and > 0; window >= 0 (0: none).
+ * Needs a device workspace of qlinear_paged_attention_workspace_size bytes, 16-byte aligned: the
+ * partial results of rows whose keys are split over workgroups. */
+size_t qlinear_paged_attention_workspace_size(int64_t t, int64_t n_seqs, int64_t hq, int64_t hk, int64_t d,
+                                              int64_t max_q, int64_t max_pages, int64_t page_size, int64_t window);
+ql_status qlinear_paged_attention(const ql_heads* q, const ql_heads* out, ql_dtype dtype, int64_t t,
+                                  const ql_paged_cache* cache, const int32_t* block_table, int64_t table_stride,
+                                  int64_t max_pages, const int32_t* cu_q, const int32_t* kv_lens, int64_t n_seqs,
+                                  int64_t max_q, float scale, int64_t window, const float* sinks, void* workspace,
+                                  size_t ws_bytes, void* stream);
+
 /* Message of the last failing call on this thread ("" after a successful call).  Errors name the
  * offending argument, as the Nx_quant API docs' constructors and products name the part they
  * reject (Weights; Products, "Raises Invalid_argument ... naming the part"). */

@@ -43,6 +43,10 @@ __all__ = [
     "qlinear_apply_experts",
     "qlinear_apply_experts_workspace_size",
     "qlinear_apply_experts_noalloc",
+    "qlinear_qk_norm_rope",
+    "qlinear_kv_append",
+    "qlinear_paged_attention",
+    "qlinear_paged_attention_workspace_size",
     "qlinear_version",
 ]
 
@@ -89,6 +93,23 @@ class _Problem(ctypes.Structure):
     ]
 
 
+class _Heads(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("heads", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class _PagedCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p)] + [
+        (f, ctypes.c_int64)
+        for f in ("n_pages", "page_size", "hk", "d", "page_stride", "token_stride", "head_stride")]
+
+
+class _NormRope(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("w_dtype", ctypes.c_int),
+                ("eps", ctypes.c_float), ("positions", ctypes.c_void_p), ("cos_sin", ctypes.c_void_p),
+                ("max_pos", ctypes.c_int64), ("rot", ctypes.c_int64), ("interleaved", ctypes.c_int)]
+
+
 _LIB = None
 _P, _I64, _INT, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
 
@@ -113,6 +134,11 @@ _SIGNATURES = {
     "qlinear_apply_experts_workspace_size": (_SZ, [_I64, _I64]),
     "qlinear_apply_experts": (_INT, [_INT, _P, _P, _I64, _I64, _I64, _P, _I64, _P, _INT, _I64, _P, _INT, _P, _SZ, _P]),
     "qlinear_apply_experts_noalloc": (_INT, [_INT, _P, _P, _I64, _I64, _I64, _P, _I64, _P, _INT, _I64, _P, _INT, _P]),
+    "qlinear_qk_norm_rope": (_INT, [_P, _P, _P, _P, _INT, _I64, _I64, _P, _P]),
+    "qlinear_kv_append": (_INT, [_P, _P, _P, _P, _P, _P, _INT, _I64, _P, _P]),
+    "qlinear_paged_attention_workspace_size": (_SZ, [_I64] * 9),
+    "qlinear_paged_attention": (_INT, [_P, _P, _INT, _I64, _P, _P, _I64, _I64, _P, _P, _I64, _I64, ctypes.c_float, _I64,
+                                       _P, _P, _SZ, _P]),
     "qlinear_last_error": (ctypes.c_char_p, []),
     "qlinear_version": (ctypes.c_char_p, []),
 }
@@ -440,3 +466,153 @@ def qlinear_apply_experts_noalloc(fmt: int, w0, w1, ids, x, *, n: int, k: int, y
     _check(lib.qlinear_apply_experts_noalloc(fmt, _ptr(w0), _ptr(w1), e, n, k, _ptr(ids), ids.numel(), _ptr(x), _dt(x),
                                              pos_per_row, _ptr(y), _dt(y), _stream()))
     return y
+
+
+def _ref(s):
+    return None if s is None else ctypes.addressof(s)
+
+
+def _need(ok, status: int, message: str):
+    if not ok:
+        raise QLError(status, message)
+
+
+def _one_gpu(*tensors):
+    """All given tensors are on one GPU."""
+    on = {t.device for t in tensors if t is not None}
+    _need(len(on) == 1 and next(iter(on)).type == "cuda", 2, f"every tensor must be on one GPU, not on {on}")
+
+
+def _dense(t, name: str, dtype, shape=None):
+    """A contiguous tensor argument of the given dtype and shape, or None."""
+    if t is not None:
+        _need(t.dtype == dtype, 3, f"{name} must have dtype {dtype}")
+        _need(shape is None or tuple(t.shape) == tuple(shape), 2, f"{name} must have shape {tuple(shape or ())}")
+        _need(t.is_contiguous(), 2, f"{name} must be contiguous")
+    return t
+
+
+def _heads(x, name: str, like=None):
+    """The ql_heads of a [t, heads, d] tensor (None: absent)."""
+    if x is None:
+        return None
+    _need(x.dim() == 3, 2, f"{name} must be [tokens, heads, d]")
+    _need(x.stride(2) == 1 or x.shape[2] <= 1, 2, f"{name}'s last dimension must be contiguous")
+    if like is not None:
+        _need(x.shape[0] == like.shape[0] and x.shape[2] == like.shape[2], 2,
+              f"{name} must have the tokens and the head size of the other tensors")
+        _need(x.dtype == like.dtype, 3, f"{name} must have dtype {like.dtype}")
+    # the stride of a dimension of one is free in torch: any legal value will do
+    ts = x.stride(0) if x.shape[0] > 1 else 0
+    hs = x.stride(1) if x.shape[1] > 1 else 0
+    return _Heads(_ptr(x), x.shape[1], ts, hs)
+
+
+def _paged_cache(k_cache, v_cache):
+    _need(k_cache.dim() == 4 and k_cache.shape == v_cache.shape, 2,
+          "k_cache and v_cache must both be [n_pages, page_size, heads, d]")
+    _need(k_cache.dtype == v_cache.dtype, 3, "k_cache and v_cache must have one dtype")
+    size = [k_cache.size(i) for i in range(4)]
+    sk, sv = ([c.stride(i) if size[i] > 1 else 0 for i in range(3)] for c in (k_cache, v_cache))
+    _need(sk == sv, 2, "k_cache and v_cache must have the same strides")
+    _need(size[3] <= 1 or (k_cache.stride(3) == 1 and v_cache.stride(3) == 1), 2,
+          "the caches' last dimension must be contiguous")
+    return _PagedCache(_ptr(k_cache), _ptr(v_cache), *size, sk[0], sk[1], sk[2])
+
+
+def _norm_rope(d, t, q_weight, k_weight, eps, positions, cos_sin, interleaved):
+    torch = _torch()
+    w = q_weight if q_weight is not None else k_weight
+    for name, x in (("q_weight", q_weight), ("k_weight", k_weight)):
+        _dense(x, name, w.dtype if w is not None else None, (d,))
+    _dense(positions, "positions", torch.int64, (t,))
+    _dense(cos_sin, "cos_sin", torch.float32)
+    _need(cos_sin is None or cos_sin.dim() == 2, 2, "cos_sin must be [positions, rotated values]")
+    rows, rot = (0, 0) if cos_sin is None else cos_sin.shape
+    return _NormRope(_ptr(q_weight), _ptr(k_weight), _dt(w) if w is not None else _QL_F32, eps, _ptr(positions),
+                     _ptr(cos_sin), rows, rot, 1 if interleaved else 0)
+
+
+def qlinear_qk_norm_rope(q, k, *, q_weight=None, k_weight=None, eps: float = 1e-6, positions=None, cos_sin=None,
+                         interleaved: bool = False, q_out=None, k_out=None):
+    """RMS norms of q [t, hq, d] and k [t, hk, d] (either may be None) per head, then the rotation by
+    the rows of cos_sin (fp32 [max_pos, rot]: rot/2 cosines, rot/2 sines) that positions (int64 [t])
+    name -> (q_out, k_out).  q and k may be strided parts of one tensor, and q_out may be q."""
+    torch = _torch()
+    lib = load_library()
+    x = q if q is not None else k
+    _need(x is not None, 1, "q and k must not both be None")
+    t, _, d = x.shape
+    if q is not None and q_out is None:
+        q_out = torch.empty(tuple(q.shape), dtype=q.dtype, device=q.device)
+    if k is not None and k_out is None:
+        k_out = torch.empty(tuple(k.shape), dtype=k.dtype, device=k.device)
+    hq, hqo, hk, hko = (_heads(a, n, x) for a, n in ((q, "q"), (q_out, "q_out"), (k, "k"), (k_out, "k_out")))
+    nr = _norm_rope(d, t, q_weight, k_weight, eps, positions, cos_sin, interleaved)
+    _one_gpu(q, q_out, k, k_out, q_weight, k_weight, positions, cos_sin)
+    _check(lib.qlinear_qk_norm_rope(_ref(hq), _ref(hqo), _ref(hk), _ref(hko), _dt(x), t, d, _ref(nr), _stream()))
+    return q_out, k_out
+
+
+def qlinear_kv_append(k, v, k_cache, v_cache, slots, *, q=None, q_out=None, q_weight=None, k_weight=None,
+                      eps: float = 1e-6, positions=None, cos_sin=None, interleaved: bool = False):
+    """Store k (normed and rotated as qlinear_qk_norm_rope does) and v [t, hk, d] at slots (int64 [t],
+    slot = page * page_size + place; out of range: not stored) of the caches [n_pages, page_size,
+    hk, d] (any strides), in one launch with q's norm and rotation where q [t, hq, d] is given
+    -> q_out (None without q)."""
+    torch = _torch()
+    lib = load_library()
+    t, _, d = k.shape
+    if q is not None and q_out is None:
+        q_out = torch.empty(tuple(q.shape), dtype=q.dtype, device=q.device)
+    cache = _paged_cache(k_cache, v_cache)
+    _need(k_cache.dtype == k.dtype, 3, f"the caches must have dtype {k.dtype}")
+    _need(cache.d == d, 2, f"the caches must have head size {d}")
+    hq, hqo, hk, hv = (_heads(a, n, k) for a, n in ((q, "q"), (q_out if q is not None else None, "q_out"), (k, "k"),
+                                                    (v, "v")))
+    _dense(slots, "slots", torch.int64, (t,))
+    nr = _norm_rope(d, t, q_weight, k_weight, eps, positions, cos_sin, interleaved)
+    _one_gpu(q, q_out, k, v, k_cache, v_cache, slots, q_weight, k_weight, positions, cos_sin)
+    _check(lib.qlinear_kv_append(_ref(hq), _ref(hqo), _ref(hk), _ref(hv), _ref(cache), _ptr(slots), _dt(k), t, _ref(nr),
+                                 _stream()))
+    return q_out
+
+
+def qlinear_paged_attention_workspace_size(q, k_cache, block_table, *, max_q: int, window: int = 0) -> int:
+    t, hq, d = q.shape
+    return int(load_library().qlinear_paged_attention_workspace_size(
+        t, block_table.shape[0], hq, k_cache.shape[2], d, max_q, block_table.shape[1], k_cache.shape[1], window))
+
+
+def qlinear_paged_attention(q, k_cache, v_cache, block_table, cu_q, kv_lens, *, max_q: int, scale=None,
+                            window: int = 0, sinks=None, out=None, workspace=None):
+    """Causal attention of new tokens q [t, hq, d] over the caches [n_pages, page_size, hk, d] that hold
+    their k and v already.  Sequence s has the queries cu_q[s] .. cu_q[s+1] (int32 [n_seqs + 1]), which
+    are the last of its kv_lens[s] positions (int32 [n_seqs]) in the pages block_table[s] (int32
+    [n_seqs, max_pages]); max_q bounds a sequence's queries.  scale defaults to d^-1/2; window > 0: a
+    query sees its last `window` positions; sinks fp32 [hq].  -> out [t, hq, d]."""
+    torch = _torch()
+    lib = load_library()
+    t, hq, d = q.shape
+    if out is None:
+        out = torch.empty(tuple(q.shape), dtype=q.dtype, device=q.device)
+    cache = _paged_cache(k_cache, v_cache)
+    _need(k_cache.dtype == q.dtype, 3, f"the caches must have dtype {q.dtype}")
+    _need(cache.d == d, 2, f"the caches must have head size {d}")
+    _need(block_table.dim() == 2 and block_table.dtype == torch.int32, 3, "block_table must be int32 [n_seqs, max_pages]")
+    n_seqs, max_pages = block_table.shape
+    _need(max_pages <= 1 or block_table.stride(1) == 1, 2, "block_table's rows must be contiguous")
+    _dense(cu_q, "cu_q", torch.int32, (n_seqs + 1,))
+    _dense(kv_lens, "kv_lens", torch.int32, (n_seqs,))
+    _dense(sinks, "sinks", torch.float32, (hq,))
+    hqs, hout = _heads(q, "q"), _heads(out, "out", q)
+    if workspace is None:
+        need = qlinear_paged_attention_workspace_size(q, k_cache, block_table, max_q=max_q, window=window)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    _one_gpu(q, out, k_cache, v_cache, block_table, cu_q, kv_lens, sinks, workspace)
+    _check(lib.qlinear_paged_attention(_ref(hqs), _ref(hout), _dt(q), t, _ref(cache), _ptr(block_table),
+                                       block_table.stride(0) if n_seqs > 1 else max_pages, max_pages, _ptr(cu_q),
+                                       _ptr(kv_lens), n_seqs, max_q, d ** -0.5 if scale is None else scale, window,
+                                       _ptr(sinks), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                       _stream()))
+    return out

@@ -18,7 +18,8 @@ LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libqlinear.so")
 SOURCES = ["qlinear_api.cpp", "quantize.hip", "dequant.hip", "gemv.hip", "gemv_m1.hip", "gemv_m2.hip", "gemv_m4.hip",
            "gemv_m8.hip", "gemm.hip", "experts.hip", "experts_mx.hip",
-           "experts_q8.hip", "experts_kq.hip", "gemv_stream.hip", "take.hip", "transcode.hip"]
+           "experts_q8.hip", "experts_kq.hip", "gemv_stream.hip", "take.hip", "transcode.hip",
+           "norm_rope.hip", "attn_few.hip", "attn_tile.hip"]
 FLAGS = [
     "--offload-arch=gfx950",
     "-O3",
@@ -27,12 +28,13 @@ FLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-I" + os.path.join(ROOT, "include"),
 ]
-# Matrix-core kernels whose VALU reads the accumulators in the loop (to apply group scales) keep
+# Matrix-core kernels whose VALU reads the accumulators in the loop (to apply group scales, or to
+# turn attention scores into weights and rescale sums) keep
 # them in the architectural VGPRs (accumulation registers would need a move per element); the
 # GEMM's accumulators are only read in its epilogue and may live in the accumulation registers.
 FILE_FLAGS = {
     f: ["-mllvm", "-amdgpu-mfma-vgpr-form"]
-    for f in ("gemv_m1.hip", "gemv_m2.hip", "gemv_m4.hip", "gemv_m8.hip")
+    for f in ("gemv_m1.hip", "gemv_m2.hip", "gemv_m4.hip", "gemv_m8.hip", "attn_few.hip", "attn_tile.hip")
 }
 
 

@@ -1,0 +1,249 @@
+// Shared parts of the paged attention kernels (attn_few.hip, attn_tile.hip): the split of the work over workgroups, the copy of cache rows into LDS and
+// the register tiles of the two products.
+//
+// Mathematics.  For one query row with scores s_j (log2 units: scale * log2(e) * q.k_j) the kernels
+// hold M (a reference not below the maximum by more than 2^kLazy), l = sum 2^(s_j - M) and
+// O = sum 2^(s_j - M) v_j in fp32; pieces of a row join as
+// sum_p 2^(M_p - M) O_p / sum_p 2^(M_p - M) l_p.  Both products run transposed, S^T = K Q^T and
+// O^T = V^T P^T, so that a lane holds one query column: the maximum, the sum and the rescaling of
+// a row are per-lane scalars, and the lane's scores are already the P^T operand of the second
+// product under a permutation of the keys that the V^T reads follow.
+#pragma once
+#include "device_common.hpp"
+#include "launch.hpp"
+
+namespace ql {
+
+typedef __attribute__((address_space(3))) void at_lds_void;
+typedef __attribute__((ext_vector_type(4))) short s16x4_t;
+typedef __attribute__((address_space(3))) s16x4_t at_lds_s16x4;
+typedef __attribute__((ext_vector_type(2))) float f32x2_t;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNegInf = -__builtin_inff();
+// The reference M is raised only when a tile's maximum passes it by more than 2^8: P stays below
+// 256 (exact range of both 16-bit types), and most tiles skip the rescaling of O.
+constexpr float kLazy = 8.0f;
+
+// 16-bit products with fp32 accumulation.
+__device__ __forceinline__ f32x4_t mfma16(BF16, u32x4_t a, u32x4_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
+                                                 0, 0, 0);
+}
+__device__ __forceinline__ f32x4_t mfma16(F16, u32x4_t a, u32x4_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0,
+                                                0, 0);
+}
+__device__ __forceinline__ f32x16_t mfma32(BF16, u32x4_t a, u32x4_t b, f32x16_t c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
+                                                 0, 0, 0);
+}
+__device__ __forceinline__ f32x16_t mfma32(F16, u32x4_t a, u32x4_t b, f32x16_t c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0,
+                                                0, 0);
+}
+// Two fp32 values rounded to nearest even into one word.
+__device__ __forceinline__ uint32_t pack2(BF16, float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
+}
+__device__ __forceinline__ uint32_t pack2(F16, float a, float b) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, f16x2_t));
+}
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// x joined with its value in the other half (lanes +-32) or the other 16 of each 32 lanes.
+template <typename F> __device__ __forceinline__ float join32(float x, F f) {
+  const uint32_t u = __float_as_uint(x);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return f(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+template <typename F> __device__ __forceinline__ float join16(float x, F f) {
+  const uint32_t u = __float_as_uint(x);
+  const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return f(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+struct MaxF {
+  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+struct SumF {
+  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+
+// Factor of a piece with reference m and sum l when pieces join under the reference mt.  A piece
+// that saw nothing has m = -inf and l = 0; one whose every score is NaN has m = -inf and l = NaN,
+// and keeps its NaN.
+__device__ __forceinline__ float join_factor(float m, float l, float mt) {
+  return m == kNegInf ? (l == 0.f ? 0.f : 1.f) : exp2_fast(m - mt);
+}
+
+// A V row that some query rows of a tile see and others do not may hold infinities or NaN, and zero
+// times those is not zero.  Tiles with such rows are checked; if one holds any, its non-finite
+// values are added one key at a time to the rows that see them, and the product takes zeros there.
+template <typename T> struct Bits16;
+template <> struct Bits16<BF16> {
+  static constexpr uint32_t expo = 0x7f80u, step = 0x0080u;
+};
+template <> struct Bits16<F16> {
+  static constexpr uint32_t expo = 0x7c00u, step = 0x0400u;
+};
+// Bit 15 of a half is set when that half of w is infinite or NaN.
+template <typename T> __device__ __forceinline__ uint32_t nonfinite2(uint32_t w) {
+  return (w & (Bits16<T>::expo * 0x10001u)) + Bits16<T>::step * 0x10001u;
+}
+// The word with its infinite and NaN halves as zero.
+template <typename T> __device__ __forceinline__ uint32_t finite2(uint32_t w) {
+  const uint32_t nf = (nonfinite2<T>(w) & 0x80008000u) >> 15;  // 1 in a half that is not finite
+  return w & ~(nf * 0xffffu);
+}
+// The halves of w that are infinite or NaN, as floats, where `on`; zero otherwise.
+template <typename T> __device__ __forceinline__ void only_nonfinite(uint32_t w, bool on, float& a, float& b) {
+  const uint32_t nf = nonfinite2<T>(w);
+  a = on && (nf & 0x8000u) ? param_to_f32<T>(w & 0xffffu) : 0.f;
+  b = on && (nf & 0x80000000u) ? param_to_f32<T>(w >> 16) : 0.f;
+}
+
+// Position of 16-byte chunk c of row r in a tile of rows of D values: K is read 16 (or 32) rows
+// at one chunk, V 8 rows at two neighbouring chunks (the transposing reads); both then meet every
+// bank once.
+template <int D> __device__ __forceinline__ int swz_k(int r) { return D >= 128 ? (r & 15) : ((r >> 1) & 7); }
+template <int D> __device__ __forceinline__ int swz_v(int r) {
+  return D >= 128 ? ((r & 7) << 1) : (((r >> 1) & 3) << 1);
+}
+
+// One sequence: its query rows [q0, q0 + nq) and cached length kv, kept inside the arrays whatever
+// the device values say.
+struct AttnSeq {
+  int q0, nq, kv;
+};
+__device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int s) {
+  AttnSeq r;
+  const int t = (int)a.t;
+  const int c0 = a.cu_q[s], c1 = a.cu_q[s + 1];
+  r.q0 = min(max(c0, 0), t);
+  r.nq = min(min(max(c1, r.q0), t) - r.q0, a.max_q);
+  r.kv = min(max(a.kv_lens[s], 0), a.max_kv);
+  return r;
+}
+// Whether the few-row kernel takes a sequence (the tile kernel takes the others with nq >= 1).
+__device__ __forceinline__ bool attn_is_few(const AttnArgs& a, int nq) { return nq * a.g <= a.few_rows; }
+
+// Cached positions [lo, hi) that the queries i0 .. i1 of a sequence may see.
+__device__ __forceinline__ void attn_span(const AttnArgs& a, const AttnSeq& q, int i0, int i1, int& lo, int& hi) {
+  hi = max(0, q.kv - q.nq + i1 + 1);
+  const int first = q.kv - q.nq + i0 + 1 - a.window;
+  lo = a.window > 0 ? min(max(0, first), hi) : 0;
+}
+// Tiles of N positions that cover [lo, hi): first tile and count (at least one: a row that sees
+// nothing is still written).
+template <int N> __device__ __forceinline__ int attn_tiles(int lo, int hi, int& first) {
+  first = lo / N;
+  return max(1, (hi + N - 1) / N - first);
+}
+
+// Cache rows of one tile that this wave copies: ROWS rows, row r of the tile looked up by the
+// lanes with lane % ROWS == r.
+template <int ROWS> struct RowLookup {
+  int pos, id;  // the lane's position and its page id
+  __device__ __forceinline__ void load(const AttnArgs& a, const int32_t* table, int base, int lo, int hi, int lane) {
+    pos = base + (lane & (ROWS - 1));
+    id = -1;
+    if (pos >= lo && pos < hi) id = table[a.page_div.div((uint32_t)pos)];
+  }
+  // Byte offset of the row from the head's start, or -1 for a row outside the span or in a page
+  // that the cache does not have.
+  __device__ __forceinline__ int64_t offset(const AttnArgs& a) const {
+    if (id < 0 || id >= a.n_pages) return -1;
+    const uint32_t p = (uint32_t)pos - a.page_div.div((uint32_t)pos) * (uint32_t)a.page_size;
+    return (int64_t)id * a.page_stride + (int64_t)p * a.token_stride;
+  }
+};
+
+// Rows that are not to be seen are copied from here: their V must be zero, since zero times an
+// infinity or a NaN left in an unused slot would not be.
+__device__ __attribute__((aligned(16))) static uint32_t kZeroRow[128] = {};
+
+// Starts a copy of 16 bytes a lane into LDS, lane l's to dst + 16 l (dst is uniform).  Written as
+// an instruction because the compiler, which cannot tell the stages apart, would wait for every
+// copy in flight at each LDS read; the kernels wait by count (attn_wait_vm) for the stage they
+// read.  The copy writes no register; the wait state between m0 and its use is in the text.
+__device__ __forceinline__ void copy16(const uint8_t* src, uint8_t* dst) {
+  const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(at_lds_void*)dst);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(at), "v"(src) : "memory", "m0");
+}
+
+// Copies ROWS rows of D values into LDS at dst (rows back to back, chunks placed by swz), 1 KB per
+// instruction.  off holds the row offsets in the lanes as RowLookup gives them; row0 is the tile
+// row of the first (a multiple of 16).
+template <int D, int ROWS, bool IS_V>
+__device__ __forceinline__ void copy_rows(const uint8_t* base, int64_t off, uint8_t* dst, int lane) {
+  constexpr int CH = D / 8;         // 16-byte chunks of a row
+  constexpr int RPI = 64 / CH;      // rows of an instruction
+  const int rl = lane / CH, c = lane % CH;
+#pragma unroll
+  for (int i = 0; i < ROWS / RPI; ++i) {
+    const int r = i * RPI + rl;
+    const int lo = __shfl((int)off, r), hi = __shfl((int)(off >> 32), r);
+    const int64_t o = ((int64_t)hi << 32) | (uint32_t)lo;
+    const int cs = c ^ (IS_V ? swz_v<D>(r) : swz_k<D>(r));
+    const uint8_t* src = (hi < 0 ? (const uint8_t*)kZeroRow : base + o) + cs * 16;
+    copy16(src, dst + i * 1024);
+  }
+}
+
+__device__ __forceinline__ s16x4_t read_tr(const uint8_t* p) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((at_lds_s16x4*)p);
+}
+// s_waitcnt with only the vector-memory count.
+template <int N> __device__ __forceinline__ void attn_wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+  asm volatile("" ::: "memory");
+}
+
+// The wave's LDS reads so far are done: copies over what they read may start.
+__device__ __forceinline__ void attn_wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// Sum over the workgroup's 256 threads, and the exclusive prefix; sh holds 8 ints.
+__device__ __forceinline__ int block_scan(int v, int* sh, int& total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int x = v;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int y = __shfl_up(x, d);
+    if (lane >= d) x += y;
+  }
+  __syncthreads();
+  if (lane == 63) sh[wave] = x;
+  __syncthreads();
+  int before = 0, sum = 0;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const int s = sh[w];
+    before += w < wave ? s : 0;
+    sum += s;
+  }
+  total = sum;
+  return before + x - v;
+}
+
+// A split item: the workgroup that began it writes where its row and pieces are.
+struct AttnRecord {
+  int32_t pieces;  // 0: nothing to join
+  int32_t q0;      // first query token of the sequence
+  int32_t row0;    // first row of the item among the sequence's nq * g rows
+  int32_t rows;    // rows of the item
+  int32_t head;    // kv head
+  int32_t pad_[3];
+};
+// Range of units [u0, u1) of workgroup w of nw over W units, and the last workgroup that holds a
+// unit below `end` (nw <= W: none is empty).
+__device__ __forceinline__ int attn_cut(int w, int nw, int W) { return (int)((int64_t)w * W / nw); }
+__device__ __forceinline__ int attn_last(int end, int nw, int W) { return (int)(((int64_t)end * nw - 1) / W); }
+
+// Stores 4 neighbouring output values of a row.
+template <typename T> __device__ __forceinline__ void store4(T t, void* p, float a, float b, float c, float d) {
+  *(u32x2_t*)p = u32x2_t{pack2(t, a, b), pack2(t, c, d)};
+}
+
+}  // namespace ql

@@ -1,0 +1,519 @@
+// Paged attention, many rows: tiles of 128 query rows of one sequence and kv head (the query heads
+// that share it are folded into the rows: row r is token r / g, head r % g of the group).
+//
+// The matrix cores bound it: 4 D flops per row and key against D / 32 bytes of cache (a tile of 64
+// keys is read once for 128 rows).  4 waves hold 32 rows each: S^T = K Q^T and O^T = V^T P^T by
+// 32x32x16 products; K and V tiles of 64 keys are copied into LDS by all waves, two stages deep,
+// so that one barrier per tile covers both the arrival of a stage and the end of its last reads.
+//
+// Work split.  With many items (sequence, kv head, row tile), one workgroup each, the longest
+// first, kv heads fastest so that a head's tiles run on one XCD and share its L2.  With few, all
+// items are laid end to end in units of one row tile x 64 keys and cut into equal runs, one per
+// resident workgroup; cut items leave pieces for the joining kernel.
+#include <algorithm>
+
+#include "attn_common.hpp"
+
+namespace ql {
+namespace {
+
+constexpr int BM = kAttnTileRows, BN = kAttnTileKeys;
+
+// V^T fragment of 32 values (tile dt) x 16 keys (step ks): two transposing reads of 4 keys each.
+template <int D> __device__ __forceinline__ u32x4_t v_frag(const uint8_t* sv, int lane, int dt, int ks) {
+  const int h = lane >> 5, l = lane & 15;
+  const int row = 16 * ks + 4 * h + (l >> 2);
+  const int c = 4 * dt + 2 * ((lane >> 4) & 1) + ((l & 3) >> 1);
+  const uint8_t* at = sv + row * (D * 2) + 8 * (l & 1);
+  const s16x4_t v0 = read_tr(at + (c ^ swz_v<D>(row)) * 16);
+  const s16x4_t v1 = read_tr(at + 8 * D * 2 + (c ^ swz_v<D>(row + 8)) * 16);
+  const u32x2_t w0 = __builtin_bit_cast(u32x2_t, v0), w1 = __builtin_bit_cast(u32x2_t, v1);
+  return u32x4_t{w0[0], w0[1], w1[0], w1[1]};
+}
+
+// Adds the non-finite values of a V tile to the wave's columns whose P is not zero.
+template <typename T, int D>
+__device__ __forceinline__ void tile_nonfinite(const uint8_t* sv, int lane, const u32x4_t* p, f32x16_t* o) {
+  asm volatile("" : "+v"(lane));  // the addresses stay in this rare path
+  const int h = lane >> 5, col = lane & 31;
+#pragma unroll 1
+  for (int j = 0; j < BN; ++j) {
+    // P of key j: of its 16 keys (step j / 16), key 8 x + 4 h + y is value 4 x + y of half h, in
+    // word 2 x + y / 2
+    uint32_t w = 0;
+#pragma unroll
+    for (int x = 0; x < 16; ++x) w = x == 4 * (j >> 4) + 2 * ((j >> 3) & 1) + ((j >> 1) & 1) ? p[x >> 2][x & 3] : w;
+    w = __shfl(w, 32 * ((j >> 2) & 1) + col);
+    const bool on = ((j & 1) ? w >> 16 : w) & 0x7fffu;
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const u32x2_t v = *(const u32x2_t*)(sv + j * (D * 2) + ((4 * d + y) ^ swz_v<D>(j)) * 16 + 8 * h);
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+          float x0, x1;
+          only_nonfinite<T>(v[z], on, x0, x1);
+          o[d][4 * y + 2 * z] += x0;
+          o[d][4 * y + 2 * z + 1] += x1;
+        }
+      }
+  }
+}
+
+// Units of row tile j of a sequence: its span's tiles of BN keys.
+__device__ __forceinline__ int tile_cost(const AttnArgs& a, const AttnSeq& q, int j, int& lo, int& hi, int& first) {
+  const int i0 = (int)a.g_div.div((uint32_t)(j * BM));
+  const int i1 = min(q.nq - 1, (int)a.g_div.div((uint32_t)(j * BM + BM - 1)));
+  attn_span(a, q, i0, i1, lo, hi);
+  return attn_tiles<BN>(lo, hi, first);
+}
+__device__ __forceinline__ int row_tiles(const AttnArgs& a, int s) {
+  if (s >= a.n_seqs) return 0;
+  const AttnSeq q = attn_seq(a, s);
+  return q.nq < 1 || attn_is_few(a, q.nq) ? 0 : (q.nq * a.g + BM - 1) / BM;
+}
+
+template <typename T, int D, bool RUNS>
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(const AttnArgs a) {
+  constexpr int ROW = D * 2;
+  constexpr int KB = BN * ROW;  // bytes of a K (or V) stage
+  constexpr int NS = D / 16;    // k-steps of the scores
+  constexpr int ND = D / 32;    // output tiles of 32 values
+  extern __shared__ __attribute__((aligned(1024))) uint8_t sm[];  // K stages, V stages, then (RUNS) the plan
+  __shared__ int ssh[8];
+  __shared__ int sfound[4];
+  __shared__ uint16_t sseen[2][4];  // per stage and wave: which of its 16 keys are loaded
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int h = lane >> 5, col = lane & 31;
+
+  int u0, u1, W, nw, w;
+  int* plan = (int*)(sm + 4 * KB);  // RUNS: first unit (of one head) of each row tile, then the sequences' first tiles
+  int nt_all = 0;
+  int* seq_first = nullptr;
+  AttnRecord* rec = nullptr;
+  if constexpr (RUNS) {
+    // first tile of each sequence, then first unit of each tile
+    seq_first = plan + a.plan_tiles + 1;
+    for (int s0 = 0; s0 < a.n_seqs; s0 += 256) {
+      int total;
+      const int e = block_scan(row_tiles(a, s0 + tid), ssh, total);
+      if (s0 + tid < a.n_seqs) seq_first[s0 + tid] = nt_all + e;
+      nt_all += total;
+    }
+    nt_all = min(nt_all, a.plan_tiles);  // overlapping sequences could ask for more than t rows hold
+    __syncthreads();
+    int units = 0;
+    for (int t0 = 0; t0 < nt_all; t0 += 256) {
+      const int ti = t0 + tid;
+      int c = 0;
+      if (ti < nt_all) {
+        int b = 0, e = a.n_seqs;  // the last sequence with seq_first <= ti
+        while (e - b > 1) {
+          const int m = (b + e) / 2;
+          if (seq_first[m] <= ti) b = m; else e = m;
+        }
+        int lo, hi, first;
+        c = tile_cost(a, attn_seq(a, b), ti - seq_first[b], lo, hi, first);
+      }
+      int total;
+      const int e = block_scan(c, ssh, total);
+      if (ti < nt_all) plan[ti] = units + e;
+      units += total;
+    }
+    if (tid == 0) plan[nt_all] = units;
+    __syncthreads();
+    W = units * a.hk;
+    nw = min(a.nw_tile, W);
+    // workgroups of one XCD (every 8th) take neighbouring runs
+    const int per = a.nw_tile / 8;
+    w = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    rec = a.rec + a.nw_few + w;
+    if (w >= nw) {
+      if (tid == 0) rec->pieces = 0;
+      return;
+    }
+    u0 = attn_cut(w, nw, W);
+    u1 = attn_cut(w + 1, nw, W);
+  } else {
+    w = 0, nw = 1, W = 0;
+    u0 = blockIdx.x;
+    u1 = u0 + 1;
+  }
+
+  bool recorded = false;
+  for (int u = u0; u < u1;) {
+    int s, j, head, ta, tb, nt, item0 = 0, lo, hi, first;
+    AttnSeq q;
+    if constexpr (RUNS) {
+      const int units = plan[nt_all];
+      head = u / units;
+      const int uh = u - head * units;
+      int b = 0, e = nt_all;
+      while (e - b > 1) {
+        const int m = (b + e) / 2;
+        if (plan[m] <= uh) b = m; else e = m;
+      }
+      const int ti = b;
+      nt = plan[ti + 1] - plan[ti];
+      ta = uh - plan[ti];
+      item0 = head * units + plan[ti];
+      b = 0, e = a.n_seqs;
+      while (e - b > 1) {
+        const int m = (b + e) / 2;
+        if (seq_first[m] <= ti) b = m; else e = m;
+      }
+      s = __builtin_amdgcn_readfirstlane(b);
+      j = __builtin_amdgcn_readfirstlane(ti - seq_first[b]);
+      head = __builtin_amdgcn_readfirstlane(head);
+      q = attn_seq(a, s);
+      tile_cost(a, q, j, lo, hi, first);
+      tb = min(nt, u1 - item0);
+      u = item0 + tb;
+    } else {
+      head = u % a.hk;
+      const int target = u / a.hk;
+      int before = 0;
+      if (tid == 0) sfound[0] = -1;
+      for (int s0 = 0; s0 < a.n_seqs; s0 += 256) {
+        int total;
+        const int c = row_tiles(a, s0 + tid);
+        const int e = before + block_scan(c, ssh, total);
+        if (e <= target && target < e + c) sfound[0] = s0 + tid, sfound[1] = c - 1 - (target - e);  // longest first
+        before += total;
+        if (before > target) break;
+      }
+      __syncthreads();
+      s = sfound[0], j = sfound[1];
+      if (s < 0) return;  // more workgroups than row tiles
+      q = attn_seq(a, s);
+      nt = tile_cost(a, q, j, lo, hi, first);
+      ta = 0, tb = nt;
+      u = u1;
+    }
+    const int rows = min(BM, q.nq * a.g - j * BM);
+
+    // The wave's 32 rows, one per column.
+    const int r = j * BM + 32 * wave + col;
+    const bool in = r < q.nq * a.g;
+    const int i = in ? (int)a.g_div.div((uint32_t)r) : q.nq - 1;
+    const int hq = head * a.g + (in ? r - i * a.g : 0);
+    const int qpos = q.kv - q.nq + i;
+    u32x4_t qf[NS];
+    {
+      const uint8_t* qp = a.q + ((int64_t)(q.q0 + i) * a.q_ts + (int64_t)hq * a.q_hs);
+#pragma unroll
+      for (int st = 0; st < NS; ++st) {
+        const u32x4_t z = {0, 0, 0, 0};
+        qf[st] = in ? *(const u32x4_t*)(qp + (2 * st + h) * 16) : z;
+      }
+    }
+    // first and last position among the wave's rows
+    const int pos_lo = q.kv - q.nq + min(q.nq - 1, (int)a.g_div.div((uint32_t)(j * BM + 32 * wave)));
+    const int pos_hi = q.kv - q.nq + min(q.nq - 1, (int)a.g_div.div((uint32_t)(j * BM + 32 * wave + 31)));
+
+    // and among the workgroup's
+    const int wg_lo = q.kv - q.nq + (int)a.g_div.div((uint32_t)(j * BM));
+    const int wg_hi = q.kv - q.nq + min(q.nq - 1, (int)a.g_div.div((uint32_t)(j * BM + BM - 1)));
+
+    f32x16_t o[ND];
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+      for (int x = 0; x < 16; ++x) o[d][x] = 0.f;
+    float m = kNegInf, l = 0.f;
+
+    const uint8_t* kb = a.k + (int64_t)head * a.head_stride;
+    const uint8_t* vb = a.v + (int64_t)head * a.head_stride;
+    const int32_t* table = a.table + (int64_t)s * a.table_stride;
+    RowLookup<16> look;
+    auto stage_in = [&](int st) {  // copies this wave's 16 rows of the looked-up tile into a stage
+      const int64_t off = look.offset(a);
+      const uint32_t seen = (uint32_t)__ballot(off >= 0) & 0xffffu;
+      if (lane == 0) sseen[st][wave] = (uint16_t)seen;
+      // rows 16 wave .. of the tile: the swizzles repeat every 16 rows
+      copy_rows<D, 16, false>(kb, off, sm + st * KB + wave * 16 * ROW, lane);
+      copy_rows<D, 16, true>(vb, off, sm + 2 * KB + st * KB + wave * 16 * ROW, lane);
+    };
+    __syncthreads();  // the last item's reads of the stages are done
+    look.load(a, table, (first + ta) * BN + 16 * wave, lo, hi, lane);
+    stage_in(0);
+    look.load(a, table, (first + ta + 1) * BN + 16 * wave, lo, ta + 1 < tb ? hi : 0, lane);
+
+    for (int t = ta; t < tb; ++t) {
+      const int st = (t - ta) & 1;
+      const int k0 = (first + t) * BN;
+      attn_wait_vm<0>();
+      __syncthreads();  // every wave's rows of stage st are there, and its reads of the other are done
+      if (t + 1 < tb) {
+        stage_in(st ^ 1);
+        look.load(a, table, k0 + 2 * BN + 16 * wave, lo, t + 2 < tb ? hi : 0, lane);
+      }
+      // a key that only some rows of the workgroup see may hold an infinity or a NaN
+      bool odd = false;
+      if (k0 + BN - 1 > wg_lo || (a.window > 0 && k0 <= wg_hi - a.window)) {
+        uint32_t acc = 0;
+#pragma unroll
+        for (int x = 0; x < KB / 4096; ++x) {
+          const u32x4_t v = *(const u32x4_t*)(sm + 2 * KB + st * KB + x * 4096 + tid * 16);
+          for (int y = 0; y < 4; ++y) acc |= nonfinite2<T>(v[y]);
+        }
+        odd = __syncthreads_or((acc & 0x80008000u) != 0);
+      }
+      // no row of the wave sees the tile
+      if (!odd && (k0 > pos_hi || (a.window > 0 && k0 + BN - 1 <= pos_lo - a.window))) continue;
+      const uint8_t* sk = sm + st * KB;
+      uint8_t* sv = sm + 2 * KB + st * KB;
+      f32x16_t sc[2];
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) {
+        const int row = 32 * kt + col;
+#pragma unroll
+        for (int x = 0; x < 16; ++x) sc[kt][x] = 0.f;
+#pragma unroll
+        for (int s2 = 0; s2 < NS; ++s2) {
+          const u32x4_t kf = *(const u32x4_t*)(sk + row * ROW + ((2 * s2 + h) ^ swz_k<D>(row)) * 16);
+          sc[kt] = mfma32(T{}, kf, qf[s2], sc[kt]);
+        }
+      }
+      const uint64_t seen = *(const uint64_t*)sseen[st];
+      const bool cut = k0 + BN - 1 > pos_lo || (a.window > 0 && k0 <= pos_hi - a.window);
+      if (cut || seen != ~(uint64_t)0) {
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            const int jj = 32 * kt + 8 * (x >> 2) + 4 * h + (x & 3);
+            const bool see = ((seen >> jj) & 1) && k0 + jj <= qpos && (a.window <= 0 || k0 + jj > qpos - a.window);
+            sc[kt][x] = see ? sc[kt][x] : kNegInf;
+          }
+      }
+      float mx = sc[0][0];
+#pragma unroll
+      for (int x = 1; x < 32; ++x) mx = fmaxf(mx, sc[x >> 4][x & 15]);
+      mx = join32(mx, MaxF()) * a.sl;
+      if (__any(mx > m + kLazy)) {
+        const float mn = fmaxf(m, mx);
+        const float f = m == kNegInf ? 0.f : exp2_fast(m - mn);
+        m = mn;
+        l *= f;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+          for (int x = 0; x < 16; ++x) o[d][x] *= f;
+      }
+      const float mr = m == kNegInf ? 0.f : m;
+      u32x4_t p[4];
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks) {
+        float e[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          e[x] = exp2_fast(__builtin_fmaf(sc[ks >> 1][8 * (ks & 1) + x], a.sl, -mr));
+          l += e[x];
+        }
+        // P rounds once to the cache's type for its product; l sums the unrounded values
+        p[ks] = u32x4_t{pack2(T{}, e[0], e[1]), pack2(T{}, e[2], e[3]), pack2(T{}, e[4], e[5]), pack2(T{}, e[6], e[7])};
+      }
+      if (odd) {
+        tile_nonfinite<T, D>(sv, lane, p, o);
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < KB / 4096; ++x) {
+          u32x4_t* at = (u32x4_t*)(sv + x * 4096 + tid * 16);
+          u32x4_t v = *at;
+          for (int y = 0; y < 4; ++y) v[y] = finite2<T>(v[y]);
+          *at = v;
+        }
+        __syncthreads();
+      }
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+        for (int d = 0; d < ND; ++d) o[d] = mfma32(T{}, v_frag<D>(sv, lane, d, ks), p[ks], o[d]);
+    }
+    l = join32(l, SumF());
+
+    // The lane holds its row's values 32 d + 8 y + 4 h .. + 3.
+    if (!RUNS || (ta == 0 && tb == nt)) {
+      if (in) {
+        float fo = 1.f, lr = l;
+        if (a.sinks) {
+          const float s2 = a.sinks[hq] * kLog2e, mn = fmaxf(m, s2);
+          fo = m == kNegInf ? 0.f : exp2_fast(m - mn);
+          lr = l * fo + exp2_fast(s2 - mn);
+        }
+        const float inv = lr == 0.f ? 0.f : fo / lr;
+        uint8_t* op = a.out + ((int64_t)(q.q0 + i) * a.out_ts + (int64_t)hq * a.out_hs) + 8 * h;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            store4(T{}, op + 64 * d + 16 * y, o[d][4 * y] * inv, o[d][4 * y + 1] * inv, o[d][4 * y + 2] * inv,
+                   o[d][4 * y + 3] * inv);
+      }
+    } else {
+      float* part = a.part_tile + (int64_t)(ta == 0 ? 2 * w + 1 : 2 * w) * (BM * (D + 2));
+      const int row = 32 * wave + col;
+      if (row < rows) {
+        if (h == 0) part[row] = m, part[BM + row] = l;
+        float* po = part + 2 * BM + row * D + 4 * h;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            *(f32x4_t*)(po + 32 * d + 8 * y) = f32x4_t{o[d][4 * y], o[d][4 * y + 1], o[d][4 * y + 2], o[d][4 * y + 3]};
+      }
+      if (ta == 0) {
+        recorded = true;
+        if (tid == 0) {
+          AttnRecord rr = {};
+          rr.pieces = attn_last(item0 + nt, nw, W) - w + 1;
+          rr.q0 = q.q0;
+          rr.row0 = j * BM;
+          rr.rows = rows;
+          rr.head = head;
+          *rec = rr;
+        }
+      }
+    }
+  }
+  if constexpr (RUNS) {
+    if (!recorded && tid == 0) rec->pieces = 0;
+  }
+}
+
+// Joins the pieces of the items that were cut: block (x, y) takes rows 16 y .. of record x.
+template <typename T, int D>
+__global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a, int first_rec, const float* part,
+                                                        int slot_floats, int rows_cap) {
+  constexpr int TPR = D / 4;        // threads of a row
+  constexpr int RPB = 256 / TPR;    // rows at once
+  const AttnRecord r = a.rec[first_rec + blockIdx.x];
+  if (r.pieces == 0) return;
+  const int c = threadIdx.x % TPR;
+  const int w = blockIdx.x;
+  for (int row = blockIdx.y * 16 + threadIdx.x / TPR; row < min(r.rows, (int)blockIdx.y * 16 + 16); row += RPB) {
+    auto slot = [&](int p) { return part + (int64_t)(p == 0 ? 2 * w + 1 : 2 * (w + p)) * slot_floats; };
+    float mt = kNegInf;
+#pragma unroll 4
+    for (int p = 0; p < r.pieces; ++p) mt = fmaxf(mt, slot(p)[row]);
+    float l = 0.f;
+    f32x4_t x = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int p = 0; p < r.pieces; ++p) {
+      const float* sp = slot(p);
+      const float lp = sp[rows_cap + row];
+      const float f = join_factor(sp[row], lp, mt);
+      const f32x4_t v = *(const f32x4_t*)(sp + 2 * rows_cap + row * D + 4 * c);
+      if (f != 0.f) {
+        l += lp * f;
+        x += v * f;
+      }
+    }
+    const int rr = r.row0 + row;
+    const int tok = (int)a.g_div.div((uint32_t)rr);
+    const int hq = r.head * a.g + rr - tok * a.g;
+    float fo = 1.f;
+    if (a.sinks) {
+      const float s2 = a.sinks[hq] * kLog2e, mn = fmaxf(mt, s2);
+      fo = mt == kNegInf ? 0.f : exp2_fast(mt - mn);
+      l = l * fo + exp2_fast(s2 - mn);
+    }
+    const float inv = l == 0.f ? 0.f : fo / l;
+    uint8_t* op = a.out + ((int64_t)(r.q0 + tok) * a.out_ts + (int64_t)hq * a.out_hs) + c * 8;
+    store4(T{}, op, x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+  }
+}
+
+template <typename T, int D> hipError_t tile(const AttnArgs& a, hipStream_t s) {
+  const size_t lds = (size_t)4 * BN * D * 2;
+  if (a.nw_tile > 0) {
+    const size_t plan = ((size_t)a.plan_tiles + 1 + a.n_seqs) * 4;
+    attn_tile_kernel<T, D, true><<<a.nw_tile, 256, lds + plan, s>>>(a);
+  } else {
+    attn_tile_kernel<T, D, false><<<a.items_tile, 256, lds, s>>>(a);
+  }
+  return hipGetLastError();
+}
+template <typename T, int D> hipError_t join(const AttnArgs& a, hipStream_t s) {
+  if (a.join_few) {
+    attn_join_kernel<T, D><<<dim3(a.nw_few, a.cap_few / 16), 256, 0, s>>>(a, 0, a.part, a.part_floats, a.cap_few);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (a.nw_tile > 0 && a.join_tile) {
+    attn_join_kernel<T, D><<<dim3(a.nw_tile, BM / 16), 256, 0, s>>>(a, a.nw_few, a.part_tile, BM * (D + 2), BM);
+    return hipGetLastError();
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+AttnPlan attn_plan(int64_t t, int64_t n_seqs, int64_t hq, int64_t hk, int d, int64_t max_q, int64_t max_kv,
+                   int64_t window) {
+  AttnPlan p{};
+  const int64_t g = hq / hk;
+  const int64_t cap = d == 256 ? 16 : 32;  // rows whose registers fit
+  const int64_t limit = int64_t(1) << 31;
+  const int64_t span = window > 0 ? std::min(max_kv, window + max_q - 1) : max_kv;  // longest span of an item
+  auto nc_of = [](int64_t rows) { return rows <= 16 ? 1 : 2; };
+  if (max_q * g <= cap) {
+    p.nc = nc_of(max_q * g);
+  } else {
+    p.tile = true;
+    // tokens that fill every sequence to max_q leave none for the few-row kernel
+    if (g <= cap && t != n_seqs * max_q) p.nc = nc_of(g);
+  }
+  p.few_rows = 16 * p.nc;
+  p.ok = true;
+  size_t at = 0;
+  if (p.nc) {
+    const int64_t tiles = span / kAttnFewKeys + 2;
+    const int64_t units = n_seqs * hk * tiles;
+    p.ok = p.ok && units < limit;
+    // two resident workgroups a compute unit (their LDS), one at 256 values a head
+    p.nw_few = (int)std::min<int64_t>(d == 64 ? 1024 : d == 128 ? 512 : 256, units);
+    p.cap_few = 16 * p.nc;
+    p.part_floats = p.cap_few * (d + 2);
+    p.join_few = max_kv > kAttnFewKeys;  // a span inside one tile is never cut
+  }
+  if (p.tile) {
+    const int64_t slots = d == 256 ? 256 : 512;  // resident workgroups
+    const int64_t full = t * g / kAttnTileRows;
+    const int64_t seqs = std::min<int64_t>(n_seqs, t * g / (p.few_rows + 1));
+    const int64_t tiles = full + seqs;
+    p.plan_tiles = (int)tiles;
+    p.ok = p.ok && tiles * hk < limit;
+    if (full * hk >= 2 * slots || tiles + n_seqs > 4096) {
+      p.items_tile = (int)(tiles * hk);
+    } else {
+      p.ok = p.ok && tiles * hk * (span / kAttnTileKeys + 4) < limit;
+      p.nw_tile = (int)slots;
+      p.join_tile = max_kv > kAttnTileKeys;
+    }
+  }
+  auto take = [&](size_t n) {
+    const size_t o = at;
+    at = (at + n + 255) / 256 * 256;
+    return o;
+  };
+  take((size_t)(p.nw_few + p.nw_tile) * sizeof(AttnRecord));
+  p.part_off = take((size_t)2 * p.nw_few * p.part_floats * 4);
+  p.part_tile_off = take((size_t)2 * p.nw_tile * kAttnTileRows * (d + 2) * 4);
+  p.bytes = at;
+  return p;
+}
+
+hipError_t launch_attn_tile(const AttnArgs& a, int dt, int d, hipStream_t s) {
+  if (dt == DT_BF16) return d == 64 ? tile<BF16, 64>(a, s) : d == 128 ? tile<BF16, 128>(a, s) : tile<BF16, 256>(a, s);
+  return d == 64 ? tile<F16, 64>(a, s) : d == 128 ? tile<F16, 128>(a, s) : tile<F16, 256>(a, s);
+}
+hipError_t launch_attn_join(const AttnArgs& a, int dt, int d, hipStream_t s) {
+  if (dt == DT_BF16) return d == 64 ? join<BF16, 64>(a, s) : d == 128 ? join<BF16, 128>(a, s) : join<BF16, 256>(a, s);
+  return d == 64 ? join<F16, 64>(a, s) : d == 128 ? join<F16, 128>(a, s) : join<F16, 256>(a, s);
+}
+
+}  // namespace ql

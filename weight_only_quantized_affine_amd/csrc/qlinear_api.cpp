@@ -80,6 +80,92 @@ ql_status check_product(const char* fn, const void* x, ql_dtype xdt, int64_t m, 
 }
 
 int dt(ql_dtype d) { return (int)d; }
+constexpr int64_t kAttnLimit = int64_t(1) << 30;  // rows of a group, positions of a sequence
+
+bool stride8(int64_t s) { return s >= 0 && s % 8 == 0 && s < (int64_t(1) << 40); }
+
+// A tensor of heads [t, heads, d] in 16 bits (present when it has heads).
+ql_status check_heads(const char* fn, const char* name, const ql_heads* h, bool required) {
+  CHECK(h != nullptr || !required, QL_ERR_NULL, "%s: %s must not be NULL", fn, name);
+  if (!h) return QL_OK;
+  CHECK(h->heads >= 0 && h->heads < (1 << 20), QL_ERR_SHAPE, "%s: %s has %lld heads", fn, name, (long long)h->heads);
+  if (h->heads == 0) return QL_OK;
+  CHECK(aligned(h->p, 16), QL_ERR_ALIGN, "%s: %s must be 16-byte aligned", fn, name);
+  CHECK(stride8(h->token_stride) && stride8(h->head_stride), QL_ERR_ALIGN,
+        "%s: strides of %s must be multiples of 8 elements", fn, name);
+  return QL_OK;
+}
+
+ql_status check_cache(const char* fn, const ql_paged_cache* c) {
+  CHECK(c != nullptr, QL_ERR_NULL, "%s: cache must not be NULL", fn);
+  CHECK(c->n_pages >= 0 && c->page_size >= 1 && c->hk >= 1 && c->hk < (1 << 20), QL_ERR_SHAPE,
+        "%s: the cache needs n_pages >= 0, page_size >= 1 and hk >= 1", fn);
+  CHECK(c->n_pages < (int64_t(1) << 31) && c->page_size < (int64_t(1) << 31) &&
+            c->n_pages * c->page_size < (int64_t(1) << 31),
+        QL_ERR_UNSUPPORTED, "%s: a cache of 2^31 slots or more", fn);
+  CHECK(c->n_pages == 0 || (c->k && c->v), QL_ERR_NULL, "%s: cache.k and cache.v must not be NULL", fn);
+  CHECK(aligned(c->k, 16) && aligned(c->v, 16), QL_ERR_ALIGN, "%s: cache.k and cache.v must be 16-byte aligned", fn);
+  CHECK(stride8(c->page_stride) && stride8(c->token_stride) && stride8(c->head_stride), QL_ERR_ALIGN,
+        "%s: the cache's strides must be multiples of 8 elements", fn);
+  return QL_OK;
+}
+
+// Checks of the norm and rotation, and their kernel arguments.
+ql_status norm_rope_args(const char* fn, const ql_norm_rope* nr, int64_t t, int64_t d, const ql_heads* q,
+                         const ql_heads* q_out, const ql_heads* k, ql::NormRopeArgs& a) {
+  CHECK(nr != nullptr, QL_ERR_NULL, "%s: nr must not be NULL", fn);
+  CHECK(t >= 0, QL_ERR_SHAPE, "%s: t=%lld must be >= 0", fn, (long long)t);
+  CHECK(d >= 8 && d <= 512 && d % 8 == 0, QL_ERR_UNSUPPORTED, "%s: d=%lld not supported (multiples of 8 up to 512)",
+        fn, (long long)d);
+  CHECK(is_out(nr->w_dtype) || (!nr->q_weight && !nr->k_weight), QL_ERR_DTYPE,
+        "%s: w_dtype must be QL_F32, QL_F16 or QL_BF16", fn);
+  CHECK(aligned(nr->q_weight, 16) && aligned(nr->k_weight, 16), QL_ERR_ALIGN,
+        "%s: q_weight and k_weight must be 16-byte aligned", fn);
+  CHECK(nr->eps >= 0.f && nr->eps <= 3.0e38f, QL_ERR_SHAPE, "%s: eps must be finite and >= 0", fn);
+  CHECK(nr->rot >= 0 && nr->rot <= d && nr->rot % 16 == 0, QL_ERR_SHAPE,
+        "%s: rot=%lld must be a multiple of 16 in [0, d]", fn, (long long)nr->rot);
+  if (nr->rot > 0) {
+    CHECK(nr->max_pos >= 1 && nr->max_pos < (int64_t(1) << 40), QL_ERR_SHAPE, "%s: max_pos must be >= 1", fn);
+    if (t > 0) CHECK(nr->positions && nr->cos_sin, QL_ERR_NULL, "%s: positions and cos_sin must not be NULL", fn);
+    CHECK(aligned(nr->positions, 8), QL_ERR_ALIGN, "%s: positions must be 8-byte aligned", fn);
+    CHECK(aligned(nr->cos_sin, 16), QL_ERR_ALIGN, "%s: cos_sin must be 16-byte aligned", fn);
+  }
+  ql_status st = check_heads(fn, "q", q, false);
+  if (st == QL_OK) st = check_heads(fn, "k", k, false);
+  if (st != QL_OK) return st;
+  if (q && q->heads > 0) {
+    st = check_heads(fn, "q_out", q_out, true);
+    if (st != QL_OK) return st;
+    CHECK(q_out->heads == q->heads, QL_ERR_SHAPE, "%s: q_out must have q's heads", fn);
+    CHECK(t == 0 || (q->p && q_out->p), QL_ERR_NULL, "%s: q and q_out must not be NULL", fn);
+    a.q = (const uint8_t*)q->p;
+    a.q_ts = 2 * q->token_stride;
+    a.q_hs = 2 * q->head_stride;
+    a.q_out = (uint8_t*)q_out->p;
+    a.qo_ts = 2 * q_out->token_stride;
+    a.qo_hs = 2 * q_out->head_stride;
+    a.hq = (int)q->heads;
+  }
+  if (k && k->heads > 0) {
+    CHECK(t == 0 || k->p, QL_ERR_NULL, "%s: k must not be NULL", fn);
+    a.k = (const uint8_t*)k->p;
+    a.k_ts = 2 * k->token_stride;
+    a.k_hs = 2 * k->head_stride;
+    a.hk = (int)k->heads;
+  }
+  a.t = t;
+  a.d = (int)d;
+  a.rot = (int)nr->rot;
+  a.interleaved = nr->interleaved ? 1 : 0;
+  a.q_weight = nr->q_weight;
+  a.k_weight = nr->k_weight;
+  a.wdt = dt(nr->w_dtype);
+  a.eps = nr->eps;
+  a.positions = nr->positions;
+  a.cos_sin = nr->cos_sin;
+  a.max_pos = nr->max_pos;
+  return QL_OK;
+}
 
 }  // namespace
 
@@ -702,6 +788,159 @@ ql_status qlinear_apply_experts(ql_format fmt, const void* w0, const void* w1, i
   return launched(ql::launch_apply_experts((int)fmt, w0, w1, e, n, k, ids, n_pos, x, dt(x_dtype), pos_per_row, y,
                                            dt(y_dtype), offsets, perm, order, xfac, s),
                   fn);
+}
+
+ql_status qlinear_qk_norm_rope(const ql_heads* q, const ql_heads* q_out, const ql_heads* k, const ql_heads* k_out,
+                               ql_dtype dtype, int64_t t, int64_t d, const ql_norm_rope* nr, void* stream) {
+  const char* fn = "qlinear_qk_norm_rope";
+  CHECK(is16(dtype), QL_ERR_DTYPE, "%s: dtype must be QL_F16 or QL_BF16", fn);
+  ql::NormRopeArgs a{};
+  ql_status st = norm_rope_args(fn, nr, t, d, q, q_out, k, a);
+  if (st != QL_OK) return st;
+  if (a.hk > 0) {
+    st = check_heads(fn, "k_out", k_out, true);
+    if (st != QL_OK) return st;
+    CHECK(k_out->heads == k->heads, QL_ERR_SHAPE, "%s: k_out must have k's heads", fn);
+    CHECK(t == 0 || k_out->p, QL_ERR_NULL, "%s: k_out must not be NULL", fn);
+    a.k_out = (uint8_t*)k_out->p;
+    a.ko_ts = 2 * k_out->token_stride;
+    a.ko_hs = 2 * k_out->head_stride;
+  }
+  if (t == 0 || a.hq + a.hk == 0) return ok();
+  CHECK(t < (int64_t(1) << 31) / (a.hq + a.hk + 4), QL_ERR_UNSUPPORTED, "%s: 2^31 rows or more", fn);
+  return launched(ql::launch_norm_rope(a, dt(dtype), (hipStream_t)stream), fn);
+}
+
+ql_status qlinear_kv_append(const ql_heads* q, const ql_heads* q_out, const ql_heads* k, const ql_heads* v,
+                            const ql_paged_cache* cache, const int64_t* slots, ql_dtype dtype, int64_t t,
+                            const ql_norm_rope* nr, void* stream) {
+  const char* fn = "qlinear_kv_append";
+  CHECK(is16(dtype), QL_ERR_DTYPE, "%s: dtype must be QL_F16 or QL_BF16", fn);
+  ql_status st = check_cache(fn, cache);
+  if (st != QL_OK) return st;
+  CHECK(k && v, QL_ERR_NULL, "%s: k and v must not be NULL", fn);
+  ql::NormRopeArgs a{};
+  st = norm_rope_args(fn, nr, t, cache->d, q, q_out, k, a);
+  if (st == QL_OK) st = check_heads(fn, "v", v, true);
+  if (st != QL_OK) return st;
+  CHECK(k->heads == cache->hk && v->heads == cache->hk, QL_ERR_SHAPE, "%s: k and v must have the cache's %lld heads",
+        fn, (long long)cache->hk);
+  if (t == 0) return ok();
+  CHECK(v->p, QL_ERR_NULL, "%s: v must not be NULL", fn);
+  CHECK(slots, QL_ERR_NULL, "%s: slots must not be NULL", fn);
+  CHECK(aligned(slots, 8), QL_ERR_ALIGN, "%s: slots must be 8-byte aligned", fn);
+  CHECK(t < (int64_t(1) << 31) / (a.hq + 2 * a.hk + 4), QL_ERR_UNSUPPORTED, "%s: 2^31 rows or more", fn);
+  a.v = (const uint8_t*)v->p;
+  a.v_ts = 2 * v->token_stride;
+  a.v_hs = 2 * v->head_stride;
+  a.hv = (int)v->heads;
+  a.k_out = (uint8_t*)cache->k;
+  a.v_out = (uint8_t*)cache->v;
+  a.ko_ts = a.vo_ts = 2 * cache->token_stride;
+  a.ko_hs = a.vo_hs = 2 * cache->head_stride;
+  a.page_stride = 2 * cache->page_stride;
+  a.slots = slots;
+  a.n_slots = cache->n_pages * cache->page_size;
+  a.page_size = (int)cache->page_size;
+  a.page_div = ql::fast_div((uint32_t)cache->page_size);
+  return launched(ql::launch_norm_rope(a, dt(dtype), (hipStream_t)stream), fn);
+}
+
+size_t qlinear_paged_attention_workspace_size(int64_t t, int64_t n_seqs, int64_t hq, int64_t hk, int64_t d,
+                                              int64_t max_q, int64_t max_pages, int64_t page_size, int64_t window) {
+  if (t <= 0 || n_seqs <= 0 || hq <= 0 || hk <= 0 || hq >= (1 << 20) || hq % hk != 0 ||
+      (d != 64 && d != 128 && d != 256) || max_q <= 0 || max_pages < 0 || page_size <= 0 || window < 0 ||
+      t >= kAttnLimit / (hq / hk) || n_seqs >= kAttnLimit || max_pages >= kAttnLimit ||
+      page_size > INT32_MAX || max_pages * page_size >= kAttnLimit)
+    return 0;
+  return ql::attn_plan(t, n_seqs, hq, hk, (int)d, std::min(max_q, t), max_pages * page_size, window).bytes;
+}
+
+ql_status qlinear_paged_attention(const ql_heads* q, const ql_heads* out, ql_dtype dtype, int64_t t,
+                                  const ql_paged_cache* cache, const int32_t* block_table, int64_t table_stride,
+                                  int64_t max_pages, const int32_t* cu_q, const int32_t* kv_lens, int64_t n_seqs,
+                                  int64_t max_q, float scale, int64_t window, const float* sinks, void* workspace,
+                                  size_t ws_bytes, void* stream) {
+  const char* fn = "qlinear_paged_attention";
+  CHECK(is16(dtype), QL_ERR_DTYPE, "%s: dtype must be QL_F16 or QL_BF16", fn);
+  ql_status st = check_cache(fn, cache);
+  if (st != QL_OK) return st;
+  CHECK(cache->d == 64 || cache->d == 128 || cache->d == 256, QL_ERR_UNSUPPORTED,
+        "%s: d=%lld not supported (64, 128 or 256)", fn, (long long)cache->d);
+  st = check_heads(fn, "q", q, true);
+  if (st == QL_OK) st = check_heads(fn, "out", out, true);
+  if (st != QL_OK) return st;
+  CHECK(q->heads >= 1 && q->heads % cache->hk == 0 && out->heads == q->heads, QL_ERR_SHAPE,
+        "%s: q and out must have the same heads, a multiple of the cache's %lld", fn, (long long)cache->hk);
+  CHECK(t >= 0 && n_seqs >= 0 && max_q >= 0 && max_pages >= 0 && table_stride >= 0, QL_ERR_SHAPE,
+        "%s: t, n_seqs, max_q, max_pages and table_stride must be >= 0", fn);
+  CHECK(scale > 0.f && scale <= 3.0e38f, QL_ERR_SHAPE, "%s: scale must be finite and > 0", fn);
+  CHECK(window >= 0, QL_ERR_SHAPE, "%s: window=%lld must be >= 0", fn, (long long)window);
+  if (t == 0 || n_seqs == 0 || max_q == 0) return ok();
+  CHECK(q->p && out->p, QL_ERR_NULL, "%s: q and out must not be NULL", fn);
+  CHECK(cu_q && kv_lens, QL_ERR_NULL, "%s: cu_q and kv_lens must not be NULL", fn);
+  CHECK(block_table || max_pages == 0, QL_ERR_NULL, "%s: block_table must not be NULL", fn);
+  CHECK(aligned(cu_q, 4) && aligned(kv_lens, 4) && aligned(block_table, 4) && aligned(sinks, 4), QL_ERR_ALIGN,
+        "%s: cu_q, kv_lens, block_table and sinks must be 4-byte aligned", fn);
+  const int64_t g = q->heads / cache->hk;
+  CHECK(t < kAttnLimit / g && n_seqs < kAttnLimit && max_pages < kAttnLimit &&
+            max_pages * cache->page_size < kAttnLimit,
+        QL_ERR_UNSUPPORTED, "%s: t times the query heads of a kv head, n_seqs and the slots of a block-table row must "
+        "be below 2^30", fn);
+  max_q = std::min(max_q, t);
+  const int64_t max_kv = max_pages * cache->page_size;
+  const ql::AttnPlan p = ql::attn_plan(t, n_seqs, q->heads, cache->hk, (int)cache->d, max_q, max_kv, window);
+  CHECK(p.ok, QL_ERR_UNSUPPORTED, "%s: n_seqs, heads and max_pages give 2^31 units of work or more", fn);
+  CHECK(workspace != nullptr && ws_bytes >= p.bytes, QL_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", fn,
+        workspace ? ws_bytes : (size_t)0, p.bytes);
+  CHECK(aligned(workspace, 16), QL_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
+  ql::AttnArgs a{};
+  a.q = (const uint8_t*)q->p;
+  a.q_ts = 2 * q->token_stride;
+  a.q_hs = 2 * q->head_stride;
+  a.k = (const uint8_t*)cache->k;
+  a.v = (const uint8_t*)cache->v;
+  a.page_stride = 2 * cache->page_stride;
+  a.token_stride = 2 * cache->token_stride;
+  a.head_stride = 2 * cache->head_stride;
+  a.n_pages = (int)cache->n_pages;
+  a.page_size = (int)cache->page_size;
+  a.page_div = ql::fast_div((uint32_t)cache->page_size);
+  a.table = block_table;
+  a.table_stride = table_stride;
+  a.max_kv = (int)max_kv;
+  a.cu_q = cu_q;
+  a.kv_lens = kv_lens;
+  a.n_seqs = (int)n_seqs;
+  a.t = t;
+  a.max_q = (int)max_q;
+  a.hk = (int)cache->hk;
+  a.g = (int)g;
+  a.g_div = ql::fast_div((uint32_t)g);
+  a.sl = scale * 1.4426950408889634f;
+  a.window = window >= max_kv ? 0 : (int)window;  // a window over the whole cache hides nothing
+  a.sinks = sinks;
+  a.out = (uint8_t*)out->p;
+  a.out_ts = 2 * out->token_stride;
+  a.out_hs = 2 * out->head_stride;
+  a.few_rows = p.few_rows;
+  a.nw_few = p.nw_few;
+  a.cap_few = p.cap_few;
+  a.part_floats = p.part_floats;
+  a.join_few = p.join_few;
+  a.nw_tile = p.nw_tile;
+  a.items_tile = p.items_tile;
+  a.plan_tiles = p.plan_tiles;
+  a.join_tile = p.join_tile;
+  a.rec = (ql::AttnRecord*)workspace;
+  a.part = (float*)((uint8_t*)workspace + p.part_off);
+  a.part_tile = (float*)((uint8_t*)workspace + p.part_tile_off);
+  const hipStream_t s = (hipStream_t)stream;
+  hipError_t e = hipSuccess;
+  if (p.tile) e = ql::launch_attn_tile(a, dt(dtype), (int)cache->d, s);
+  if (e == hipSuccess && p.nc) e = ql::launch_attn_few(a, dt(dtype), (int)cache->d, p.nc, s);
+  if (e == hipSuccess) e = ql::launch_attn_join(a, dt(dtype), (int)cache->d, s);
+  return launched(e, fn);
 }
 
 }  // extern "C"
