@@ -2,7 +2,7 @@
 
 Tolerance of an output o = sum w_j v_j with A = sum w_j |v_j| (u = 2^-24, h = half a step of the
 16-bit type relative to the value):
-  h A           each weight rounds once for its product;   h |o|   the output rounds once
+  h (A + |o|)   each weight rounds once, in the product and in the sum;   h |o|   the output rounds once
   2 E A         E bounds the relative error of an unnormalised weight (numerator and sum): the
                 score's fp32 sum of d products, d u sum|q k| scale, its scaling and difference,
                 4 u (|s| + |max|), and the exponential, 2 u
@@ -75,7 +75,7 @@ def close(got, want, scale_d, dtype):
     h = torch.finfo(dtype).eps / 2
     qk, s, n, z = (info[..., i:i + 1] for i in range(4))
     e = scale_d * U * qk + 8 * U * s + 2 * U
-    tol = (h * a + h * np.abs(out) + 2 * e * a + 2 * (n + 8) * U * a) * (1 + 2.0 ** -6)
+    tol = (h * a + 2 * h * np.abs(out) + 2 * e * a + 2 * (n + 8) * U * a) * (1 + 2.0 ** -6)
     tol += torch.finfo(dtype).smallest_normal * torch.finfo(dtype).eps / 2
     if dtype == HF:
         tol += 2.0 ** -25 * n * 6.0 / np.maximum(1.0, z * 2.0 ** -8)  # |v| < 6

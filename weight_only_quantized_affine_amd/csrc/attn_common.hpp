@@ -3,7 +3,8 @@
 //
 // Mathematics.  For one query row with scores s_j (log2 units: scale * log2(e) * q.k_j) the kernels
 // hold M (a reference not below the maximum by more than 2^kLazy), l = sum 2^(s_j - M) and
-// O = sum 2^(s_j - M) v_j in fp32; pieces of a row join as
+// O = sum 2^(s_j - M) v_j in fp32, the weights 2^(s_j - M) rounded once to the cache's 16-bit type
+// (the matrix cores' operand) in the sum l as in O, so that the normalized weights sum to one; pieces of a row join as
 // sum_p 2^(M_p - M) O_p / sum_p 2^(M_p - M) l_p.  Both products run transposed, S^T = K Q^T and
 // O^T = V^T P^T, so that a lane holds one query column: the maximum, the sum and the rescaling of
 // a row are per-lane scalars, and the lane's scores are already the P^T operand of the second
@@ -49,6 +50,9 @@ __device__ __forceinline__ uint32_t pack2(BF16, float a, float b) {
 __device__ __forceinline__ uint32_t pack2(F16, float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, f16x2_t));
 }
+// acc plus the two 16-bit values of a word.
+__device__ __forceinline__ float add2(BF16, uint32_t w, float acc) { return dot2(BF16{}, w, 0x3f803f80u, acc); }
+__device__ __forceinline__ float add2(F16, uint32_t w, float acc) { return dot2(F16{}, w, 0x3c003c00u, acc); }
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // x joined with its value in the other half (lanes +-32) or the other 16 of each 32 lanes.
@@ -61,6 +65,12 @@ template <typename F> __device__ __forceinline__ float join16(float x, F f) {
   const uint32_t u = __float_as_uint(x);
   const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
   return f(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+// The larger of three, ignoring NaN (fmaxf would first quiet each operand).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
 }
 struct MaxF {
   __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
@@ -140,55 +150,159 @@ template <int N> __device__ __forceinline__ int attn_tiles(int lo, int hi, int& 
   return max(1, (hi + N - 1) / N - first);
 }
 
-// Cache rows of one tile that this wave copies: ROWS rows, row r of the tile looked up by the
-// lanes with lane % ROWS == r.
-template <int ROWS> struct RowLookup {
-  int pos, id;  // the lane's position and its page id
-  __device__ __forceinline__ void load(const AttnArgs& a, const int32_t* table, int base, int lo, int hi, int lane) {
-    pos = base + (lane & (ROWS - 1));
-    id = -1;
-    if (pos >= lo && pos < hi) id = table[a.page_div.div((uint32_t)pos)];
-  }
-  // Byte offset of the row from the head's start, or -1 for a row outside the span or in a page
-  // that the cache does not have.
-  __device__ __forceinline__ int64_t offset(const AttnArgs& a) const {
-    if (id < 0 || id >= a.n_pages) return -1;
-    const uint32_t p = (uint32_t)pos - a.page_div.div((uint32_t)pos) * (uint32_t)a.page_size;
-    return (int64_t)id * a.page_stride + (int64_t)p * a.token_stride;
-  }
-};
-
 // Rows that are not to be seen are copied from here: their V must be zero, since zero times an
 // infinity or a NaN left in an unused slot would not be.
 __device__ __attribute__((aligned(16))) static uint32_t kZeroRow[128] = {};
 
-// Starts a copy of 16 bytes a lane into LDS, lane l's to dst + 16 l (dst is uniform).  Written as
-// an instruction because the compiler, which cannot tell the stages apart, would wait for every
-// copy in flight at each LDS read; the kernels wait by count (attn_wait_vm) for the stage they
-// read.  The copy writes no register; the wait state between m0 and its use is in the text.
+// Starts a copy of 16 bytes a lane into LDS, lane l's from src to dst + 16 l (dst is uniform).
+// Written as an instruction because the compiler,
+// which cannot tell the stages apart, would wait for every copy in flight at each LDS read; the
+// kernels wait by count (attn_wait_vm) for the stage they read.  The copy writes no register; the
+// wait state between m0 and its use is in the text.
+__device__ __forceinline__ uint32_t lds_at(const uint8_t* p) {
+  return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(at_lds_void*)p);
+}
 __device__ __forceinline__ void copy16(const uint8_t* src, uint8_t* dst) {
-  const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(at_lds_void*)dst);
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(at), "v"(src) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :
+               : "s"(lds_at(dst)), "v"(src)
+               : "memory", "m0");
+}
+__device__ __forceinline__ int64_t uniform64(int64_t x) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x), hi = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
+// The same from a uniform base plus the lane's offset.  (A scalar written by a vector instruction
+// needs 5 wait states before a load takes it.)
+__device__ __forceinline__ void copy16(int64_t base, uint32_t off, uint8_t* dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2"
+               :
+               : "s"(lds_at(dst)), "v"(off), "s"(base)
+               : "memory", "m0");
+}
+// Two of them, 1 KB apart in LDS.
+__device__ __forceinline__ void copy16_pair(int64_t base, uint32_t off0, uint32_t off1, uint8_t* dst) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %3\n\t"
+      "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3"
+      :
+      : "s"(lds_at(dst)), "v"(off0), "v"(off1), "s"(base)
+      : "memory", "m0", "scc");
 }
 
-// Copies ROWS rows of D values into LDS at dst (rows back to back, chunks placed by swz), 1 KB per
-// instruction.  off holds the row offsets in the lanes as RowLookup gives them; row0 is the tile
-// row of the first (a multiple of 16).
-template <int D, int ROWS, bool IS_V>
-__device__ __forceinline__ void copy_rows(const uint8_t* base, int64_t off, uint8_t* dst, int lane) {
-  constexpr int CH = D / 8;         // 16-byte chunks of a row
-  constexpr int RPI = 64 / CH;      // rows of an instruction
-  const int rl = lane / CH, c = lane % CH;
+// The cache rows of a tile that one wave copies, U runs of R rows (positions base .. base + U R; R
+// divides 16 and base is a multiple of R), K and V alike; tiles are STEP positions apart.
+//
+// Where pages are multiples of 16 slots (a.page16) a run lies in one page: the ids of the next 64 / U
+// tiles are read at once, one per lane, and the copies take a scalar base and lane offsets that
+// never change.  (One scalar load per tile instead shares its counter with the LDS reads: every
+// read after it waits for it.)  Else, and for runs that end inside, row r is looked up by the lanes
+// with lane % (U R) == r, and handed to the lanes that copy it.
+template <int D, int R, int U, int STEP> struct TileCopy {
+  static constexpr int CH = D / 8;      // 16-byte chunks of a row
+  static constexpr int RPI = 64 / CH;   // rows of an instruction (1 KB)
+  static constexpr int NI = R / RPI;    // instructions of a run
+  static constexpr int ROWS = U * R, BLOCK = 64 / U;
+  struct Place {       // where a tile's rows lie
+    int64_t row;       // the lane's row, -1 for a row that is not to be seen
+    int64_t at[U];     // uniform: the runs, -1: by rows
+  };
+  uint32_t off_k[NI], off_v[NI];  // lane offsets within a run
+  int pos, id;                    // the lane's row: position, page (a.page16: unused)
+  int ids, block;                 // a.page16: pages of the runs of BLOCK tiles, position of the first
+  int base, uid[U];               // uniform: first position, pages of the runs
+  Place now;
+  uint32_t seen;                  // bit r: row r is to be seen
+
+  // row0: place of the first row in the tile, whose swizzle the chunks follow.
+  __device__ __forceinline__ void init(const AttnArgs& a, int row0, int lane) {
 #pragma unroll
-  for (int i = 0; i < ROWS / RPI; ++i) {
-    const int r = i * RPI + rl;
-    const int lo = __shfl((int)off, r), hi = __shfl((int)(off >> 32), r);
-    const int64_t o = ((int64_t)hi << 32) | (uint32_t)lo;
-    const int cs = c ^ (IS_V ? swz_v<D>(r) : swz_k<D>(r));
-    const uint8_t* src = (hi < 0 ? (const uint8_t*)kZeroRow : base + o) + cs * 16;
-    copy16(src, dst + i * 1024);
+    for (int i = 0; i < NI; ++i) {
+      const int r = i * RPI + lane / CH, c = lane % CH;
+      off_k[i] = (uint32_t)r * (uint32_t)a.token_stride + (c ^ swz_k<D>(row0 + r)) * 16;
+      off_v[i] = (uint32_t)r * (uint32_t)a.token_stride + (c ^ swz_v<D>(row0 + r)) * 16;
+    }
   }
-}
+  // Reads the page ids of the rows of the tile at `first` that lie in [lo, hi); `begins` at the
+  // first of a sequence's tiles.
+  __device__ __forceinline__ void lookup(const AttnArgs& a, const int32_t* table, int first, int lo, int hi, int lane,
+                                         bool begins) {
+    base = first;
+    pos = first + (lane & (ROWS - 1));
+    if (a.page16) {
+      if (begins || first - block >= BLOCK * STEP) {
+        block = first;
+        const int p = first + (lane % BLOCK) * STEP + (lane / BLOCK) * R;
+        ids = -1;
+        if (p + R > lo && p < hi) ids = table[a.page_div.div((uint32_t)p)];
+        asm volatile("" : "+v"(ids));  // the wait for the load is here
+      }
+      const int i = (first - block) / STEP;
+#pragma unroll
+      for (int u = 0; u < U; ++u) uid[u] = __builtin_amdgcn_readlane(ids, i + u * BLOCK);
+    } else {
+      id = -1;
+      if (pos >= lo && pos < hi) id = table[a.page_div.div((uint32_t)pos)];
+    }
+  }
+  // Turns the page ids into places; sets seen.
+  __device__ __forceinline__ void resolve(const AttnArgs& a, int lo, int hi, int lane) {
+    constexpr uint32_t kRun = (uint32_t)((1ull << R) - 1), kAll = (uint32_t)((1ull << ROWS) - 1);
+    bool by_rows = true;
+    if (a.page16) {
+      by_rows = false;
+      seen = kAll;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int p = base + R * u;
+        const bool known = (uint32_t)uid[u] < (uint32_t)a.n_pages;
+        now.at[u] = known ? (int64_t)uid[u] * a.page_stride +
+                                (int64_t)(p - (int)a.page_div.div((uint32_t)p) * a.page_size) * a.token_stride
+                          : -1;
+        by_rows |= !(known && p >= lo && p + R <= hi);
+      }
+      if (by_rows) {
+        int64_t b = now.at[0];
+        if (U > 1 && (lane & (ROWS - 1)) >= R) b = now.at[U - 1];
+        now.row = b >= 0 && pos >= lo && pos < hi ? b + (int64_t)(lane & (R - 1)) * a.token_stride : -1;
+      }
+    } else {
+      const uint32_t in = (uint32_t)pos - a.page_div.div((uint32_t)pos) * (uint32_t)a.page_size;
+      now.row = id >= 0 && id < a.n_pages ? (int64_t)id * a.page_stride + (int64_t)in * a.token_stride : -1;
+    }
+    if (by_rows) {
+      seen = (uint32_t)__ballot(now.row >= 0) & kAll;
+      now.at[0] = -1;
+    }
+    static_assert(U <= 2 && ROWS <= 32 && kRun != 0, "places of one or two runs");
+  }
+  // Starts the copies of the rows into LDS at dst (rows back to back, chunks placed by the swizzle).
+  template <bool IS_V>
+  __device__ __forceinline__ void copy(const Place& pl, const uint8_t* head, uint8_t* dst, int row0, int lane) const {
+    if (pl.at[0] >= 0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t b = uniform64((int64_t)(uintptr_t)head + pl.at[u]);
+        if constexpr (NI == 1)
+          copy16(b, IS_V ? off_v[0] : off_k[0], dst + u * 1024);
+        else
+#pragma unroll
+          for (int i = 0; i < NI; i += 2)
+            copy16_pair(b, IS_V ? off_v[i] : off_k[i], IS_V ? off_v[i + 1] : off_k[i + 1], dst + (u * NI + i) * 1024);
+      }
+    } else {
+      asm volatile("" : "+v"(lane));  // the lane's places are worked out here, not kept in registers
+#pragma unroll
+      for (int i = 0; i < U * NI; ++i) {
+        const int r = i * RPI + lane / CH;
+        const int lo = __shfl((int)pl.row, r), hi = __shfl((int)(pl.row >> 32), r);
+        const int64_t o = ((int64_t)hi << 32) | (uint32_t)lo;
+        const int c = (lane % CH) ^ (IS_V ? swz_v<D>(row0 + r) : swz_k<D>(row0 + r));
+        copy16((hi < 0 ? (const uint8_t*)kZeroRow : head + o) + c * 16, dst + i * 1024);
+      }
+    }
+  }
+};
 
 __device__ __forceinline__ s16x4_t read_tr(const uint8_t* p) {
   return __builtin_amdgcn_ds_read_tr16_b64_v4i16((at_lds_s16x4*)p);
@@ -204,8 +318,13 @@ template <int N> __device__ __forceinline__ void attn_wait_vm() {
 // The wave's LDS reads so far are done: copies over what they read may start.
 __device__ __forceinline__ void attn_wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
-// Sum over the workgroup's 256 threads, and the exclusive prefix; sh holds 8 ints.
-__device__ __forceinline__ int block_scan(int v, int* sh, int& total) {
+// Workgroup barrier after this wave's LDS accesses (not its copies: those are waited for by count).
+__device__ __forceinline__ void attn_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// Sum over the workgroup's threads, and the exclusive prefix; sh holds an int per wave.
+template <int WAVES> __device__ __forceinline__ int block_scan(int v, int* sh, int& total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int x = v;
 #pragma unroll
@@ -218,7 +337,7 @@ __device__ __forceinline__ int block_scan(int v, int* sh, int& total) {
   __syncthreads();
   int before = 0, sum = 0;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
+  for (int w = 0; w < WAVES; ++w) {
     const int s = sh[w];
     before += w < wave ? s : 0;
     sum += s;

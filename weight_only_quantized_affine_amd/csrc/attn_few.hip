@@ -108,7 +108,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few_kernel(const A
   int W = 0;
   for (int s0 = 0; s0 < a.n_seqs; s0 += 256) {
     int total;
-    block_scan(cost(s0 + tid), ssh, total);
+    block_scan<4>(cost(s0 + tid), ssh, total);
     W += total;
   }
   const int nw = min(a.nw_few, W);
@@ -125,7 +125,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few_kernel(const A
     for (int s0 = 0; s0 < a.n_seqs; s0 += 256) {
       int total;
       const int c = cost(s0 + tid);
-      const int e = before + block_scan(c, ssh, total);
+      const int e = before + block_scan<4>(c, ssh, total);
       if (e <= u0 && u0 < e + c) sfound[0] = s0 + tid, sfound[1] = e;
       before += total;
       if (before > u0) break;
@@ -136,6 +136,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few_kernel(const A
 
   uint8_t* sk = sm + wave * 2 * TILE;
   uint8_t* sv = sk + TILE;
+  TileCopy<D, 16, 2, 128> tc;
+  tc.init(a, 0, lane);
   bool recorded = false;
   for (int u = u0; u < u1;) {
     const AttnSeq q = attn_seq(a, s);
@@ -185,14 +187,13 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few_kernel(const A
       for (int d = 0; d < ND; ++d) o[n][d] = f32x4_t{0, 0, 0, 0};
     }
 
-    RowLookup<32> look;
     const int k00 = (first + ta) * 128 + wave * 32;
-    look.load(a, table, k00, lo, hi, lane);
-    int64_t off = look.offset(a);
-    uint32_t seen = (uint32_t)__ballot(off >= 0);
-    copy_rows<D, 32, false>(kb, off, sk, lane);
-    copy_rows<D, 32, true>(vb, off, sv, lane);
-    look.load(a, table, k00 + 128, lo, ta + 1 < tb ? hi : 0, lane);
+    tc.lookup(a, table, k00, lo, hi, lane, true);
+    tc.resolve(a, lo, hi, lane);
+    tc.template copy<false>(tc.now, kb, sk, 0, lane);
+    tc.template copy<true>(tc.now, vb, sv, 0, lane);
+    uint32_t seen = tc.seen;
+    if (ta + 1 < tb) tc.lookup(a, table, k00 + 128, lo, hi, lane, false);
 
     for (int t = ta; t < tb; ++t) {
       const int k0 = (first + t) * 128 + wave * 32;
@@ -215,32 +216,32 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few_kernel(const A
       }
       const uint32_t seen_now = seen;
       if (more) {
-        off = look.offset(a);
-        seen = (uint32_t)__ballot(off >= 0);
-        look.load(a, table, k0 + 256, lo, t + 2 < tb ? hi : 0, lane);
+        tc.resolve(a, lo, hi, lane);
+        seen = tc.seen;
         attn_wait_lds();
-        copy_rows<D, 32, false>(kb, off, sk, lane);
+        tc.template copy<false>(tc.now, kb, sk, 0, lane);
       }
       // masks: rows that are not loaded, keys past a column's query, keys before its window
       const bool cut = k0 + 31 > pos_lo || (a.window > 0 && k0 <= pos_hi - a.window);
       if (cut || seen_now != 0xffffffffu) {
 #pragma unroll
-        for (int n = 0; n < NC; ++n)
+        for (int n = 0; n < NC; ++n) {
+          const int last = qpos[n] - k0, before = a.window > 0 ? last - a.window : -1;
 #pragma unroll
-          for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const int j = 16 * kt + 4 * g + r;
-              const bool see = ((seen_now >> j) & 1) && k0 + j <= qpos[n] && (a.window <= 0 || k0 + j > qpos[n] - a.window);
-              sc[n][kt][r] = see ? sc[n][kt][r] : kNegInf;
-            }
+          for (int r = 0; r < 8; ++r) {
+            const int j = 16 * (r >> 2) + 4 * g + (r & 3);
+            const bool see = ((int)((seen_now >> j) & 1) & (int)(j <= last) & (int)(j > before)) != 0;
+            sc[n][r >> 2][r & 3] = see ? sc[n][r >> 2][r & 3] : kNegInf;
+          }
+        }
       }
       u32x4_t p[NC];
 #pragma unroll
       for (int n = 0; n < NC; ++n) {
-        float mx = sc[n][0][0];
-#pragma unroll
-        for (int r = 1; r < 8; ++r) mx = fmaxf(mx, sc[n][r >> 2][r & 3]);
+        float mx = max3(sc[n][0][0], sc[n][0][1], sc[n][0][2]);
+        mx = max3(mx, sc[n][0][3], sc[n][1][0]);
+        mx = max3(mx, sc[n][1][1], sc[n][1][2]);
+        mx = max3(mx, sc[n][1][3], sc[n][1][3]);
         mx = join32(join16(mx, MaxF()), MaxF()) * a.sl;
         if (__any(mx > m[n] + kLazy)) {
           const float mn = fmaxf(m[n], mx);
@@ -254,12 +255,12 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few_kernel(const A
         const float mr = m[n] == kNegInf ? 0.f : m[n];
         float e[8];
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          e[r] = exp2_fast(__builtin_fmaf(sc[n][r >> 2][r & 3], a.sl, -mr));
-          l[n] += e[r];
+        for (int r = 0; r < 8; ++r) e[r] = exp2_fast(__builtin_fmaf(sc[n][r >> 2][r & 3], a.sl, -mr));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          p[n][r] = pack2(T{}, e[2 * r], e[2 * r + 1]);
+          l[n] = add2(T{}, p[n][r], l[n]);
         }
-        // P rounds once to the cache's type for its product; l sums the unrounded values
-        p[n] = u32x4_t{pack2(T{}, e[0], e[1]), pack2(T{}, e[2], e[3]), pack2(T{}, e[4], e[5]), pack2(T{}, e[6], e[7])};
       }
       if (more)
         attn_wait_vm<NI>();  // V of this tile; the next K may be in flight
@@ -271,7 +272,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few_kernel(const A
       for (int n = 0; n < NC; ++n) few_pv<T, D>(sv, lane, p[n], o[n]);
       if (more) {
         attn_wait_lds();
-        copy_rows<D, 32, true>(vb, off, sv, lane);
+        tc.template copy<true>(tc.now, vb, sv, 0, lane);
+        if (t + 2 < tb) tc.lookup(a, table, k0 + 256, lo, hi, lane, false);
       }
     }
 

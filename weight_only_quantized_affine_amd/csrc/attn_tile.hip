@@ -1,23 +1,35 @@
-// Paged attention, many rows: tiles of 128 query rows of one sequence and kv head (the query heads
-// that share it are folded into the rows: row r is token r / g, head r % g of the group).
+// Paged attention, many rows: tiles of 256 query rows (128 at 256 values a head) of one sequence and
+// kv head (the query heads that share it are folded into the rows: row r is token r / g, head r % g
+// of the group).
 //
-// The matrix cores bound it: 4 D flops per row and key against D / 32 bytes of cache (a tile of 64
-// keys is read once for 128 rows).  4 waves hold 32 rows each: S^T = K Q^T and O^T = V^T P^T by
-// 32x32x16 products; K and V tiles of 64 keys are copied into LDS by all waves, two stages deep,
-// so that one barrier per tile covers both the arrival of a stage and the end of its last reads.
+// The matrix cores bound it: 4 D flops per row and key against D / 64 bytes of cache (a tile of keys
+// is read once for 256 rows).  8 waves hold 32 rows each, two on every SIMD, and take turns: while
+// the first four multiply (O += V^T P^T of the last tile, then S^T = K Q^T of this one), the other
+// four turn their scores into weights on the vector units, and a barrier swaps them.  Left to
+// themselves the two waves of a SIMD fall into step and wait for the same unit (matrix cores 42 %
+// and vector units 37 % busy, never together).  At 256 values a head the registers hold one wave a
+// SIMD.  K and V tiles are copied into LDS by all waves, two stages each, V one turn later than K.
 //
 // Work split.  With many items (sequence, kv head, row tile), one workgroup each, the longest
 // first, kv heads fastest so that a head's tiles run on one XCD and share its L2.  With few, all
-// items are laid end to end in units of one row tile x 64 keys and cut into equal runs, one per
-// resident workgroup; cut items leave pieces for the joining kernel.
+// items are laid end to end in units of one row tile x 64 keys and cut into equal runs, one
+// per compute unit; cut items leave pieces for the joining kernel.
 #include <algorithm>
+#include <type_traits>
 
 #include "attn_common.hpp"
 
 namespace ql {
 namespace {
 
-constexpr int BM = kAttnTileRows, BN = kAttnTileKeys;
+constexpr int BN = kAttnTileKeys;
+// LDS fragments read ahead of the products that take them: a product lasts 32 cycles, a read about
+// four of them.  The order is pinned, since the compiler puts each read right before its product.
+constexpr int kAhead = 4;
+
+// LDS for the finite copy of a V tile (at 256 values a head, where none is left, the fragments are
+// cleaned in registers; the spare registers allow it there).
+constexpr int tile_clean_bytes(int d) { return d == 256 ? 0 : BN * d * 2; }
 
 // V^T fragment of 32 values (tile dt) x 16 keys (step ks): two transposing reads of 4 keys each.
 template <int D> __device__ __forceinline__ u32x4_t v_frag(const uint8_t* sv, int lane, int dt, int ks) {
@@ -42,7 +54,7 @@ __device__ __forceinline__ void tile_nonfinite(const uint8_t* sv, int lane, cons
     // word 2 x + y / 2
     uint32_t w = 0;
 #pragma unroll
-    for (int x = 0; x < 16; ++x) w = x == 4 * (j >> 4) + 2 * ((j >> 3) & 1) + ((j >> 1) & 1) ? p[x >> 2][x & 3] : w;
+    for (int x = 0; x < BN / 4; ++x) w = x == 4 * (j >> 4) + 2 * ((j >> 3) & 1) + ((j >> 1) & 1) ? p[x >> 2][x & 3] : w;
     w = __shfl(w, 32 * ((j >> 2) & 1) + col);
     const bool on = ((j & 1) ? w >> 16 : w) & 0x7fffu;
 #pragma unroll
@@ -62,50 +74,56 @@ __device__ __forceinline__ void tile_nonfinite(const uint8_t* sv, int lane, cons
 }
 
 // Units of row tile j of a sequence: its span's tiles of BN keys.
-__device__ __forceinline__ int tile_cost(const AttnArgs& a, const AttnSeq& q, int j, int& lo, int& hi, int& first) {
+template <int BM> __device__ __forceinline__ int tile_cost(const AttnArgs& a, const AttnSeq& q, int j, int& lo, int& hi, int& first) {
   const int i0 = (int)a.g_div.div((uint32_t)(j * BM));
   const int i1 = min(q.nq - 1, (int)a.g_div.div((uint32_t)(j * BM + BM - 1)));
   attn_span(a, q, i0, i1, lo, hi);
   return attn_tiles<BN>(lo, hi, first);
 }
-__device__ __forceinline__ int row_tiles(const AttnArgs& a, int s) {
+template <int BM> __device__ __forceinline__ int row_tiles(const AttnArgs& a, int s) {
   if (s >= a.n_seqs) return 0;
   const AttnSeq q = attn_seq(a, s);
   return q.nq < 1 || attn_is_few(a, q.nq) ? 0 : (q.nq * a.g + BM - 1) / BM;
 }
 
 template <typename T, int D, bool RUNS>
-__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(const AttnArgs a) {
+__global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) void attn_tile_kernel(const AttnArgs a) {
+  constexpr int WAVES = attn_tile_waves(D), BM = 32 * WAVES;
   constexpr int ROW = D * 2;
   constexpr int KB = BN * ROW;  // bytes of a K (or V) stage
+  constexpr int NK = BN / 32;   // score tiles of 32 keys
   constexpr int NS = D / 16;    // k-steps of the scores
   constexpr int ND = D / 32;    // output tiles of 32 values
-  extern __shared__ __attribute__((aligned(1024))) uint8_t sm[];  // K stages, V stages, then (RUNS) the plan
-  __shared__ int ssh[8];
+  constexpr int NV = BN / 16;   // k-steps of the output
+  constexpr int R = BN / 4;     // keys a wave copies (the second four waves do)
+  constexpr bool kClean = tile_clean_bytes(D) > 0;
+  // K stages, V stages, the finite copy of a V tile, then (RUNS) the plan
+  extern __shared__ __attribute__((aligned(1024))) uint8_t sm[];
+  __shared__ int ssh[WAVES];
   __shared__ int sfound[4];
-  __shared__ uint16_t sseen[2][4];  // per stage and wave: which of its 16 keys are loaded
+  __shared__ __attribute__((aligned(8))) uint16_t sseen[4][4];  // per tile % 4: bit j: key j is loaded
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int h = lane >> 5, col = lane & 31;
 
   int u0, u1, W, nw, w;
-  int* plan = (int*)(sm + 4 * KB);  // RUNS: first unit (of one head) of each row tile, then the sequences' first tiles
+  int* plan = (int*)(sm + 4 * KB + tile_clean_bytes(D));  // RUNS: first unit (of one head) of each row tile, then the sequences' first tiles
   int nt_all = 0;
   int* seq_first = nullptr;
   AttnRecord* rec = nullptr;
   if constexpr (RUNS) {
     // first tile of each sequence, then first unit of each tile
     seq_first = plan + a.plan_tiles + 1;
-    for (int s0 = 0; s0 < a.n_seqs; s0 += 256) {
+    for (int s0 = 0; s0 < a.n_seqs; s0 += 64 * WAVES) {
       int total;
-      const int e = block_scan(row_tiles(a, s0 + tid), ssh, total);
+      const int e = block_scan<WAVES>(row_tiles<BM>(a, s0 + tid), ssh, total);
       if (s0 + tid < a.n_seqs) seq_first[s0 + tid] = nt_all + e;
       nt_all += total;
     }
     nt_all = min(nt_all, a.plan_tiles);  // overlapping sequences could ask for more than t rows hold
     __syncthreads();
     int units = 0;
-    for (int t0 = 0; t0 < nt_all; t0 += 256) {
+    for (int t0 = 0; t0 < nt_all; t0 += 64 * WAVES) {
       const int ti = t0 + tid;
       int c = 0;
       if (ti < nt_all) {
@@ -115,10 +133,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(const 
           if (seq_first[m] <= ti) b = m; else e = m;
         }
         int lo, hi, first;
-        c = tile_cost(a, attn_seq(a, b), ti - seq_first[b], lo, hi, first);
+        c = tile_cost<BM>(a, attn_seq(a, b), ti - seq_first[b], lo, hi, first);
       }
       int total;
-      const int e = block_scan(c, ssh, total);
+      const int e = block_scan<WAVES>(c, ssh, total);
       if (ti < nt_all) plan[ti] = units + e;
       units += total;
     }
@@ -142,6 +160,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(const 
     u1 = u0 + 1;
   }
 
+  const int late = wave / 4;  // the second four waves run one turn behind
+  const bool copier = wave >= WAVES - 4;
+  const int row0 = R * (wave & 3);  // first key of a tile that a copying wave copies
+  TileCopy<D, R, 1, BN> tc;
+  tc.init(a, row0, lane);
   bool recorded = false;
   for (int u = u0; u < u1;) {
     int s, j, head, ta, tb, nt, item0 = 0, lo, hi, first;
@@ -168,7 +191,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(const 
       j = __builtin_amdgcn_readfirstlane(ti - seq_first[b]);
       head = __builtin_amdgcn_readfirstlane(head);
       q = attn_seq(a, s);
-      tile_cost(a, q, j, lo, hi, first);
+      tile_cost<BM>(a, q, j, lo, hi, first);
       tb = min(nt, u1 - item0);
       u = item0 + tb;
     } else {
@@ -176,10 +199,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(const 
       const int target = u / a.hk;
       int before = 0;
       if (tid == 0) sfound[0] = -1;
-      for (int s0 = 0; s0 < a.n_seqs; s0 += 256) {
+      for (int s0 = 0; s0 < a.n_seqs; s0 += 64 * WAVES) {
         int total;
-        const int c = row_tiles(a, s0 + tid);
-        const int e = before + block_scan(c, ssh, total);
+        const int c = row_tiles<BM>(a, s0 + tid);
+        const int e = before + block_scan<WAVES>(c, ssh, total);
         if (e <= target && target < e + c) sfound[0] = s0 + tid, sfound[1] = c - 1 - (target - e);  // longest first
         before += total;
         if (before > target) break;
@@ -188,7 +211,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(const 
       s = sfound[0], j = sfound[1];
       if (s < 0) return;  // more workgroups than row tiles
       q = attn_seq(a, s);
-      nt = tile_cost(a, q, j, lo, hi, first);
+      nt = tile_cost<BM>(a, q, j, lo, hi, first);
       ta = 0, tb = nt;
       u = u1;
     }
@@ -213,9 +236,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(const 
     const int pos_lo = q.kv - q.nq + min(q.nq - 1, (int)a.g_div.div((uint32_t)(j * BM + 32 * wave)));
     const int pos_hi = q.kv - q.nq + min(q.nq - 1, (int)a.g_div.div((uint32_t)(j * BM + 32 * wave + 31)));
 
-    // and among the workgroup's
-    const int wg_lo = q.kv - q.nq + (int)a.g_div.div((uint32_t)(j * BM));
-    const int wg_hi = q.kv - q.nq + min(q.nq - 1, (int)a.g_div.div((uint32_t)(j * BM + BM - 1)));
+    const bool idle = 32 * wave >= rows;
 
     f32x16_t o[ND];
 #pragma unroll
@@ -223,75 +244,115 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(const 
 #pragma unroll
       for (int x = 0; x < 16; ++x) o[d][x] = 0.f;
     float m = kNegInf, l = 0.f;
+    f32x16_t sc[NK];
+    u32x4_t p[NV];
 
     const uint8_t* kb = a.k + (int64_t)head * a.head_stride;
     const uint8_t* vb = a.v + (int64_t)head * a.head_stride;
     const int32_t* table = a.table + (int64_t)s * a.table_stride;
-    RowLookup<16> look;
-    auto stage_in = [&](int st) {  // copies this wave's 16 rows of the looked-up tile into a stage
-      const int64_t off = look.offset(a);
-      const uint32_t seen = (uint32_t)__ballot(off >= 0) & 0xffffu;
-      if (lane == 0) sseen[st][wave] = (uint16_t)seen;
-      // rows 16 wave .. of the tile: the swizzles repeat every 16 rows
-      copy_rows<D, 16, false>(kb, off, sm + st * KB + wave * 16 * ROW, lane);
-      copy_rows<D, 16, true>(vb, off, sm + 2 * KB + st * KB + wave * 16 * ROW, lane);
+    const int n = tb - ta, kfirst = (first + ta) * BN;
+    auto copy_k = [&](int t) {
+      tc.resolve(a, lo, hi, lane);
+      if (lane == 0) sseen[t & 3][wave & 3] = (uint16_t)tc.seen;
+      tc.template copy<false>(tc.now, kb, sm + (t & 1) * KB + row0 * ROW, row0, lane);
     };
-    __syncthreads();  // the last item's reads of the stages are done
-    look.load(a, table, (first + ta) * BN + 16 * wave, lo, hi, lane);
-    stage_in(0);
-    look.load(a, table, (first + ta + 1) * BN + 16 * wave, lo, ta + 1 < tb ? hi : 0, lane);
+    // V of t and K of t + 1 start, the pages of t + 2 are read
+    auto copies = [&](int t) {
+      if (t >= n) return;
+      tc.template copy<true>(tc.now, vb, sm + 2 * KB + (t & 1) * KB + row0 * ROW, row0, lane);
+      if (t + 1 < n) copy_k(t + 1);
+      if (t + 2 < n) tc.lookup(a, table, kfirst + (t + 2) * BN + row0, lo, hi, lane, false);
+    };
+    auto is_cut = [&](int t) {  // whether some row does not see all of it
+      const int k0 = kfirst + t * BN;
+      return k0 + BN - 1 > pos_lo || (a.window > 0 && k0 <= pos_hi - a.window);
+    };
 
-    for (int t = ta; t < tb; ++t) {
-      const int st = (t - ta) & 1;
-      const int k0 = (first + t) * BN;
-      attn_wait_vm<0>();
-      __syncthreads();  // every wave's rows of stage st are there, and its reads of the other are done
-      if (t + 1 < tb) {
-        stage_in(st ^ 1);
-        look.load(a, table, k0 + 2 * BN + 16 * wave, lo, t + 2 < tb ? hi : 0, lane);
-      }
-      // a key that only some rows of the workgroup see may hold an infinity or a NaN
+    // Products A .. B of the list: first the NV ND of output(t), o += V^T P^T, then the NK NS of
+    // scores(t + 1), with the LDS fragments read kAhead products before their own.
+    constexpr int NO = NV * ND, NP = NO + NK * NS;
+    auto products = [&](int t, auto A, auto B) {
+      const uint8_t* sv = sm + 2 * KB + (t & 1) * KB;
       bool odd = false;
-      if (k0 + BN - 1 > wg_lo || (a.window > 0 && k0 <= wg_hi - a.window)) {
+      if (A < NO && is_cut(t)) {  // a key that only some rows see may hold an infinity or a NaN
         uint32_t acc = 0;
-#pragma unroll
-        for (int x = 0; x < KB / 4096; ++x) {
-          const u32x4_t v = *(const u32x4_t*)(sm + 2 * KB + st * KB + x * 4096 + tid * 16);
+#pragma unroll 4
+        for (int x = 0; x < KB / 1024; ++x) {
+          const u32x4_t v = *(const u32x4_t*)(sv + x * 1024 + lane * 16);
           for (int y = 0; y < 4; ++y) acc |= nonfinite2<T>(v[y]);
         }
-        odd = __syncthreads_or((acc & 0x80008000u) != 0);
-      }
-      // no row of the wave sees the tile
-      if (!odd && (k0 > pos_hi || (a.window > 0 && k0 + BN - 1 <= pos_lo - a.window))) continue;
-      const uint8_t* sk = sm + st * KB;
-      uint8_t* sv = sm + 2 * KB + st * KB;
-      f32x16_t sc[2];
-#pragma unroll
-      for (int kt = 0; kt < 2; ++kt) {
-        const int row = 32 * kt + col;
-#pragma unroll
-        for (int x = 0; x < 16; ++x) sc[kt][x] = 0.f;
-#pragma unroll
-        for (int s2 = 0; s2 < NS; ++s2) {
-          const u32x4_t kf = *(const u32x4_t*)(sk + row * ROW + ((2 * s2 + h) ^ swz_k<D>(row)) * 16);
-          sc[kt] = mfma32(T{}, kf, qf[s2], sc[kt]);
+        odd = __any((acc & 0x80008000u) != 0);
+        if (odd) tile_nonfinite<T, D>(sv, lane, p, o);
+        if (kClean && odd) {
+          // every wave that meets such a tile writes the same finite copy of it before its own reads
+          uint8_t* clean = sm + 4 * KB;
+#pragma unroll 4
+          for (int x = 0; x < KB / 1024; ++x) {
+            u32x4_t v = *(const u32x4_t*)(sv + x * 1024 + lane * 16);
+            for (int y = 0; y < 4; ++y) v[y] = finite2<T>(v[y]);
+            *(u32x4_t*)(clean + x * 1024 + lane * 16) = v;
+          }
+          sv = clean;
         }
       }
-      const uint64_t seen = *(const uint64_t*)sseen[st];
-      const bool cut = k0 + BN - 1 > pos_lo || (a.window > 0 && k0 <= pos_hi - a.window);
-      if (cut || seen != ~(uint64_t)0) {
+      const uint8_t* kr = sm + ((t + 1) & 1) * KB + col * ROW;
+      auto load = [&](int i) {
+        if (i >= NO) {  // step j / NK of keys 32 (j % NK) ..
+          const int j = i - NO;
+          return *(const u32x4_t*)(kr + (j % NK) * (32 * ROW) + ((2 * (j / NK) + h) ^ swz_k<D>(col)) * 16);
+        }
+        u32x4_t v = v_frag<D>(sv, lane, i % ND, i / ND);
+        if (!kClean && odd)
+          for (int y = 0; y < 4; ++y) v[y] = finite2<T>(v[y]);
+        return v;
+      };
+      if (B > NO) {
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt)
+        for (int kt = 0; kt < NK; ++kt)
 #pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            const int jj = 32 * kt + 8 * (x >> 2) + 4 * h + (x & 3);
-            const bool see = ((seen >> jj) & 1) && k0 + jj <= qpos && (a.window <= 0 || k0 + jj > qpos - a.window);
-            sc[kt][x] = see ? sc[kt][x] : kNegInf;
-          }
+          for (int x = 0; x < 16; ++x) sc[kt][x] = 0.f;
       }
-      float mx = sc[0][0];
+      u32x4_t f[NP];
 #pragma unroll
-      for (int x = 1; x < 32; ++x) mx = fmaxf(mx, sc[x >> 4][x & 15]);
+      for (int i = A; i < A + kAhead; ++i) f[i] = load(i);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = A; i < B; ++i) {
+        if (i < NO)
+          o[i % ND] = mfma32(T{}, f[i], p[i / ND], o[i % ND]);
+        else
+          sc[(i - NO) % NK] = mfma32(T{}, f[i], qf[(i - NO) / NK], sc[(i - NO) % NK]);
+        if (i + kAhead < B) f[i + kAhead] = load(i + kAhead);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    constexpr std::integral_constant<int, 0> kFirst{};
+    constexpr std::integral_constant<int, NO> kScores{};
+    constexpr std::integral_constant<int, NP> kLast{};
+
+    auto weights = [&](int t) {
+      const int k0 = kfirst + t * BN;
+      if (is_cut(t)) {
+        asm volatile("");  // kept a branch: few tiles are cut
+        const int last = qpos - k0 - 4 * h, before = a.window > 0 ? last - a.window : -BN - 1;
+#pragma unroll
+        for (int x = 0; x < 16 * NK; ++x) {
+          const int jj = 32 * (x >> 4) + 8 * ((x >> 2) & 3) + (x & 3);
+          sc[x >> 4][x & 15] = ((int)(jj <= last) & (int)(jj > before)) ? sc[x >> 4][x & 15] : kNegInf;
+        }
+      }
+      const uint64_t seen = *(const uint64_t*)sseen[t & 3];
+      if (seen != ~(uint64_t)0) {
+        asm volatile("");
+        const uint32_t s0 = (uint32_t)seen >> (4 * h), s1 = (uint32_t)(seen >> 32) >> (4 * h);
+#pragma unroll
+        for (int x = 0; x < 32; ++x)
+          sc[x >> 4][x & 15] = ((x < 16 ? s0 : s1) >> (8 * ((x >> 2) & 3) + (x & 3)) & 1) ? sc[x >> 4][x & 15] : kNegInf;
+      }
+      float mx = max3(sc[0][0], sc[0][1], sc[0][2]);
+#pragma unroll
+      for (int x = 3; x < 16 * NK - 1; x += 2) mx = max3(mx, sc[x >> 4][x & 15], sc[(x + 1) >> 4][(x + 1) & 15]);
+      mx = max3(mx, sc[NK - 1][15], sc[NK - 1][15]);
       mx = join32(mx, MaxF()) * a.sl;
       if (__any(mx > m + kLazy)) {
         const float mn = fmaxf(m, mx);
@@ -304,34 +365,53 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_tile_kernel(const 
           for (int x = 0; x < 16; ++x) o[d][x] *= f;
       }
       const float mr = m == kNegInf ? 0.f : m;
-      u32x4_t p[4];
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks) {
+      for (int ks = 0; ks < NV; ++ks) {
         float e[8];
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          e[x] = exp2_fast(__builtin_fmaf(sc[ks >> 1][8 * (ks & 1) + x], a.sl, -mr));
-          l += e[x];
+        for (int x = 0; x < 8; ++x) e[x] = exp2_fast(__builtin_fmaf(sc[ks >> 1][8 * (ks & 1) + x], a.sl, -mr));
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          p[ks][x] = pack2(T{}, e[2 * x], e[2 * x + 1]);
+          l = add2(T{}, p[ks][x], l);
         }
-        // P rounds once to the cache's type for its product; l sums the unrounded values
-        p[ks] = u32x4_t{pack2(T{}, e[0], e[1]), pack2(T{}, e[2], e[3]), pack2(T{}, e[4], e[5]), pack2(T{}, e[6], e[7])};
       }
-      if (odd) {
-        tile_nonfinite<T, D>(sv, lane, p, o);
-        __syncthreads();
-#pragma unroll
-        for (int x = 0; x < KB / 4096; ++x) {
-          u32x4_t* at = (u32x4_t*)(sv + x * 4096 + tid * 16);
-          u32x4_t v = *at;
-          for (int y = 0; y < 4; ++y) v[y] = finite2<T>(v[y]);
-          *at = v;
-        }
-        __syncthreads();
+    };
+    // Turn i: the first four waves take scores(0) in turn 0, weights(t) in turn 2 t + 1, output(t)
+    // and scores(t + 1) in turn 2 t + 2; the others the same one turn later, and in even turns, beside
+    // their weights, they start the copies, which are waited for at the end of odd turns.
+    int turn = 0;
+    auto begin = [&] {
+      if (copier && (turn & 1) == 0) copies(turn >> 1);
+    };
+    auto end = [&] {
+      if (copier && (turn & 1)) attn_wait_vm<0>();
+      attn_barrier();
+      ++turn;
+    };
+    if (copier) {
+      tc.lookup(a, table, kfirst + row0, lo, hi, lane, true);
+      copy_k(0);
+      if (n > 1) tc.lookup(a, table, kfirst + BN + row0, lo, hi, lane, false);
+      attn_wait_vm<0>();
+    }
+    attn_barrier();  // K of the first tile is there, and the last item's reads are done
+    if (idle) {      // no rows: the copies only
+      while (turn < 2 * n + 2) begin(), end();
+    } else {
+      if (late) begin(), end();
+      begin();
+      products(-1, kScores, kLast);
+      end();
+      for (int t = 0; t < n; ++t) {
+        begin();
+        weights(t);
+        end();
+        begin();
+        products(t, kFirst, kLast);  // (after the last tile the scores are of stale keys and unused)
+        end();
       }
-#pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
-#pragma unroll
-        for (int d = 0; d < ND; ++d) o[d] = mfma32(T{}, v_frag<D>(sv, lane, d, ks), p[ks], o[d]);
+      if (!late) begin(), end();
     }
     l = join32(l, SumF());
 
@@ -428,12 +508,13 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a, int fi
 }
 
 template <typename T, int D> hipError_t tile(const AttnArgs& a, hipStream_t s) {
-  const size_t lds = (size_t)4 * BN * D * 2;
+  const size_t lds = (size_t)4 * BN * D * 2 + tile_clean_bytes(D);
+  constexpr int threads = 64 * attn_tile_waves(D);
   if (a.nw_tile > 0) {
     const size_t plan = ((size_t)a.plan_tiles + 1 + a.n_seqs) * 4;
-    attn_tile_kernel<T, D, true><<<a.nw_tile, 256, lds + plan, s>>>(a);
+    attn_tile_kernel<T, D, true><<<a.nw_tile, threads, lds + plan, s>>>(a);
   } else {
-    attn_tile_kernel<T, D, false><<<a.items_tile, 256, lds, s>>>(a);
+    attn_tile_kernel<T, D, false><<<a.items_tile, threads, lds, s>>>(a);
   }
   return hipGetLastError();
 }
@@ -444,6 +525,7 @@ template <typename T, int D> hipError_t join(const AttnArgs& a, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   if (a.nw_tile > 0 && a.join_tile) {
+    constexpr int BM = 32 * attn_tile_waves(D);
     attn_join_kernel<T, D><<<dim3(a.nw_tile, BM / 16), 256, 0, s>>>(a, a.nw_few, a.part_tile, BM * (D + 2), BM);
     return hipGetLastError();
   }
@@ -455,7 +537,7 @@ template <typename T, int D> hipError_t join(const AttnArgs& a, hipStream_t s) {
 AttnPlan attn_plan(int64_t t, int64_t n_seqs, int64_t hq, int64_t hk, int d, int64_t max_q, int64_t max_kv,
                    int64_t window) {
   AttnPlan p{};
-  const int64_t g = hq / hk;
+  const int64_t g = hq / hk, bm = 32 * attn_tile_waves(d);
   const int64_t cap = d == 256 ? 16 : 32;  // rows whose registers fit
   const int64_t limit = int64_t(1) << 31;
   const int64_t span = window > 0 ? std::min(max_kv, window + max_q - 1) : max_kv;  // longest span of an item
@@ -481,8 +563,8 @@ AttnPlan attn_plan(int64_t t, int64_t n_seqs, int64_t hq, int64_t hk, int d, int
     p.join_few = max_kv > kAttnFewKeys;  // a span inside one tile is never cut
   }
   if (p.tile) {
-    const int64_t slots = d == 256 ? 256 : 512;  // resident workgroups
-    const int64_t full = t * g / kAttnTileRows;
+    const int64_t slots = 256;  // resident workgroups
+    const int64_t full = t * g / bm;
     const int64_t seqs = std::min<int64_t>(n_seqs, t * g / (p.few_rows + 1));
     const int64_t tiles = full + seqs;
     p.plan_tiles = (int)tiles;
@@ -502,7 +584,7 @@ AttnPlan attn_plan(int64_t t, int64_t n_seqs, int64_t hq, int64_t hk, int d, int
   };
   take((size_t)(p.nw_few + p.nw_tile) * sizeof(AttnRecord));
   p.part_off = take((size_t)2 * p.nw_few * p.part_floats * 4);
-  p.part_tile_off = take((size_t)2 * p.nw_tile * kAttnTileRows * (d + 2) * 4);
+  p.part_tile_off = take((size_t)2 * p.nw_tile * bm * (d + 2) * 4);
   p.bytes = at;
   return p;
 }

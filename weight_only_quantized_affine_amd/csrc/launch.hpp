@@ -350,8 +350,9 @@ hipError_t launch_norm_rope(const NormRopeArgs& a, int dt, hipStream_t s);
 
 // Paged attention (attn_few.hip: sequences of few rows; attn_tile.hip: the others and the joining of
 // split items).  Strides in bytes.
-constexpr int kAttnTileRows = 128;  // query rows of a row tile
-constexpr int kAttnTileKeys = 64;   // keys of its unit of work
+constexpr int kAttnTileKeys = 64;  // keys of the tile kernel's unit of work
+// Waves of its workgroups, 32 query rows each (256 values a head fill a SIMD's registers).
+constexpr int attn_tile_waves(int d) { return d == 256 ? 4 : 8; }
 constexpr int kAttnFewKeys = 128;   // keys of the few-row kernel's unit
 struct AttnRecord;
 struct AttnArgs {
@@ -360,6 +361,7 @@ struct AttnArgs {
   const uint8_t *k, *v;
   int64_t page_stride, token_stride, head_stride;
   int n_pages, page_size;
+  int page16;  // pages are multiples of 16 slots, and 16 rows of one lie within 2^31 bytes
   FastDiv page_div;
   const int32_t* table;
   int64_t table_stride;  // entries

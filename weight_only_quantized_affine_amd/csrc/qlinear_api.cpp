@@ -905,6 +905,7 @@ ql_status qlinear_paged_attention(const ql_heads* q, const ql_heads* out, ql_dty
   a.head_stride = 2 * cache->head_stride;
   a.n_pages = (int)cache->n_pages;
   a.page_size = (int)cache->page_size;
+  a.page16 = cache->page_size % 16 == 0 && a.token_stride < (int64_t(1) << 27);
   a.page_div = ql::fast_div((uint32_t)cache->page_size);
   a.table = block_table;
   a.table_stride = table_stride;
