@@ -112,12 +112,15 @@ template <typename T> __device__ __forceinline__ void only_nonfinite(uint32_t w,
   b = on && (nf & 0x80000000u) ? param_to_f32<T>(w >> 16) : 0.f;
 }
 
-// Position of 16-byte chunk c of row r in a tile of rows of D values: K is read 16 (or 32) rows
-// at one chunk, V 8 rows at two neighbouring chunks (the transposing reads); both then meet every
-// bank once.
+// Position of 16-byte chunk c of row r in a tile of rows of D values.  The LDS has 256 bytes of banks:
+// K is read 16 rows at one chunk per pass, V (transposing, 32 bytes of a row) either 8 rows at one
+// chunk pair or 4 rows at two neighbouring pairs; the positions of each set are distinct modulo 256
+// bytes.  (V's pairs by r & 7 alone: the tile kernel's reads met every bank twice, a third of its
+// LDS cycles.)
 template <int D> __device__ __forceinline__ int swz_k(int r) { return D >= 128 ? (r & 15) : ((r >> 1) & 7); }
 template <int D> __device__ __forceinline__ int swz_v(int r) {
-  return D >= 128 ? ((r & 7) << 1) : (((r >> 1) & 3) << 1);
+  if (D >= 128) return ((r & 3) << 2) | ((r & 4) >> 1);
+  return ((r & 2) << 1) | ((r & 4) >> 1);
 }
 
 // One sequence: its query rows [q0, q0 + nq) and cached length kv, kept inside the arrays whatever

@@ -27,9 +27,12 @@ constexpr int BN = kAttnTileKeys;
 // four of them.  The order is pinned, since the compiler puts each read right before its product.
 constexpr int kAhead = 4;
 
-// LDS for the finite copy of a V tile (at 256 values a head, where none is left, the fragments are
+// Stages of K and of V: three let a copy take four turns, which the fabric needs under load (two:
+// 582 against ... us); 256 values a head leave room for two.
+constexpr int tile_stages(int d) { return d == 256 ? 2 : 3; }
+// LDS for the finite copies of two V tiles, one for each wave group (at 256 values a head, where none is left, the fragments are
 // cleaned in registers; the spare registers allow it there).
-constexpr int tile_clean_bytes(int d) { return d == 256 ? 0 : BN * d * 2; }
+constexpr int tile_clean_bytes(int d) { return d == 256 ? 0 : 2 * BN * d * 2; }
 
 // V^T fragment of 32 values (tile dt) x 16 keys (step ks): two transposing reads of 4 keys each.
 template <int D> __device__ __forceinline__ u32x4_t v_frag(const uint8_t* sv, int lane, int dt, int ks) {
@@ -97,7 +100,8 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
   constexpr int NV = BN / 16;   // k-steps of the output
   constexpr int R = BN / 4;     // keys a wave copies (the second four waves do)
   constexpr bool kClean = tile_clean_bytes(D) > 0;
-  // K stages, V stages, the finite copy of a V tile, then (RUNS) the plan
+  constexpr int ST = tile_stages(D);  // stages of K, and of V
+  // K stages, V stages, finite copies of V, then (RUNS) the plan
   extern __shared__ __attribute__((aligned(1024))) uint8_t sm[];
   __shared__ int ssh[WAVES];
   __shared__ int sfound[4];
@@ -107,7 +111,7 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
   const int h = lane >> 5, col = lane & 31;
 
   int u0, u1, W, nw, w;
-  int* plan = (int*)(sm + 4 * KB + tile_clean_bytes(D));  // RUNS: first unit (of one head) of each row tile, then the sequences' first tiles
+  int* plan = (int*)(sm + 2 * ST * KB + tile_clean_bytes(D));  // RUNS: first unit (of one head) of each row tile, then the sequences' first tiles
   int nt_all = 0;
   int* seq_first = nullptr;
   AttnRecord* rec = nullptr;
@@ -161,7 +165,7 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
   }
 
   const int late = wave / 4;  // the second four waves run one turn behind
-  const bool copier = wave >= WAVES - 4;
+  const bool copier = wave < 4;
   const int row0 = R * (wave & 3);  // first key of a tile that a copying wave copies
   TileCopy<D, R, 1, BN> tc;
   tc.init(a, row0, lane);
@@ -251,17 +255,18 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
     const uint8_t* vb = a.v + (int64_t)head * a.head_stride;
     const int32_t* table = a.table + (int64_t)s * a.table_stride;
     const int n = tb - ta, kfirst = (first + ta) * BN;
+    auto stage_k = [&](int t) { return sm + (t % ST) * KB; };
+    auto stage_v = [&](int t) { return sm + (ST + t % ST) * KB; };
     auto copy_k = [&](int t) {
       tc.resolve(a, lo, hi, lane);
       if (lane == 0) sseen[t & 3][wave & 3] = (uint16_t)tc.seen;
-      tc.template copy<false>(tc.now, kb, sm + (t & 1) * KB + row0 * ROW, row0, lane);
+      tc.template copy<false>(tc.now, kb, stage_k(t) + row0 * ROW, row0, lane);
+      if (t + 1 < n) tc.lookup(a, table, kfirst + (t + 1) * BN + row0, lo, hi, lane, false);
     };
-    // V of t and K of t + 1 start, the pages of t + 2 are read
+    // V of t and K of t + 1 start (their stages' last readers are a period past)
     auto copies = [&](int t) {
-      if (t >= n) return;
-      tc.template copy<true>(tc.now, vb, sm + 2 * KB + (t & 1) * KB + row0 * ROW, row0, lane);
+      if (t < n) tc.template copy<true>(tc.now, vb, stage_v(t) + row0 * ROW, row0, lane);
       if (t + 1 < n) copy_k(t + 1);
-      if (t + 2 < n) tc.lookup(a, table, kfirst + (t + 2) * BN + row0, lo, hi, lane, false);
     };
     auto is_cut = [&](int t) {  // whether some row does not see all of it
       const int k0 = kfirst + t * BN;
@@ -272,7 +277,7 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
     // scores(t + 1), with the LDS fragments read kAhead products before their own.
     constexpr int NO = NV * ND, NP = NO + NK * NS;
     auto products = [&](int t, auto A, auto B) {
-      const uint8_t* sv = sm + 2 * KB + (t & 1) * KB;
+      const uint8_t* sv = stage_v(t);
       bool odd = false;
       if (A < NO && is_cut(t)) {  // a key that only some rows see may hold an infinity or a NaN
         uint32_t acc = 0;
@@ -285,7 +290,7 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
         if (odd) tile_nonfinite<T, D>(sv, lane, p, o);
         if (kClean && odd) {
           // every wave that meets such a tile writes the same finite copy of it before its own reads
-          uint8_t* clean = sm + 4 * KB;
+          uint8_t* clean = sm + (2 * ST + (t & 1)) * KB;
 #pragma unroll 4
           for (int x = 0; x < KB / 1024; ++x) {
             u32x4_t v = *(const u32x4_t*)(sv + x * 1024 + lane * 16);
@@ -295,7 +300,7 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
           sv = clean;
         }
       }
-      const uint8_t* kr = sm + ((t + 1) & 1) * KB + col * ROW;
+      const uint8_t* kr = stage_k(t + 1) + col * ROW;
       auto load = [&](int i) {
         if (i >= NO) {  // step j / NK of keys 32 (j % NK) ..
           const int j = i - NO;
@@ -377,41 +382,37 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
         }
       }
     };
-    // Turn i: the first four waves take scores(0) in turn 0, weights(t) in turn 2 t + 1, output(t)
-    // and scores(t + 1) in turn 2 t + 2; the others the same one turn later, and in even turns, beside
-    // their weights, they start the copies, which are waited for at the end of odd turns.
-    int turn = 0;
-    auto begin = [&] {
-      if (copier && (turn & 1) == 0) copies(turn >> 1);
-    };
-    auto end = [&] {
-      if (copier && (turn & 1)) attn_wait_vm<0>();
-      attn_barrier();
-      ++turn;
-    };
+    // Every wave takes weights(t), then output(t) and scores(t + 1).  A period ends with a barrier,
+    // which the first four waves meet after the products and the others after the weights.  Copies
+    // start with a period and are waited for at its end.
+    attn_barrier();  // the last item's reads are done
     if (copier) {
       tc.lookup(a, table, kfirst + row0, lo, hi, lane, true);
       copy_k(0);
-      if (n > 1) tc.lookup(a, table, kfirst + BN + row0, lo, hi, lane, false);
+      copies(0);
       attn_wait_vm<0>();
     }
-    attn_barrier();  // K of the first tile is there, and the last item's reads are done
-    if (idle) {      // no rows: the copies only
-      while (turn < 2 * n + 2) begin(), end();
-    } else {
-      if (late) begin(), end();
-      begin();
-      products(-1, kScores, kLast);
-      end();
+    attn_barrier();
+    if (idle) {  // no rows: the copies only
       for (int t = 0; t < n; ++t) {
-        begin();
-        weights(t);
-        end();
-        begin();
-        products(t, kFirst, kLast);  // (after the last tile the scores are of stale keys and unused)
-        end();
+        if (copier) {
+          copies(t + 1);
+          attn_wait_vm<0>();
+        }
+        attn_barrier();
       }
-      if (!late) begin(), end();
+    } else {
+      products(-1, kScores, kLast);
+      for (int t = 0; t < n; ++t) {
+        if (copier) copies(t + 1);
+        weights(t);
+        if (late) attn_barrier();
+        products(t, kFirst, kLast);  // (after the last tile the scores are of stale keys and unused)
+        if (!late) {
+          attn_wait_vm<0>();
+          attn_barrier();
+        }
+      }
     }
     l = join32(l, SumF());
 
@@ -508,7 +509,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a, int fi
 }
 
 template <typename T, int D> hipError_t tile(const AttnArgs& a, hipStream_t s) {
-  const size_t lds = (size_t)4 * BN * D * 2 + tile_clean_bytes(D);
+  const size_t lds = (size_t)2 * tile_stages(D) * BN * D * 2 + tile_clean_bytes(D);
   constexpr int threads = 64 * attn_tile_waves(D);
   if (a.nw_tile > 0) {
     const size_t plan = ((size_t)a.plan_tiles + 1 + a.n_seqs) * 4;
