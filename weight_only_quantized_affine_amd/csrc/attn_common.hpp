@@ -165,32 +165,54 @@ __device__ __attribute__((aligned(16))) static uint32_t kZeroRow[128] = {};
 __device__ __forceinline__ uint32_t lds_at(const uint8_t* p) {
   return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(at_lds_void*)p);
 }
-__device__ __forceinline__ void copy16(const uint8_t* src, uint8_t* dst) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
-               :
-               : "s"(lds_at(dst)), "v"(src)
-               : "memory", "m0");
+//
+// NT: the non-temporal policy, for rows that no other workgroup reads (few-row kernel: one sequence
+// of 131071 114 -> 102 us, 64 ragged ones 163 -> 147 us; the tile kernel's row tiles share their
+// keys, and lose 10 % by it).
+template <bool NT> __device__ __forceinline__ void copy16(const uint8_t* src, uint8_t* dst) {
+  if constexpr (NT)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off nt"
+                 :
+                 : "s"(lds_at(dst)), "v"(src)
+                 : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                 :
+                 : "s"(lds_at(dst)), "v"(src)
+                 : "memory", "m0");
 }
 __device__ __forceinline__ int64_t uniform64(int64_t x) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x), hi = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
   return (int64_t)((uint64_t)hi << 32 | lo);
 }
-// The same from a uniform base plus the lane's offset.  (A scalar written by a vector instruction
-// needs 5 wait states before a load takes it.)
-__device__ __forceinline__ void copy16(int64_t base, uint32_t off, uint8_t* dst) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2"
-               :
-               : "s"(lds_at(dst)), "v"(off), "s"(base)
-               : "memory", "m0");
-}
-// Two of them, 1 KB apart in LDS.
-__device__ __forceinline__ void copy16_pair(int64_t base, uint32_t off0, uint32_t off1, uint8_t* dst) {
-  asm volatile(
-      "s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %3\n\t"
-      "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3"
-      :
-      : "s"(lds_at(dst)), "v"(off0), "v"(off1), "s"(base)
-      : "memory", "m0", "scc");
+// Two of them, 1 KB apart in LDS, from a uniform base plus the lane's offsets (off1 is not used for
+// one).  A scalar written by a vector instruction needs 5 wait states before a load takes it.
+template <bool NT, bool TWO>
+__device__ __forceinline__ void copy16_from(int64_t base, uint32_t off0, uint32_t off1, uint8_t* dst) {
+  if constexpr (TWO && NT)
+    asm volatile(
+        "s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %3 nt\n\t"
+        "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3 nt"
+        :
+        : "s"(lds_at(dst)), "v"(off0), "v"(off1), "s"(base)
+        : "memory", "m0", "scc");
+  else if constexpr (TWO)
+    asm volatile(
+        "s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %3\n\t"
+        "s_add_u32 m0, m0, 0x400\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3"
+        :
+        : "s"(lds_at(dst)), "v"(off0), "v"(off1), "s"(base)
+        : "memory", "m0", "scc");
+  else if constexpr (NT)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2 nt"
+                 :
+                 : "s"(lds_at(dst)), "v"(off0), "s"(base)
+                 : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(lds_at(dst)), "v"(off0), "s"(base)
+                 : "memory", "m0");
 }
 
 // The cache rows of a tile that one wave copies, U runs of R rows (positions base .. base + U R; R
@@ -201,7 +223,7 @@ __device__ __forceinline__ void copy16_pair(int64_t base, uint32_t off0, uint32_
 // never change.  (One scalar load per tile instead shares its counter with the LDS reads: every
 // read after it waits for it.)  Else, and for runs that end inside, row r is looked up by the lanes
 // with lane % (U R) == r, and handed to the lanes that copy it.
-template <int D, int R, int U, int STEP> struct TileCopy {
+template <int D, int R, int U, int STEP, bool NT> struct TileCopy {
   static constexpr int CH = D / 8;      // 16-byte chunks of a row
   static constexpr int RPI = 64 / CH;   // rows of an instruction (1 KB)
   static constexpr int NI = R / RPI;    // instructions of a run
@@ -286,12 +308,10 @@ template <int D, int R, int U, int STEP> struct TileCopy {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int64_t b = uniform64((int64_t)(uintptr_t)head + pl.at[u]);
-        if constexpr (NI == 1)
-          copy16(b, IS_V ? off_v[0] : off_k[0], dst + u * 1024);
-        else
 #pragma unroll
-          for (int i = 0; i < NI; i += 2)
-            copy16_pair(b, IS_V ? off_v[i] : off_k[i], IS_V ? off_v[i + 1] : off_k[i + 1], dst + (u * NI + i) * 1024);
+        for (int i = 0; i < NI; i += 2)
+          copy16_from<NT, (NI > 1)>(b, IS_V ? off_v[i] : off_k[i], IS_V ? off_v[(i + 1) % NI] : off_k[(i + 1) % NI],
+                                    dst + (u * NI + i) * 1024);
       }
     } else {
       asm volatile("" : "+v"(lane));  // the lane's places are worked out here, not kept in registers
@@ -301,7 +321,7 @@ template <int D, int R, int U, int STEP> struct TileCopy {
         const int lo = __shfl((int)pl.row, r), hi = __shfl((int)(pl.row >> 32), r);
         const int64_t o = ((int64_t)hi << 32) | (uint32_t)lo;
         const int c = (lane % CH) ^ (IS_V ? swz_v<D>(row0 + r) : swz_k<D>(row0 + r));
-        copy16((hi < 0 ? (const uint8_t*)kZeroRow : head + o) + c * 16, dst + i * 1024);
+        copy16<NT>((hi < 0 ? (const uint8_t*)kZeroRow : head + o) + c * 16, dst + i * 1024);
       }
     }
   }

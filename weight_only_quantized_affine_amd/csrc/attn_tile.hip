@@ -167,7 +167,7 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
   const int late = wave / 4;  // the second four waves run one turn behind
   const bool copier = wave < 4;
   const int row0 = R * (wave & 3);  // first key of a tile that a copying wave copies
-  TileCopy<D, R, 1, BN> tc;
+  TileCopy<D, R, 1, BN, false> tc;
   tc.init(a, row0, lane);
   bool recorded = false;
   for (int u = u0; u < u1;) {
@@ -465,46 +465,105 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
   }
 }
 
-// Joins the pieces of the items that were cut: block (x, y) takes rows 16 y .. of record x.
+// Joins the pieces of the items that were cut.  A block takes `rows_cap` rows or 64 of them of one
+// record, 16 at a time; the threads of a row (4 values each) share its pieces out in as many lanes
+// as the block's 1024 threads allow, each a running maximum and sum, and the lanes join in LDS (one
+// sequence of 131071, 4 rows, 64 pieces of each: 33 us with one lane a row).
+constexpr int kJoinThreads = 1024;
 template <typename T, int D>
-__global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a, int first_rec, const float* part,
-                                                        int slot_floats, int rows_cap) {
-  constexpr int TPR = D / 4;        // threads of a row
-  constexpr int RPB = 256 / TPR;    // rows at once
-  const AttnRecord r = a.rec[first_rec + blockIdx.x];
+__global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const AttnArgs a) {
+  constexpr int TPR = D / 4;                  // threads of a row
+  constexpr int SLOTS = kJoinThreads / TPR;   // of a block
+  __shared__ f32x4_t sx[kJoinThreads];
+  __shared__ float sl[SLOTS], sm[SLOTS];
+  const int few_blocks = a.join_few ? a.nw_few : 0;
+  const bool is_few = (int)blockIdx.x < few_blocks;
+  constexpr int BM = 32 * attn_tile_waves(D);
+  const int b = blockIdx.x - few_blocks;
+  const int w = is_few ? blockIdx.x : b / (BM / 64);
+  const int row_begin = is_few ? 0 : b % (BM / 64) * 64;
+  const AttnRecord r = a.rec[is_few ? w : a.nw_few + w];
   if (r.pieces == 0) return;
-  const int c = threadIdx.x % TPR;
-  const int w = blockIdx.x;
-  for (int row = blockIdx.y * 16 + threadIdx.x / TPR; row < min(r.rows, (int)blockIdx.y * 16 + 16); row += RPB) {
-    auto slot = [&](int p) { return part + (int64_t)(p == 0 ? 2 * w + 1 : 2 * (w + p)) * slot_floats; };
-    float mt = kNegInf;
-#pragma unroll 4
-    for (int p = 0; p < r.pieces; ++p) mt = fmaxf(mt, slot(p)[row]);
-    float l = 0.f;
+  const int cap = is_few ? a.cap_few : BM;
+  const int slot_floats = is_few ? a.part_floats : BM * (D + 2);
+  const float* part = is_few ? a.part : a.part_tile;
+  const int row_end = min(r.rows, row_begin + 64);
+  const int c = threadIdx.x % TPR, slot = threadIdx.x / TPR;
+  auto piece = [&](int p) { return part + (int64_t)(p == 0 ? 2 * w + 1 : 2 * (w + p)) * slot_floats; };
+  int at_once = 1;  // rows side by side, a power of two
+  while (at_once < min(row_end - row_begin, min(16, SLOTS))) at_once *= 2;
+  const int lanes = SLOTS / at_once;
+  const int lane = slot % lanes;
+  for (int row0 = row_begin; row0 < row_end; row0 += at_once) {
+    const int row = row0 + slot / lanes;
+    float m = kNegInf, l = 0.f;
     f32x4_t x = {0, 0, 0, 0};
-#pragma unroll 4
-    for (int p = 0; p < r.pieces; ++p) {
-      const float* sp = slot(p);
-      const float lp = sp[rows_cap + row];
-      const float f = join_factor(sp[row], lp, mt);
-      const f32x4_t v = *(const f32x4_t*)(sp + 2 * rows_cap + row * D + 4 * c);
-      if (f != 0.f) {
-        l += lp * f;
-        x += v * f;
+    if (row < row_end) {
+      for (int p0 = lane; p0 < r.pieces; p0 += 4 * lanes) {
+        float mp[4], lp[4];
+        f32x4_t v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int p = p0 + i * lanes;
+          mp[i] = kNegInf;
+          lp[i] = 0.f;
+          v[i] = f32x4_t{0, 0, 0, 0};
+          if (p < r.pieces) {
+            const float* sp = piece(p);
+            mp[i] = sp[row];
+            lp[i] = sp[cap + row];
+            v[i] = *(const f32x4_t*)(sp + 2 * cap + row * D + 4 * c);
+          }
+        }
+        const float mn = max3(max3(mp[0], mp[1], mp[2]), mp[3], m);
+        const float f = m == kNegInf ? (l == 0.f ? 0.f : 1.f) : exp2_fast(m - mn);
+        l = f == 0.f ? 0.f : l * f;
+        for (int y = 0; y < 4; ++y) x[y] = f == 0.f ? 0.f : x[y] * f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float fp = join_factor(mp[i], lp[i], mn);
+          if (fp != 0.f) {
+            l += lp[i] * fp;
+            x += v[i] * fp;
+          }
+        }
+        m = mn;
       }
     }
-    const int rr = r.row0 + row;
-    const int tok = (int)a.g_div.div((uint32_t)rr);
-    const int hq = r.head * a.g + rr - tok * a.g;
-    float fo = 1.f;
-    if (a.sinks) {
-      const float s2 = a.sinks[hq] * kLog2e, mn = fmaxf(mt, s2);
-      fo = mt == kNegInf ? 0.f : exp2_fast(mt - mn);
-      l = l * fo + exp2_fast(s2 - mn);
+    if (lanes > 1) {
+      __syncthreads();
+      sx[threadIdx.x] = x;
+      if (c == 0) sl[slot] = l, sm[slot] = m;
+      __syncthreads();
+      if (lane == 0) {
+        float mt = m;
+        for (int i = 1; i < lanes; ++i) mt = fmaxf(mt, sm[slot + i]);
+        l = 0.f;
+        x = f32x4_t{0, 0, 0, 0};
+        for (int i = 0; i < lanes; ++i) {
+          const float li = sl[slot + i], f = join_factor(sm[slot + i], li, mt);
+          if (f != 0.f) {
+            l += li * f;
+            x += sx[threadIdx.x + i * TPR] * f;
+          }
+        }
+        m = mt;
+      }
     }
-    const float inv = l == 0.f ? 0.f : fo / l;
-    uint8_t* op = a.out + ((int64_t)(r.q0 + tok) * a.out_ts + (int64_t)hq * a.out_hs) + c * 8;
-    store4(T{}, op, x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+    if (lane == 0 && row < row_end) {
+      const int rr = r.row0 + row;
+      const int tok = (int)a.g_div.div((uint32_t)rr);
+      const int hq = r.head * a.g + rr - tok * a.g;
+      float fo = 1.f;
+      if (a.sinks) {
+        const float s2 = a.sinks[hq] * kLog2e, mn = fmaxf(m, s2);
+        fo = m == kNegInf ? (l == 0.f ? 0.f : 1.f) : exp2_fast(m - mn);
+        l = l * fo + exp2_fast(s2 - mn);
+      }
+      const float inv = l == 0.f ? 0.f : fo / l;
+      uint8_t* op = a.out + ((int64_t)(r.q0 + tok) * a.out_ts + (int64_t)hq * a.out_hs) + c * 8;
+      store4(T{}, op, x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
+    }
   }
 }
 
@@ -520,17 +579,11 @@ template <typename T, int D> hipError_t tile(const AttnArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 template <typename T, int D> hipError_t join(const AttnArgs& a, hipStream_t s) {
-  if (a.join_few) {
-    attn_join_kernel<T, D><<<dim3(a.nw_few, a.cap_few / 16), 256, 0, s>>>(a, 0, a.part, a.part_floats, a.cap_few);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  if (a.nw_tile > 0 && a.join_tile) {
-    constexpr int BM = 32 * attn_tile_waves(D);
-    attn_join_kernel<T, D><<<dim3(a.nw_tile, BM / 16), 256, 0, s>>>(a, a.nw_few, a.part_tile, BM * (D + 2), BM);
-    return hipGetLastError();
-  }
-  return hipSuccess;
+  const int few = a.join_few ? a.nw_few : 0;
+  const int many = a.nw_tile > 0 && a.join_tile ? a.nw_tile * (attn_tile_waves(D) / 2) : 0;
+  if (few + many == 0) return hipSuccess;
+  attn_join_kernel<T, D><<<few + many, kJoinThreads, 0, s>>>(a);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -557,8 +610,9 @@ AttnPlan attn_plan(int64_t t, int64_t n_seqs, int64_t hq, int64_t hk, int d, int
     const int64_t tiles = span / kAttnFewKeys + 2;
     const int64_t units = n_seqs * hk * tiles;
     p.ok = p.ok && units < limit;
-    // two resident workgroups a compute unit (their LDS), one at 256 values a head
-    p.nw_few = (int)std::min<int64_t>(d == 64 ? 1024 : d == 128 ? 512 : 256, units);
+    // two resident workgroups a compute unit, one at 256 values a head (their LDS; four at 64 values
+    // would fit, but the pieces cost more than they hide: 16 x 5 drafted tokens 34 against 28 us)
+    p.nw_few = (int)std::min<int64_t>(d == 256 ? 256 : 512, units);
     p.cap_few = 16 * p.nc;
     p.part_floats = p.cap_few * (d + 2);
     p.join_few = max_kv > kAttnFewKeys;  // a span inside one tile is never cut
