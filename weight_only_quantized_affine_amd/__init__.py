@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import threading
 from typing import Optional, Sequence
 
 __all__ = [
@@ -468,69 +469,97 @@ def qlinear_apply_experts_noalloc(fmt: int, w0, w1, ids, x, *, n: int, k: int, y
     return y
 
 
-def _ref(s):
-    return None if s is None else ctypes.addressof(s)
+# ---- attention side.  These calls are short enough for the marshalling to show: the argument
+# structures are kept, one set a thread, and messages are only put together for a refusal.
+class _Args(threading.local):
+    def __init__(self):
+        self.q, self.q_out, self.k, self.v = _Heads(), _Heads(), _Heads(), _Heads()
+        self.cache, self.nr = _PagedCache(), _NormRope()
+        self.at = {n: ctypes.addressof(getattr(self, n)) for n in ("q", "q_out", "k", "v", "cache", "nr")}
 
 
-def _need(ok, status: int, message: str):
-    if not ok:
-        raise QLError(status, message)
+_ARGS = _Args()
 
 
-def _one_gpu(*tensors):
-    """All given tensors are on one GPU."""
-    on = {t.device for t in tensors if t is not None}
-    _need(len(on) == 1 and next(iter(on)).type == "cuda", 2, f"every tensor must be on one GPU, not on {on}")
+def _heads(h: _Heads, x, name: str, t: int, d: int, dtype, device: int):
+    """Fill h from x [t, heads, d]."""
+    shape = x.shape
+    if len(shape) != 3 or shape[0] != t or shape[2] != d:
+        raise QLError(2, f"{name} must be [{t}, heads, {d}], not {list(shape)}")
+    if x.dtype is not dtype:
+        raise QLError(3, f"{name} must have dtype {dtype}, not {x.dtype}")
+    strides = x.stride()
+    if strides[2] != 1 and d > 1:
+        raise QLError(2, f"{name}'s last dimension must be contiguous")
+    _same_device(x, name, device)
+    h.p = x.data_ptr()
+    h.heads = shape[1]
+    # the stride of a dimension of one is free in torch: any legal value will do
+    h.token_stride = strides[0] if t > 1 else 0
+    h.head_stride = strides[1] if shape[1] > 1 else 0
 
 
-def _dense(t, name: str, dtype, shape=None):
-    """A contiguous tensor argument of the given dtype and shape, or None."""
-    if t is not None:
-        _need(t.dtype == dtype, 3, f"{name} must have dtype {dtype}")
-        _need(shape is None or tuple(t.shape) == tuple(shape), 2, f"{name} must have shape {tuple(shape or ())}")
-        _need(t.is_contiguous(), 2, f"{name} must be contiguous")
-    return t
+def _same_device(x, name: str, device: int):
+    if x.get_device() != device:
+        raise QLError(2, f"every tensor must be on one GPU: {name} is on {x.device}")
 
 
-def _heads(x, name: str, like=None):
-    """The ql_heads of a [t, heads, d] tensor (None: absent)."""
+def _array(x, name: str, dtype, shape, device: int):
+    """Pointer of a contiguous tensor of the given dtype and shape (None: None)."""
     if x is None:
         return None
-    _need(x.dim() == 3, 2, f"{name} must be [tokens, heads, d]")
-    _need(x.stride(2) == 1 or x.shape[2] <= 1, 2, f"{name}'s last dimension must be contiguous")
-    if like is not None:
-        _need(x.shape[0] == like.shape[0] and x.shape[2] == like.shape[2], 2,
-              f"{name} must have the tokens and the head size of the other tensors")
-        _need(x.dtype == like.dtype, 3, f"{name} must have dtype {like.dtype}")
-    # the stride of a dimension of one is free in torch: any legal value will do
-    ts = x.stride(0) if x.shape[0] > 1 else 0
-    hs = x.stride(1) if x.shape[1] > 1 else 0
-    return _Heads(_ptr(x), x.shape[1], ts, hs)
+    if x.dtype is not dtype:
+        raise QLError(3, f"{name} must have dtype {dtype}, not {x.dtype}")
+    if x.shape != shape or not x.is_contiguous():
+        raise QLError(2, f"{name} must be contiguous of shape {list(shape)}, not {list(x.shape)}")
+    _same_device(x, name, device)
+    return x.data_ptr()
 
 
-def _paged_cache(k_cache, v_cache):
-    _need(k_cache.dim() == 4 and k_cache.shape == v_cache.shape, 2,
-          "k_cache and v_cache must both be [n_pages, page_size, heads, d]")
-    _need(k_cache.dtype == v_cache.dtype, 3, "k_cache and v_cache must have one dtype")
-    size = [k_cache.size(i) for i in range(4)]
-    sk, sv = ([c.stride(i) if size[i] > 1 else 0 for i in range(3)] for c in (k_cache, v_cache))
-    _need(sk == sv, 2, "k_cache and v_cache must have the same strides")
-    _need(size[3] <= 1 or (k_cache.stride(3) == 1 and v_cache.stride(3) == 1), 2,
-          "the caches' last dimension must be contiguous")
-    return _PagedCache(_ptr(k_cache), _ptr(v_cache), *size, sk[0], sk[1], sk[2])
+def _paged_cache(c: _PagedCache, k_cache, v_cache, d: int, dtype, device: int):
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape or shape[3] != d:
+        raise QLError(2, f"k_cache and v_cache must both be [n_pages, page_size, heads, {d}]")
+    if k_cache.dtype is not dtype or v_cache.dtype is not dtype:
+        raise QLError(3, f"the caches must have dtype {dtype}")
+    sk, sv = k_cache.stride(), v_cache.stride()
+    if sk != sv and any(a != b for a, b, n in zip(sk, sv, shape) if n > 1):
+        raise QLError(2, "k_cache and v_cache must have the same strides")
+    if d > 1 and (sk[3] != 1 or sv[3] != 1):
+        raise QLError(2, "the caches' last dimension must be contiguous")
+    _same_device(k_cache, "k_cache", device)
+    _same_device(v_cache, "v_cache", device)
+    c.k, c.v = k_cache.data_ptr(), v_cache.data_ptr()
+    c.n_pages, c.page_size, c.hk, c.d = shape
+    c.page_stride = sk[0] if shape[0] > 1 else 0
+    c.token_stride = sk[1] if shape[1] > 1 else 0
+    c.head_stride = sk[2] if shape[2] > 1 else 0
 
 
-def _norm_rope(d, t, q_weight, k_weight, eps, positions, cos_sin, interleaved):
+def _norm_rope(n: _NormRope, t: int, d: int, q_weight, k_weight, eps, positions, cos_sin, interleaved, device: int):
     torch = _torch()
     w = q_weight if q_weight is not None else k_weight
-    for name, x in (("q_weight", q_weight), ("k_weight", k_weight)):
-        _dense(x, name, w.dtype if w is not None else None, (d,))
-    _dense(positions, "positions", torch.int64, (t,))
-    _dense(cos_sin, "cos_sin", torch.float32)
-    _need(cos_sin is None or cos_sin.dim() == 2, 2, "cos_sin must be [positions, rotated values]")
-    rows, rot = (0, 0) if cos_sin is None else cos_sin.shape
-    return _NormRope(_ptr(q_weight), _ptr(k_weight), _dt(w) if w is not None else _QL_F32, eps, _ptr(positions),
-                     _ptr(cos_sin), rows, rot, 1 if interleaved else 0)
+    if w is not None:
+        n.w_dtype = _dt(w)
+    n.q_weight = _array(q_weight, "q_weight", w.dtype if w is not None else None, (d,), device)
+    n.k_weight = _array(k_weight, "k_weight", w.dtype if w is not None else None, (d,), device)
+    n.eps = eps
+    n.positions = _array(positions, "positions", torch.int64, (t,), device)
+    if cos_sin is None:
+        n.cos_sin, n.max_pos, n.rot = None, 0, 0
+    else:
+        shape = cos_sin.shape
+        if len(shape) != 2:
+            raise QLError(2, "cos_sin must be [positions, rotated values]")
+        n.cos_sin = _array(cos_sin, "cos_sin", torch.float32, shape, device)
+        n.max_pos, n.rot = shape
+    n.interleaved = 1 if interleaved else 0
+
+
+def _stream_on(device: int) -> int:
+    if device < 0:
+        raise QLError(2, "every tensor must be on one GPU, not in host memory")
+    return _torch()._C._cuda_getCurrentRawStream(device)
 
 
 def qlinear_qk_norm_rope(q, k, *, q_weight=None, k_weight=None, eps: float = 1e-6, positions=None, cos_sin=None,
@@ -541,16 +570,26 @@ def qlinear_qk_norm_rope(q, k, *, q_weight=None, k_weight=None, eps: float = 1e-
     torch = _torch()
     lib = load_library()
     x = q if q is not None else k
-    _need(x is not None, 1, "q and k must not both be None")
+    if x is None or x.dim() != 3:
+        raise QLError(2, "q or k must be given, [tokens, heads, d]")
     t, _, d = x.shape
-    if q is not None and q_out is None:
-        q_out = torch.empty(tuple(q.shape), dtype=q.dtype, device=q.device)
-    if k is not None and k_out is None:
-        k_out = torch.empty(tuple(k.shape), dtype=k.dtype, device=k.device)
-    hq, hqo, hk, hko = (_heads(a, n, x) for a, n in ((q, "q"), (q_out, "q_out"), (k, "k"), (k_out, "k_out")))
-    nr = _norm_rope(d, t, q_weight, k_weight, eps, positions, cos_sin, interleaved)
-    _one_gpu(q, q_out, k, k_out, q_weight, k_weight, positions, cos_sin)
-    _check(lib.qlinear_qk_norm_rope(_ref(hq), _ref(hqo), _ref(hk), _ref(hko), _dt(x), t, d, _ref(nr), _stream()))
+    dtype, device, args = x.dtype, x.get_device(), _ARGS
+    at = args.at
+    if q is not None:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
+        _heads(args.q, q, "q", t, d, dtype, device)
+        _heads(args.q_out, q_out, "q_out", t, d, dtype, device)
+    if k is not None:
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=dtype, device=k.device)
+        _heads(args.k, k, "k", t, d, dtype, device)
+        _heads(args.v, k_out, "k_out", t, d, dtype, device)
+    _norm_rope(args.nr, t, d, q_weight, k_weight, eps, positions, cos_sin, interleaved, device)
+    status = lib.qlinear_qk_norm_rope(at["q"] if q is not None else None, at["q_out"], at["k"] if k is not None else None,
+                                      at["v"], _dt(dtype), t, d, at["nr"], _stream_on(device))
+    if status:
+        _check(status)
     return q_out, k_out
 
 
@@ -562,20 +601,26 @@ def qlinear_kv_append(k, v, k_cache, v_cache, slots, *, q=None, q_out=None, q_we
     -> q_out (None without q)."""
     torch = _torch()
     lib = load_library()
+    if k.dim() != 3:
+        raise QLError(2, "k must be [tokens, heads, d]")
     t, _, d = k.shape
-    if q is not None and q_out is None:
-        q_out = torch.empty(tuple(q.shape), dtype=q.dtype, device=q.device)
-    cache = _paged_cache(k_cache, v_cache)
-    _need(k_cache.dtype == k.dtype, 3, f"the caches must have dtype {k.dtype}")
-    _need(cache.d == d, 2, f"the caches must have head size {d}")
-    hq, hqo, hk, hv = (_heads(a, n, k) for a, n in ((q, "q"), (q_out if q is not None else None, "q_out"), (k, "k"),
-                                                    (v, "v")))
-    _dense(slots, "slots", torch.int64, (t,))
-    nr = _norm_rope(d, t, q_weight, k_weight, eps, positions, cos_sin, interleaved)
-    _one_gpu(q, q_out, k, v, k_cache, v_cache, slots, q_weight, k_weight, positions, cos_sin)
-    _check(lib.qlinear_kv_append(_ref(hq), _ref(hqo), _ref(hk), _ref(hv), _ref(cache), _ptr(slots), _dt(k), t, _ref(nr),
-                                 _stream()))
-    return q_out
+    dtype, device, args = k.dtype, k.get_device(), _ARGS
+    at = args.at
+    if q is not None:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
+        _heads(args.q, q, "q", t, d, dtype, device)
+        _heads(args.q_out, q_out, "q_out", t, d, dtype, device)
+    _heads(args.k, k, "k", t, d, dtype, device)
+    _heads(args.v, v, "v", t, d, dtype, device)
+    _paged_cache(args.cache, k_cache, v_cache, d, dtype, device)
+    slots_at = _array(slots, "slots", torch.int64, (t,), device)
+    _norm_rope(args.nr, t, d, q_weight, k_weight, eps, positions, cos_sin, interleaved, device)
+    status = lib.qlinear_kv_append(at["q"] if q is not None else None, at["q_out"], at["k"], at["v"], at["cache"],
+                                   slots_at, _dt(dtype), t, at["nr"], _stream_on(device))
+    if status:
+        _check(status)
+    return q_out if q is not None else None
 
 
 def qlinear_paged_attention_workspace_size(q, k_cache, block_table, *, max_q: int, window: int = 0) -> int:
@@ -593,26 +638,36 @@ def qlinear_paged_attention(q, k_cache, v_cache, block_table, cu_q, kv_lens, *, 
     query sees its last `window` positions; sinks fp32 [hq].  -> out [t, hq, d]."""
     torch = _torch()
     lib = load_library()
+    if q.dim() != 3:
+        raise QLError(2, "q must be [tokens, heads, d]")
     t, hq, d = q.shape
+    dtype, device, args = q.dtype, q.get_device(), _ARGS
+    at = args.at
     if out is None:
-        out = torch.empty(tuple(q.shape), dtype=q.dtype, device=q.device)
-    cache = _paged_cache(k_cache, v_cache)
-    _need(k_cache.dtype == q.dtype, 3, f"the caches must have dtype {q.dtype}")
-    _need(cache.d == d, 2, f"the caches must have head size {d}")
-    _need(block_table.dim() == 2 and block_table.dtype == torch.int32, 3, "block_table must be int32 [n_seqs, max_pages]")
+        out = torch.empty((t, hq, d), dtype=dtype, device=q.device)
+    _heads(args.q, q, "q", t, d, dtype, device)
+    _heads(args.q_out, out, "out", t, d, dtype, device)
+    _paged_cache(args.cache, k_cache, v_cache, d, dtype, device)
+    if block_table.dim() != 2 or block_table.dtype is not torch.int32:
+        raise QLError(3, "block_table must be int32 [n_seqs, max_pages]")
     n_seqs, max_pages = block_table.shape
-    _need(max_pages <= 1 or block_table.stride(1) == 1, 2, "block_table's rows must be contiguous")
-    _dense(cu_q, "cu_q", torch.int32, (n_seqs + 1,))
-    _dense(kv_lens, "kv_lens", torch.int32, (n_seqs,))
-    _dense(sinks, "sinks", torch.float32, (hq,))
-    hqs, hout = _heads(q, "q"), _heads(out, "out", q)
+    row, place = block_table.stride()
+    if place != 1 and max_pages > 1:
+        raise QLError(2, "block_table's rows must be contiguous")
+    _same_device(block_table, "block_table", device)
+    cu_at = _array(cu_q, "cu_q", torch.int32, (n_seqs + 1,), device)
+    lens_at = _array(kv_lens, "kv_lens", torch.int32, (n_seqs,), device)
+    sinks_at = _array(sinks, "sinks", torch.float32, (hq,), device)
     if workspace is None:
         need = qlinear_paged_attention_workspace_size(q, k_cache, block_table, max_q=max_q, window=window)
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    _one_gpu(q, out, k_cache, v_cache, block_table, cu_q, kv_lens, sinks, workspace)
-    _check(lib.qlinear_paged_attention(_ref(hqs), _ref(hout), _dt(q), t, _ref(cache), _ptr(block_table),
-                                       block_table.stride(0) if n_seqs > 1 else max_pages, max_pages, _ptr(cu_q),
-                                       _ptr(kv_lens), n_seqs, max_q, d ** -0.5 if scale is None else scale, window,
-                                       _ptr(sinks), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                       _stream()))
+    elif not workspace.is_contiguous():
+        raise QLError(2, "workspace must be contiguous")
+    _same_device(workspace, "workspace", device)
+    status = lib.qlinear_paged_attention(at["q"], at["q_out"], _dt(dtype), t, at["cache"], block_table.data_ptr(),
+                                         row if n_seqs > 1 else max_pages, max_pages, cu_at, lens_at, n_seqs, max_q,
+                                         d ** -0.5 if scale is None else scale, window, sinks_at, workspace.data_ptr(),
+                                         workspace.nbytes, _stream_on(device))
+    if status:
+        _check(status)
     return out

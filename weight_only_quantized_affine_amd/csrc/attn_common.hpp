@@ -18,7 +18,6 @@ namespace ql {
 typedef __attribute__((address_space(3))) void at_lds_void;
 typedef __attribute__((ext_vector_type(4))) short s16x4_t;
 typedef __attribute__((address_space(3))) s16x4_t at_lds_s16x4;
-typedef __attribute__((ext_vector_type(2))) float f32x2_t;
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNegInf = -__builtin_inff();
@@ -42,13 +41,6 @@ __device__ __forceinline__ f32x16_t mfma32(BF16, u32x4_t a, u32x4_t b, f32x16_t 
 __device__ __forceinline__ f32x16_t mfma32(F16, u32x4_t a, u32x4_t b, f32x16_t c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0,
                                                 0, 0);
-}
-// Two fp32 values rounded to nearest even into one word.
-__device__ __forceinline__ uint32_t pack2(BF16, float a, float b) {
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
-}
-__device__ __forceinline__ uint32_t pack2(F16, float a, float b) {
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, f16x2_t));
 }
 // acc plus the two 16-bit values of a word.
 __device__ __forceinline__ float add2(BF16, uint32_t w, float acc) { return dot2(BF16{}, w, 0x3f803f80u, acc); }

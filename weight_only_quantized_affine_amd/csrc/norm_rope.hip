@@ -6,7 +6,7 @@
 // interleaved.
 //
 // Bound by memory at many tokens (each row is read and written once) and by the launch at few.  A
-// group of lanes with 8 values each holds a row (16 lanes at d = 128) and takes kRows heads of one
+// group of lanes with 8 values each holds a row (16 lanes at d = 128) and takes ROWS heads of one
 // token: their loads are in flight together and the token's table values are read once for all of
 // them.  The mean is a reduction by DPP within 16 lanes, and a value's partner lies in a lane
 // rot/16 further in its group.
@@ -15,8 +15,6 @@
 
 namespace ql {
 namespace {
-
-constexpr int kRows = 4;
 
 // x + x of the lane that DPP control CTRL names (within 16 lanes).
 template <int CTRL> __device__ __forceinline__ float add_dpp(float x) {
@@ -54,7 +52,7 @@ __device__ __forceinline__ void weights8(const void* w, int wdt, int c, float* f
   }
 }
 
-template <typename T, int L>
+template <typename T, int L, int ROWS>
 __global__ __launch_bounds__(256) void norm_rope_kernel(const NormRopeArgs a, FastDiv per_token, int groups,
                                                         int64_t units) {
   const int lane = threadIdx.x & 63;
@@ -62,7 +60,7 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(const NormRopeArgs a, Fa
   const int64_t unit = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
   if (unit >= units) return;  // whole groups of lanes
   const int64_t tok = (int64_t)per_token.div((uint32_t)unit);
-  const int h0 = (int)(unit - tok * groups) * kRows;
+  const int h0 = (int)(unit - tok * groups) * ROWS;
   const int heads = a.hq + a.hk + a.hv;
   const bool on = 8 * c < a.d;
 
@@ -76,9 +74,9 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(const NormRopeArgs a, Fa
     }
   }
   // loads of every row first
-  u32x4_t x[kRows];
+  u32x4_t x[ROWS];
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
+  for (int i = 0; i < ROWS; ++i) {
     const int h = h0 + i;
     x[i] = u32x4_t{0, 0, 0, 0};
     if (h < heads && on) {
@@ -89,7 +87,7 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(const NormRopeArgs a, Fa
     }
   }
   // the token's cosines and sines for this lane's values
-  float cs[8], sn[8];
+  float cs[8] = {}, sn[8] = {};
   bool known = true;
   const bool turned = 8 * c < a.rot;
   const int half = a.rot / 16;  // lanes between the two values of a pair
@@ -108,28 +106,35 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(const NormRopeArgs a, Fa
         const int b = 2 * (second ? c - half : c);
         const f32x4_t u0 = row[b], u1 = row[b + 1], v0 = row[n + b], v1 = row[n + b + 1];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) cs[i] = u0[i], cs[4 + i] = u1[i], sn[i] = v0[i], sn[4 + i] = v1[i];
+        for (int i = 0; i < 4; ++i) {
+          cs[i] = u0[i], cs[4 + i] = u1[i];
+          sn[i] = second ? v0[i] : -v0[i], sn[4 + i] = second ? v1[i] : -v1[i];
+        }
       }
     }
   }
+  float w[8];
+  const void* loaded = nullptr;
+  const float inv_d = 1.0f / (float)a.d;
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
+  for (int i = 0; i < ROWS; ++i) {
     const int h = h0 + i;
     const bool is_q = h < a.hq, is_v = h >= a.hq + a.hk;
-    const void* wp = is_q ? a.q_weight : a.k_weight;
-    float f[8], w[8];
+    const void* wp = is_q ? a.q_weight : is_v ? nullptr : a.k_weight;
+    float f[8];
     unpack8<T>(x[i], f);
     if (wp) {
       float ss = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) ss = __builtin_fmaf(f[j], f[j], ss);
       ss = group_sum<L>(ss);
-      const float r = 1.0f / __builtin_sqrtf(ss / (float)a.d + a.eps);
-      if (on) {
-        weights8(wp, a.wdt, c, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = f[j] * r * w[j];
+      const float r = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, inv_d, a.eps));
+      if (wp != loaded) {  // most heads share the weights of the one before
+        if (on) weights8(wp, a.wdt, c, w);
+        loaded = wp;
       }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = f[j] * r * w[j];
     }
     if (a.rot > 0) {
       float y[8];
@@ -140,12 +145,19 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(const NormRopeArgs a, Fa
           y[j + 1] = f[j + 1] * cs[j] + f[j] * sn[j];
         }
       } else {
-        const int from = (lane & ~(L - 1)) | ((second ? c - half : c + half) & (L - 1));
+        float o[8];
+        if (L == 16 && half == 8) {  // the other half of the row: a rotation of 16 lanes by 8
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float o = __shfl(f[j], from);
-          y[j] = second ? f[j] * cs[j] + o * sn[j] : f[j] * cs[j] - o * sn[j];
+          for (int j = 0; j < 8; ++j)
+            o[j] = __builtin_bit_cast(
+                float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, f[j]), 0x128, 0xf, 0xf, false));
+        } else {
+          const int from = (lane & ~(L - 1)) | ((second ? c - half : c + half) & (L - 1));
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o[j] = __shfl(f[j], from);
         }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = f[j] * cs[j] + o[j] * sn[j];  // sn holds the sign
       }
       if (turned) {
 #pragma unroll
@@ -156,7 +168,7 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(const NormRopeArgs a, Fa
     u32x4_t o = x[i];
     if (!is_v) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] = known ? f32_to_bits<T>(f[2 * j]) | f32_to_bits<T>(f[2 * j + 1]) << 16 : 0u;
+      for (int j = 0; j < 4; ++j) o[j] = known ? pack2(T{}, f[2 * j], f[2 * j + 1]) : 0u;
     }
     uint8_t* p;
     if (is_q) {
@@ -171,16 +183,28 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(const NormRopeArgs a, Fa
         p += tok * a.ko_ts;
       }
     }
-    *(u32x4_t*)(p + 16 * c) = o;
+    if (ROWS > 1)
+      __builtin_nontemporal_store(o, (u32x4_t*)(p + 16 * c));
+    else
+      *(u32x4_t*)(p + 16 * c) = o;
   }
 }
 
-template <typename T, int L> hipError_t run(const NormRopeArgs& a, hipStream_t s) {
-  const int groups = (a.hq + a.hk + a.hv + kRows - 1) / kRows;
+template <typename T, int L, int ROWS> hipError_t run_rows(const NormRopeArgs& a, hipStream_t s) {
+  const int groups = (a.hq + a.hk + a.hv + ROWS - 1) / ROWS;
   const int64_t units = a.t * groups;
   const unsigned grid = (unsigned)((units + 256 / L - 1) / (256 / L));
-  norm_rope_kernel<T, L><<<grid, 256, 0, s>>>(a, fast_div((uint32_t)groups), groups, units);
+  norm_rope_kernel<T, L, ROWS><<<grid, 256, 0, s>>>(a, fast_div((uint32_t)groups), groups, units);
   return hipGetLastError();
+}
+template <typename T, int L> hipError_t run(const NormRopeArgs& a, hipStream_t s) {
+  // Waves when each lane holds one row: below 16 a compute unit the launch's latency counts and one
+  // row a lane is shortest (1, 2, 4 rows: 1 token x 40 rows of 128 2.9, 3.3, 4.2 us; 256 tokens 3.6,
+  // 3.9, 4.8); from 64 on the rows in flight count (512 tokens 4.9, 4.5, 5.3; 1024 8.5, 6.2, 6.8;
+  // 2048 12.5, 10.8, 10.0; 4096 21.3, 17.6, 17.0).  Outputs of that size pass the caches on the way
+  // to memory (non-temporal stores, 8192 tokens: 41 -> 35 us; what reads them next is not slower).
+  const int64_t waves = a.t * (a.hq + a.hk + a.hv) * L / 64;
+  return waves < 4096 ? run_rows<T, L, 1>(a, s) : waves < 16384 ? run_rows<T, L, 2>(a, s) : run_rows<T, L, 4>(a, s);
 }
 template <typename T> hipError_t run_l(const NormRopeArgs& a, hipStream_t s) {
   const int n = a.d / 8;
