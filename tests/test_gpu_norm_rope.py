@@ -188,3 +188,28 @@ def test_append_in_a_graph_and_on_another_stream():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(caches, eager))
+
+
+@pytest.mark.parametrize("t,hq,hk,d,dtype,inter", [(900, 21, 5, 128, BF, False), (3000, 21, 5, 128, HF, True),
+                                                   (3000, 13, 3, 256, BF, False), (5000, 26, 5, 64, BF, False)])
+def test_large_launches_match_small_ones(t, hq, hk, d, dtype, inter):
+    """Every number of rows a lane holds: bit for bit what calls of a few tokens give, which the oracle checks."""
+    g = torch.Generator().manual_seed(t + d)
+    page, n_pages = 16, t // 16 + 3
+    x, w, cs = randn(g, t, hq + 2 * hk, d, dtype=dtype), [randn(g, d, dtype=dtype) for _ in range(2)], table(6000, d // 2)
+    pos = torch.arange(t, device=DEV)
+    slots = torch.randperm(n_pages * page, generator=g)[:t].to(DEV)
+    caches = [[torch.zeros(n_pages, page, hk, d, dtype=dtype, device=DEV) for _ in range(2)] for _ in range(2)]
+    outs = [torch.empty(t, hq, d, dtype=dtype, device=DEV) for _ in range(3)]
+    k_out = torch.empty(t, hk, d, dtype=dtype, device=DEV)
+    for c, out, step in ((caches[0], outs[0], t), (caches[1], outs[1], 37)):
+        for i in range(0, t, step):
+            j = slice(i, i + step)
+            q.qlinear_kv_append(x[j, hq:hq + hk], x[j, hq + hk:], *c, slots[j], q=x[j, :hq], q_out=out[j], q_weight=w[0],
+                                k_weight=w[1], positions=pos[j], cos_sin=cs, interleaved=inter)
+    assert torch.equal(outs[0], outs[1])
+    assert all(torch.equal(a, b) for a, b in zip(*caches))
+    q.qlinear_qk_norm_rope(x[:, :hq], x[:, hq:hq + hk], q_weight=w[0], k_weight=w[1], positions=pos, cos_sin=cs,
+                           interleaved=inter, q_out=outs[2], k_out=k_out)
+    assert torch.equal(outs[2], outs[1])
+    assert torch.equal(caches[1][0].view(-1, hk, d)[slots], k_out)
