@@ -465,37 +465,33 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
   }
 }
 
-// Joins the pieces of the items that were cut.  A block takes `rows_cap` rows or 64 of them of one
-// record, 16 at a time; the threads of a row (4 values each) share its pieces out in as many lanes
-// as the block's 1024 threads allow, each a running maximum and sum, and the lanes join in LDS (one
-// sequence of 131071, 4 rows, 64 pieces of each: 33 us with one lane a row).
-constexpr int kJoinThreads = 1024;
+// Joins the pieces of the items that were cut.  The threads of a row hold 4 values each; a block has
+// room for SLOTS rows, or for fewer whose pieces are shared out to `lanes` of them: each lane keeps
+// a running maximum and sum over its pieces, four loads in flight, and the lanes join in LDS.  The
+// host sets lanes from the pieces an item has on average (one sequence of 131071, 4 rows of 64
+// pieces: 33 us with one lane; 12 mixed sequences, 256-row items of 3 pieces: 25 us with two).
+constexpr int kJoinThreads = 256;
+template <int D> constexpr int join_slots() { return kJoinThreads / (D / 4); }
 template <typename T, int D>
-__global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const AttnArgs a) {
-  constexpr int TPR = D / 4;                  // threads of a row
-  constexpr int SLOTS = kJoinThreads / TPR;   // of a block
+__global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const AttnArgs a, int few_blocks, int few_per,
+                                                                 int few_lanes, int tile_per, int tile_lanes) {
+  constexpr int TPR = D / 4, SLOTS = join_slots<D>(), BM = 32 * attn_tile_waves(D);
   __shared__ f32x4_t sx[kJoinThreads];
   __shared__ float sl[SLOTS], sm[SLOTS];
-  const int few_blocks = a.join_few ? a.nw_few : 0;
   const bool is_few = (int)blockIdx.x < few_blocks;
-  constexpr int BM = 32 * attn_tile_waves(D);
-  const int b = blockIdx.x - few_blocks;
-  const int w = is_few ? blockIdx.x : b / (BM / 64);
-  const int row_begin = is_few ? 0 : b % (BM / 64) * 64;
+  const int b = is_few ? blockIdx.x : blockIdx.x - few_blocks;
+  const int per = is_few ? few_per : tile_per, lanes = is_few ? few_lanes : tile_lanes;
+  const int w = b / per;
   const AttnRecord r = a.rec[is_few ? w : a.nw_few + w];
-  if (r.pieces == 0) return;
+  const int row0 = b % per * (SLOTS / lanes);
+  if (r.pieces == 0 || row0 >= r.rows) return;
   const int cap = is_few ? a.cap_few : BM;
   const int slot_floats = is_few ? a.part_floats : BM * (D + 2);
   const float* part = is_few ? a.part : a.part_tile;
-  const int row_end = min(r.rows, row_begin + 64);
   const int c = threadIdx.x % TPR, slot = threadIdx.x / TPR;
+  const int lane = slot & (lanes - 1), row = row0 + slot / lanes, row_end = r.rows;
   auto piece = [&](int p) { return part + (int64_t)(p == 0 ? 2 * w + 1 : 2 * (w + p)) * slot_floats; };
-  int at_once = 1;  // rows side by side, a power of two
-  while (at_once < min(row_end - row_begin, min(16, SLOTS))) at_once *= 2;
-  const int lanes = SLOTS / at_once;
-  const int lane = slot % lanes;
-  for (int row0 = row_begin; row0 < row_end; row0 += at_once) {
-    const int row = row0 + slot / lanes;
+  {
     float m = kNegInf, l = 0.f;
     f32x4_t x = {0, 0, 0, 0};
     if (row < row_end) {
@@ -579,10 +575,27 @@ template <typename T, int D> hipError_t tile(const AttnArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 template <typename T, int D> hipError_t join(const AttnArgs& a, hipStream_t s) {
-  const int few = a.join_few ? a.nw_few : 0;
-  const int many = a.nw_tile > 0 && a.join_tile ? a.nw_tile * (attn_tile_waves(D) / 2) : 0;
+  constexpr int SLOTS = join_slots<D>(), BM = 32 * attn_tile_waves(D);
+  // pieces of an item, on average, at four a lane
+  auto lanes_for = [](int64_t workgroups, int64_t items) {
+    int n = 1;
+    while (n < SLOTS && 4 * n * items < workgroups) n *= 2;
+    return n;
+  };
+  int few = 0, few_per = 1, few_lanes = 1, many = 0, tile_per = 1, tile_lanes = 1;
+  if (a.join_few) {
+    few_lanes = lanes_for(a.nw_few, (int64_t)a.n_seqs * a.hk);
+    const int rows = (int)std::min<int64_t>(a.cap_few, (int64_t)a.max_q * a.g);
+    few_per = (rows * few_lanes + SLOTS - 1) / SLOTS;
+    few = a.nw_few * few_per;
+  }
+  if (a.nw_tile > 0 && a.join_tile) {
+    tile_lanes = lanes_for(a.nw_tile, (int64_t)a.plan_tiles * a.hk);
+    tile_per = BM * tile_lanes / SLOTS;
+    many = a.nw_tile * tile_per;
+  }
   if (few + many == 0) return hipSuccess;
-  attn_join_kernel<T, D><<<few + many, kJoinThreads, 0, s>>>(a);
+  attn_join_kernel<T, D><<<few + many, kJoinThreads, 0, s>>>(a, few, few_per, few_lanes, tile_per, tile_lanes);
   return hipGetLastError();
 }
 
