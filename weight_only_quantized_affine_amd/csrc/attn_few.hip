@@ -105,10 +105,11 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few_kernel(const A
     attn_span(a, q, 0, q.nq - 1, lo, hi);
     return attn_tiles<128>(lo, hi, first) * a.hk;
   };
-  int W = 0;
+  int W = 0, mine = 0, before = 0;  // the thread's own sequence tid: its units and those before it
   for (int s0 = 0; s0 < a.n_seqs; s0 += 256) {
     int total;
-    block_scan<4>(cost(s0 + tid), ssh, total);
+    const int c = cost(s0 + tid), e = block_scan<4>(c, ssh, total);
+    if (s0 == 0) mine = c, before = e;
     W += total;
   }
   const int nw = min(a.nw_few, W);
@@ -120,20 +121,22 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few_kernel(const A
     return;
   }
   const int u0 = attn_cut(w, nw, W), u1 = attn_cut(w + 1, nw, W);
-  int s = 0, base = 0;  // sequence of unit u0 and its first unit
-  {
-    int before = 0;
-    for (int s0 = 0; s0 < a.n_seqs; s0 += 256) {
+  // sequence of unit u0 and its first unit; beyond 256 sequences the scan is run again
+  for (int s0 = 0, sum = 0; s0 < a.n_seqs && sum <= u0; s0 += 256) {
+    if (s0 > 0) {
       int total;
-      const int c = cost(s0 + tid);
-      const int e = before + block_scan<4>(c, ssh, total);
-      if (e <= u0 && u0 < e + c) sfound[0] = s0 + tid, sfound[1] = e;
-      before += total;
-      if (before > u0) break;
+      mine = cost(s0 + tid);
+      before = sum + block_scan<4>(mine, ssh, total);
+      sum += total;
+    } else if (a.n_seqs > 256) {
+      int total;
+      block_scan<4>(mine, ssh, total);
+      sum += total;
     }
-    __syncthreads();
-    s = sfound[0], base = sfound[1];
+    if (before <= u0 && u0 < before + mine) sfound[0] = s0 + tid, sfound[1] = before;
   }
+  __syncthreads();
+  int s = sfound[0], base = sfound[1];
 
   uint8_t* sk = sm + wave * 2 * TILE;
   uint8_t* sv = sk + TILE;
@@ -144,10 +147,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few_kernel(const A
     const AttnSeq q = attn_seq(a, s);
     int lo, hi, first;
     attn_span(a, q, 0, q.nq - 1, lo, hi);
-    const bool mine = q.nq >= 1 && attn_is_few(a, q.nq);
+    const bool ours = q.nq >= 1 && attn_is_few(a, q.nq);
     const int nt = attn_tiles<128>(lo, hi, first);
-    if (!mine || u >= base + nt * a.hk) {  // on to the next sequence
-      if (mine) base += nt * a.hk;
+    if (!ours || u >= base + nt * a.hk) {  // on to the next sequence
+      if (ours) base += nt * a.hk;
       ++s;
       continue;
     }
