@@ -26,6 +26,10 @@ constexpr int BN = kAttnTileKeys;
 // LDS fragments read ahead of the products that take them: a product lasts 32 cycles, a read about
 // four of them.  The order is pinned, since the compiler puts each read right before its product.
 constexpr int kAhead = 4;
+// An item's start and end, and its pieces' way through memory, cost as much as several of its key
+// tiles (10 against 2 us): in the division of the work each item has units for them before its first
+// tile (0, 4, 8, 12 units: 12 mixed sequences 147, 144, 141, 144 us; 8 x 500 tokens 73, 68, 58, 57).
+constexpr int kItemUnits = 8;
 
 // Stages of K and of V: three let a copy take four turns, which the fabric needs under load (two:
 // 582 against ... us); 256 values a head leave room for two.
@@ -137,7 +141,7 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
           if (seq_first[m] <= ti) b = m; else e = m;
         }
         int lo, hi, first;
-        c = tile_cost<BM>(a, attn_seq(a, b), ti - seq_first[b], lo, hi, first);
+        c = kItemUnits + tile_cost<BM>(a, attn_seq(a, b), ti - seq_first[b], lo, hi, first);
       }
       int total;
       const int e = block_scan<WAVES>(c, ssh, total);
@@ -183,9 +187,12 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
         if (plan[m] <= uh) b = m; else e = m;
       }
       const int ti = b;
-      nt = plan[ti + 1] - plan[ti];
-      ta = uh - plan[ti];
-      item0 = head * units + plan[ti];
+      nt = plan[ti + 1] - plan[ti] - kItemUnits;
+      item0 = head * units + plan[ti] + kItemUnits;  // the item's tiles are the units [item0, item0 + nt)
+      ta = max(0, u - item0);
+      tb = min(nt, u1 - item0);
+      u = item0 + nt;
+      if (tb <= ta) continue;  // the run ends before the item's first tile
       b = 0, e = a.n_seqs;
       while (e - b > 1) {
         const int m = (b + e) / 2;
@@ -196,8 +203,6 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
       head = __builtin_amdgcn_readfirstlane(head);
       q = attn_seq(a, s);
       tile_cost<BM>(a, q, j, lo, hi, first);
-      tb = min(nt, u1 - item0);
-      u = item0 + tb;
     } else {
       head = u % a.hk;
       const int target = u / a.hk;
@@ -620,7 +625,7 @@ AttnPlan attn_plan(int64_t t, int64_t n_seqs, int64_t hq, int64_t hk, int d, int
   p.ok = true;
   size_t at = 0;
   if (p.nc) {
-    const int64_t tiles = span / kAttnFewKeys + 2;
+    const int64_t tiles = span / kAttnFewKeys + 10;
     const int64_t units = n_seqs * hk * tiles;
     p.ok = p.ok && units < limit;
     // two resident workgroups a compute unit, one at 256 values a head (their LDS; four at 64 values
@@ -637,10 +642,14 @@ AttnPlan attn_plan(int64_t t, int64_t n_seqs, int64_t hq, int64_t hk, int d, int
     const int64_t tiles = full + seqs;
     p.plan_tiles = (int)tiles;
     p.ok = p.ok && tiles * hk < limit;
-    if (full * hk >= 2 * slots || tiles + n_seqs > 4096) {
+    // whole items to workgroups where that fills them: two items or more each, or a last round that
+    // is four fifths full (4096 tokens, 28 heads on 4: 448 items 151 us, cut into runs 181; 1000 tokens
+    // at 32767, 32 heads on 8: 128 items would leave half the chip idle)
+    const int64_t items = full * hk, rounds = (items + slots - 1) / slots;
+    if (items >= 2 * slots || (items > 0 && 5 * items >= 4 * slots * rounds) || tiles + n_seqs > 4096) {
       p.items_tile = (int)(tiles * hk);
     } else {
-      p.ok = p.ok && tiles * hk * (span / kAttnTileKeys + 4) < limit;
+      p.ok = p.ok && tiles * hk * (span / kAttnTileKeys + 16) < limit;
       p.nw_tile = (int)slots;
       p.join_tile = max_kv > kAttnTileKeys;
     }
