@@ -34,8 +34,8 @@ constexpr int kItemUnits = 8;
 // Stages of K and of V: three let a copy take four turns, which the fabric needs under load (two:
 // 582 against ... us); 256 values a head leave room for two.
 constexpr int tile_stages(int d) { return d == 256 ? 2 : 3; }
-// LDS for the finite copies of two V tiles, one for each wave group (at 256 values a head, where none is left, the fragments are
-// cleaned in registers; the spare registers allow it there).
+// LDS for the finite copies of two V tiles, one for each wave group (at 256 values a head none is
+// left).
 constexpr int tile_clean_bytes(int d) { return d == 256 ? 0 : 2 * BN * d * 2; }
 
 // V^T fragment of 32 values (tile dt) x 16 keys (step ks): two transposing reads of 4 keys each.
@@ -245,6 +245,9 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
     const int pos_lo = q.kv - q.nq + min(q.nq - 1, (int)a.g_div.div((uint32_t)(j * BM + 32 * wave)));
     const int pos_hi = q.kv - q.nq + min(q.nq - 1, (int)a.g_div.div((uint32_t)(j * BM + 32 * wave + 31)));
 
+    // and among the workgroup's
+    const int wg_lo = q.kv - q.nq + (int)a.g_div.div((uint32_t)(j * BM));
+    const int wg_hi = q.kv - q.nq + min(q.nq - 1, (int)a.g_div.div((uint32_t)(j * BM + BM - 1)));
     const bool idle = 32 * wave >= rows;
 
     f32x16_t o[ND];
@@ -278,13 +281,46 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
       return k0 + BN - 1 > pos_lo || (a.window > 0 && k0 <= pos_hi - a.window);
     };
 
+    // Without room for a finite copy the workgroup cleans the tile in place, all waves (which are in
+    // step there) between barriers: a quarter is searched and cleaned by each.
+    auto wg_cut = [&](int t) {
+      const int k0 = kfirst + t * BN;
+      return k0 + BN - 1 > wg_lo || (a.window > 0 && k0 <= wg_hi - a.window);
+    };
+    auto found_odd = [&](int t) {
+      uint32_t acc = 0;
+#pragma unroll 4
+      for (int x = 0; x < KB / (1024 * WAVES); ++x) {
+        const u32x4_t v = *(const u32x4_t*)(stage_v(t) + x * (1024 * WAVES) + tid * 16);
+        for (int y = 0; y < 4; ++y) acc |= nonfinite2<T>(v[y]);
+      }
+      return __syncthreads_or((acc & 0x80008000u) != 0) != 0;
+    };
+    auto clean_in_place = [&](int t) {
+      attn_barrier();
+#pragma unroll 4
+      for (int x = 0; x < KB / (1024 * WAVES); ++x) {
+        u32x4_t* at = (u32x4_t*)(stage_v(t) + x * (1024 * WAVES) + tid * 16);
+        u32x4_t v = *at;
+        for (int y = 0; y < 4; ++y) v[y] = finite2<T>(v[y]);
+        *at = v;
+      }
+      attn_barrier();
+    };
+
     // Products A .. B of the list: first the NV ND of output(t), o += V^T P^T, then the NK NS of
     // scores(t + 1), with the LDS fragments read kAhead products before their own.
     constexpr int NO = NV * ND, NP = NO + NK * NS;
     auto products = [&](int t, auto A, auto B) {
       const uint8_t* sv = stage_v(t);
       bool odd = false;
-      if (A < NO && is_cut(t)) {  // a key that only some rows see may hold an infinity or a NaN
+      if (!kClean && A < NO && wg_cut(t)) {
+        if (found_odd(t)) {
+          tile_nonfinite<T, D>(sv, lane, p, o);
+          clean_in_place(t);
+        }
+      }
+      if (kClean && A < NO && is_cut(t)) {  // a key that only some rows see may hold an infinity or a NaN
         uint32_t acc = 0;
 #pragma unroll 4
         for (int x = 0; x < KB / 1024; ++x) {
@@ -293,7 +329,7 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
         }
         odd = __any((acc & 0x80008000u) != 0);
         if (odd) tile_nonfinite<T, D>(sv, lane, p, o);
-        if (kClean && odd) {
+        if (odd) {
           // every wave that meets such a tile writes the same finite copy of it before its own reads
           uint8_t* clean = sm + (2 * ST + (t & 1)) * KB;
 #pragma unroll 4
@@ -311,10 +347,7 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
           const int j = i - NO;
           return *(const u32x4_t*)(kr + (j % NK) * (32 * ROW) + ((2 * (j / NK) + h) ^ swz_k<D>(col)) * 16);
         }
-        u32x4_t v = v_frag<D>(sv, lane, i % ND, i / ND);
-        if (!kClean && odd)
-          for (int y = 0; y < 4; ++y) v[y] = finite2<T>(v[y]);
-        return v;
+        return v_frag<D>(sv, lane, i % ND, i / ND);
       };
       if (B > NO) {
 #pragma unroll
@@ -400,10 +433,9 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
     attn_barrier();
     if (idle) {  // no rows: the copies only
       for (int t = 0; t < n; ++t) {
-        if (copier) {
-          copies(t + 1);
-          attn_wait_vm<0>();
-        }
+        if (copier) copies(t + 1);
+        if (!kClean && wg_cut(t) && found_odd(t)) clean_in_place(t);
+        if (copier) attn_wait_vm<0>();
         attn_barrier();
       }
     } else {
