@@ -107,8 +107,8 @@ template <typename T> __device__ __forceinline__ void only_nonfinite(uint32_t w,
 // Position of 16-byte chunk c of row r in a tile of rows of D values.  The LDS has 256 bytes of banks:
 // K is read 16 rows at one chunk per pass, V (transposing, 32 bytes of a row) either 8 rows at one
 // chunk pair or 4 rows at two neighbouring pairs; the positions of each set are distinct modulo 256
-// bytes.  (V's pairs by r & 7 alone: the tile kernel's reads met every bank twice, a third of its
-// LDS cycles.)
+// bytes.  (V's pairs by r & 7 alone: the tile kernel's reads met banks twice, a third of its LDS
+// cycles.)
 template <int D> __device__ __forceinline__ int swz_k(int r) { return D >= 128 ? (r & 15) : ((r >> 1) & 7); }
 template <int D> __device__ __forceinline__ int swz_v(int r) {
   if (D >= 128) return ((r & 3) << 2) | ((r & 4) >> 1);
@@ -264,7 +264,7 @@ template <int D, int R, int U, int STEP, bool NT> struct TileCopy {
   }
   // Turns the page ids into places; sets seen.
   __device__ __forceinline__ void resolve(const AttnArgs& a, int lo, int hi, int lane) {
-    constexpr uint32_t kRun = (uint32_t)((1ull << R) - 1), kAll = (uint32_t)((1ull << ROWS) - 1);
+    constexpr uint32_t kAll = (uint32_t)((1ull << ROWS) - 1);
     bool by_rows = true;
     if (a.page16) {
       by_rows = false;
@@ -291,7 +291,7 @@ template <int D, int R, int U, int STEP, bool NT> struct TileCopy {
       seen = (uint32_t)__ballot(now.row >= 0) & kAll;
       now.at[0] = -1;
     }
-    static_assert(U <= 2 && ROWS <= 32 && kRun != 0, "places of one or two runs");
+    static_assert(U <= 2 && ROWS <= 32, "places of one or two runs");
   }
   // Starts the copies of the rows into LDS at dst (rows back to back, chunks placed by the swizzle).
   template <bool IS_V>

@@ -3,16 +3,25 @@
 // of the group).
 //
 // The matrix cores bound it: 4 D flops per row and key against D / 64 bytes of cache (a tile of keys
-// is read once for 256 rows).  8 waves hold 32 rows each, two on every SIMD, and take turns: while
-// the first four multiply (O += V^T P^T of the last tile, then S^T = K Q^T of this one), the other
-// four turn their scores into weights on the vector units, and a barrier swaps them.  Left to
-// themselves the two waves of a SIMD fall into step and wait for the same unit (matrix cores 42 %
-// and vector units 37 % busy, never together).  At 256 values a head the registers hold one wave a
-// SIMD.  K and V tiles are copied into LDS by all waves, two stages each, V one turn later than K.
+// is read once for 256 rows).  8 waves hold 32 rows each, two on every SIMD.  Every wave turns a
+// tile's scores into weights on the vector units, then multiplies: O += V^T P^T of this tile and
+// S^T = K Q^T of the next, one stream of 32x32x16 products whose LDS fragments are read ahead.  One
+// barrier a tile, met by the first four waves after their products and by the others after their
+// weights, keeps the two groups half a tile apart, so that one multiplies while the other is on the
+// vector units.  (Left to themselves the two waves of a SIMD fall into step and wait for the same
+// unit: matrix cores 42 % busy, vector units 37 %, never together, 646 us against 490 for 1000
+// tokens at 32767, 32 heads on 8 of 128.  A barrier at every half tile: 520.  Now 51 %, what is left
+// is each wave's own chain of weights and products; two waves a SIMD fill the registers.)  The
+// first four waves copy the K and V tiles into LDS, a period ahead of their first reader.
 //
-// Work split.  With many items (sequence, kv head, row tile), one workgroup each, the longest
-// first, kv heads fastest so that a head's tiles run on one XCD and share its L2.  With few, all
-// items are laid end to end in units of one row tile x 64 keys and cut into equal runs, one
+// At 256 values a head the registers hold one wave a SIMD: 4 waves, all in step.
+//
+// Measured (bf16, 32 heads on 8 of 128): 4096 tokens 146 us, 940 TFLOP/s; 1000 tokens at 32767
+// 490 us, 1080 TFLOP/s; a large bf16 library product reaches 1219 here.
+//
+// Work split.  With enough items (sequence, kv head, row tile) to fill the chip, one workgroup each,
+// the longest first, kv heads fastest so that a head's tiles run on one XCD and share its L2.  Else
+// all items are laid end to end in units of one row tile x 64 keys and cut into equal runs, one
 // per compute unit; cut items leave pieces for the joining kernel.
 #include <algorithm>
 #include <type_traits>
@@ -31,8 +40,8 @@ constexpr int kAhead = 4;
 // tile (0, 4, 8, 12 units: 12 mixed sequences 147, 144, 141, 144 us; 8 x 500 tokens 73, 68, 58, 57).
 constexpr int kItemUnits = 8;
 
-// Stages of K and of V: three let a copy take four turns, which the fabric needs under load (two:
-// 582 against ... us); 256 values a head leave room for two.
+// Stages of K and of V: the two wave groups read neighbouring tiles while a third is copied; one
+// group reads one.
 constexpr int tile_stages(int d) { return d == 256 ? 2 : 3; }
 // LDS for the finite copies of two V tiles, one for each wave group (at 256 values a head none is
 // left).
@@ -102,7 +111,7 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
   constexpr int NS = D / 16;    // k-steps of the scores
   constexpr int ND = D / 32;    // output tiles of 32 values
   constexpr int NV = BN / 16;   // k-steps of the output
-  constexpr int R = BN / 4;     // keys a wave copies (the second four waves do)
+  constexpr int R = BN / 4;     // keys of a tile that each of the first four waves copies
   constexpr bool kClean = tile_clean_bytes(D) > 0;
   constexpr int ST = tile_stages(D);  // stages of K, and of V
   // K stages, V stages, finite copies of V, then (RUNS) the plan
@@ -115,7 +124,8 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
   const int h = lane >> 5, col = lane & 31;
 
   int u0, u1, W, nw, w;
-  int* plan = (int*)(sm + 2 * ST * KB + tile_clean_bytes(D));  // RUNS: first unit (of one head) of each row tile, then the sequences' first tiles
+  // RUNS: first unit (of one head) of each row tile, then the sequences' first tiles
+  int* plan = (int*)(sm + 2 * ST * KB + tile_clean_bytes(D));
   int nt_all = 0;
   int* seq_first = nullptr;
   AttnRecord* rec = nullptr;
@@ -168,7 +178,7 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
     u1 = u0 + 1;
   }
 
-  const int late = wave / 4;  // the second four waves run one turn behind
+  const int late = wave / 4;  // the second four waves run half a tile behind
   const bool copier = wave < 4;
   const int row0 = R * (wave & 3);  // first key of a tile that a copying wave copies
   TileCopy<D, R, 1, BN, false> tc;
@@ -313,12 +323,9 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
     constexpr int NO = NV * ND, NP = NO + NK * NS;
     auto products = [&](int t, auto A, auto B) {
       const uint8_t* sv = stage_v(t);
-      bool odd = false;
-      if (!kClean && A < NO && wg_cut(t)) {
-        if (found_odd(t)) {
-          tile_nonfinite<T, D>(sv, lane, p, o);
-          clean_in_place(t);
-        }
+      if (!kClean && A < NO && wg_cut(t) && found_odd(t)) {
+        tile_nonfinite<T, D>(sv, lane, p, o);
+        clean_in_place(t);
       }
       if (kClean && A < NO && is_cut(t)) {  // a key that only some rows see may hold an infinity or a NaN
         uint32_t acc = 0;
@@ -327,9 +334,9 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
           const u32x4_t v = *(const u32x4_t*)(sv + x * 1024 + lane * 16);
           for (int y = 0; y < 4; ++y) acc |= nonfinite2<T>(v[y]);
         }
-        odd = __any((acc & 0x80008000u) != 0);
-        if (odd) tile_nonfinite<T, D>(sv, lane, p, o);
+        const bool odd = __any((acc & 0x80008000u) != 0);
         if (odd) {
+          tile_nonfinite<T, D>(sv, lane, p, o);
           // every wave that meets such a tile writes the same finite copy of it before its own reads
           uint8_t* clean = sm + (2 * ST + (t & 1)) * KB;
 #pragma unroll 4

@@ -10,6 +10,9 @@
 // token: their loads are in flight together and the token's table values are read once for all of
 // them.  The mean is a reduction by DPP within 16 lanes, and a value's partner lies in a lane
 // rot/16 further in its group.
+//
+// Measured (bf16, 40 heads of 128): 8192 tokens 34 us, 172 MB, 5.1 TB/s (a large copy reaches 5.1
+// here); append of 4096 tokens 19 us; one token 2.9 us.
 #include "device_common.hpp"
 #include "launch.hpp"
 
