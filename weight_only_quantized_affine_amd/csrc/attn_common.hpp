@@ -10,8 +10,7 @@
 // a row are per-lane scalars, and the lane's scores are already the P^T operand of the second
 // product under a permutation of the keys that the V^T reads follow.
 #pragma once
-#include "device_common.hpp"
-#include "launch.hpp"
+#include "head_common.hpp"
 
 namespace ql {
 

@@ -10,7 +10,6 @@ typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
 typedef __attribute__((ext_vector_type(2))) _Float16 f16x2_t;
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8_t;
 typedef __attribute__((ext_vector_type(8))) _Float16 f16x8_t;
-typedef __attribute__((ext_vector_type(2))) float f32x2_t;
 typedef __attribute__((ext_vector_type(4))) float f32x4_t;
 typedef __attribute__((ext_vector_type(16))) float f32x16_t;
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4_t;
@@ -46,14 +45,6 @@ template <> __device__ __forceinline__ float param_to_f32<F16>(uint32_t b) { ret
 template <typename T> __device__ __forceinline__ uint32_t f32_to_bits(float f);
 template <> __device__ __forceinline__ uint32_t f32_to_bits<BF16>(float f) { return f32_to_bf16_bits(f); }
 template <> __device__ __forceinline__ uint32_t f32_to_bits<F16>(float f) { return f32_to_f16_bits(f); }
-
-// Two fp32 values rounded to nearest even into one word.
-__device__ __forceinline__ uint32_t pack2(BF16, float a, float b) {
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, bf16x2_t));
-}
-__device__ __forceinline__ uint32_t pack2(F16, float a, float b) {
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2_t{a, b}, f16x2_t));
-}
 
 // Store one fp32 result rounded once to the output dtype.
 __device__ __forceinline__ void store_out(void* y, int64_t i, float v, int dt) {

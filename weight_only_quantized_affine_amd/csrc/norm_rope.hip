@@ -13,8 +13,7 @@
 //
 // Measured (bf16, 40 heads of 128): 8192 tokens 34 us, 172 MB, 5.1 TB/s (a large copy reaches 5.1
 // here); append of 4096 tokens 19 us; one token 2.9 us.
-#include "device_common.hpp"
-#include "launch.hpp"
+#include "head_common.hpp"
 
 namespace ql {
 namespace {

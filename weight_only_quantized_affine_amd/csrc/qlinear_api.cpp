@@ -12,6 +12,7 @@
 #include <vector>
 
 #include "../../include/qlinear.h"
+#include "attn_launch.hpp"
 #include "launch.hpp"
 
 namespace {
