@@ -16,7 +16,8 @@
  * Conventions for every entry point:
  *   - W is [n, k]: n outputs by k inputs, quantized along k.  x is [m, k], y is [m, n], row-major,
  *     contiguous.  Integer sizes are element counts.
- *   - Every pointer except the host problem list of qlinear_gemv_batched is DEVICE memory on the
+ *   - Every pointer except the host problem list of qlinear_gemv_batched, the weight list of
+ *     qlinear_gemm_grouped and the argument structs of the attention side is DEVICE memory on the
  *     current HIP device, owned by the caller.  The library allocates nothing and keeps no state
  *     between calls (no decoded or dense weight cache).
  *   - `stream` is a hipStream_t (NULL = the null stream).  Calls are asynchronous on it; none
