@@ -559,7 +559,10 @@ def _norm_rope(n: _NormRope, t: int, d: int, q_weight, k_weight, eps, positions,
 def _stream_on(device: int) -> int:
     if device < 0:
         raise QLError(2, "every tensor must be on one GPU, not in host memory")
-    return _torch()._C._cuda_getCurrentRawStream(device)
+    cuda = _torch()._C
+    if device != cuda._cuda_getDevice():
+        raise QLError(2, f"the tensors are on cuda:{device}, which is not the current device")
+    return cuda._cuda_getCurrentRawStream(device)
 
 
 def qlinear_qk_norm_rope(q, k, *, q_weight=None, k_weight=None, eps: float = 1e-6, positions=None, cos_sin=None,

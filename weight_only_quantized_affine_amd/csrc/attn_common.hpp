@@ -360,14 +360,17 @@ template <int WAVES> __device__ __forceinline__ int block_scan(int v, int* sh, i
   return before + x - v;
 }
 
-// A split item: the workgroup that began it writes where its row and pieces are.
+// A split item: the workgroup that began it writes where its rows and pieces are.  Records are kept
+// by item where there are at most as many as workgroups (few records to look through), else by
+// the workgroup that began the item, which begins at most one that it does not finish.
 struct AttnRecord {
   int32_t pieces;  // 0: nothing to join
   int32_t q0;      // first query token of the sequence
   int32_t row0;    // first row of the item among the sequence's nq * g rows
   int32_t rows;    // rows of the item
   int32_t head;    // kv head
-  int32_t pad_[3];
+  int32_t w;       // the workgroup that began it
+  int32_t pad_[2];
 };
 // Range of units [u0, u1) of workgroup w of nw over W units, and the last workgroup that holds a
 // unit below `end` (nw <= W: none is empty).

@@ -133,10 +133,15 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few_kernel(const A
   // workgroups of one XCD (every 8th) take neighbouring runs (one sequence of 131071: 102 -> 97 us)
   const int w = a.nw_few % 8 == 0 ? (blockIdx.x & 7) * (a.nw_few >> 3) + (blockIdx.x >> 3) : blockIdx.x;
   AttnRecord* rec = a.rec + w;
-  if (w >= nw) {
-    if (tid == 0) rec->pieces = 0;
-    return;
+  if (a.few_by_item) {  // the first workgroup clears the records of sequences that are not taken here
+    if (blockIdx.x == 0)
+      for (int i = tid; i < a.n_seqs; i += 256)
+        if (cost(i) == 0)
+          for (int h = 0; h < a.hk; ++h) a.rec[i * a.hk + h].pieces = 0;
+  } else if (w >= nw && tid == 0) {
+    rec->pieces = 0;
   }
+  if (w >= nw) return;
   const int u0 = attn_cut(w, nw, W), u1 = attn_cut(w + 1, nw, W);
   // sequence of unit u0 and its first unit; beyond 256 sequences the scan is run again
   for (int s0 = 0, sum = 0; s0 < a.n_seqs && sum <= u0; s0 += 256) {
@@ -360,11 +365,13 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few_kernel(const A
       }
       __syncthreads();
     }
-    if (!whole && ta == 0) {
+    if (ta == 0 && (!whole || a.few_by_item)) {
       recorded = true;
       if (tid == 0) {
         AttnRecord r = {};
-        r.pieces = attn_last(item0 + nt, nw, W) - w + 1;
+        if (a.few_by_item) rec = a.rec + s * a.hk + head;
+        r.pieces = whole ? 0 : attn_last(item0 + nt, nw, W) - w + 1;
+        r.w = w;
         r.q0 = q.q0;
         r.row0 = 0;
         r.rows = rows;
@@ -373,7 +380,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few_kernel(const A
       }
     }
   }
-  if (!recorded && tid == 0) rec->pieces = 0;
+  if (!recorded && !a.few_by_item && tid == 0) rec->pieces = 0;
 }
 
 }  // namespace
@@ -387,7 +394,8 @@ template <typename T> static hipError_t few_d(const AttnArgs& a, int d, int nc, 
   if (d == 128) return nc == 1 ? few<T, 128, 1>(a, s) : few<T, 128, 2>(a, s);
   return few<T, 256, 1>(a, s);
 }
-hipError_t launch_attn_few(const AttnArgs& a, int dt, int d, int nc, hipStream_t s) {
+hipError_t launch_attn_few(const AttnArgs& args, int dt, int d, int nc, hipStream_t s) {
+  const AttnArgs a = attn_record_kind(args);
   return dt == DT_BF16 ? few_d<BF16>(a, d, nc, s) : few_d<F16>(a, d, nc, s);
 }
 

@@ -78,6 +78,7 @@ struct AttnArgs {
   int few_rows;  // sequences of at most this many rows go to the few-row kernel
   int nw_few, cap_few, part_floats, join_few;
   int nw_tile, items_tile, plan_tiles, join_tile;
+  int few_by_item, tile_by_item;  // records by item, else by workgroup
   AttnRecord* rec;
   float *part, *part_tile;
 };
@@ -92,6 +93,8 @@ struct AttnPlan {
 };
 AttnPlan attn_plan(int64_t t, int64_t n_seqs, int64_t hq, int64_t hk, int d, int64_t max_q, int64_t max_kv,
                    int64_t window);
+// The arguments with the kind of records set.
+AttnArgs attn_record_kind(AttnArgs a);
 hipError_t launch_attn_few(const AttnArgs& a, int dt, int d, int nc, hipStream_t s);
 hipError_t launch_attn_tile(const AttnArgs& a, int dt, int d, hipStream_t s);
 hipError_t launch_attn_join(const AttnArgs& a, int dt, int d, hipStream_t s);

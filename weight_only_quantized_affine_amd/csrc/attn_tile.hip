@@ -166,10 +166,13 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
     const int per = a.nw_tile / 8;
     w = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
     rec = a.rec + a.nw_few + w;
-    if (w >= nw) {
-      if (tid == 0) rec->pieces = 0;
-      return;
+    if (a.tile_by_item) {  // the first workgroup clears the records of items that there are not
+      if (blockIdx.x == 0)
+        for (int i = nt_all * a.hk + tid; i < a.plan_tiles * a.hk; i += 64 * WAVES) a.rec[a.nw_few + i].pieces = 0;
+    } else if (w >= nw && tid == 0) {
+      rec->pieces = 0;
     }
+    if (w >= nw) return;
     u0 = attn_cut(w, nw, W);
     u1 = attn_cut(w + 1, nw, W);
   } else {
@@ -203,6 +206,10 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
       tb = min(nt, u1 - item0);
       u = item0 + nt;
       if (tb <= ta) continue;  // the run ends before the item's first tile
+      if (a.tile_by_item) {
+        rec = a.rec + a.nw_few + ti * a.hk + head;
+        if (ta == 0 && tb == nt && tid == 0) rec->pieces = 0;
+      }
       b = 0, e = a.n_seqs;
       while (e - b > 1) {
         const int m = (b + e) / 2;
@@ -494,6 +501,7 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
         recorded = true;
         if (tid == 0) {
           AttnRecord rr = {};
+          rr.w = w;
           rr.pieces = attn_last(item0 + nt, nw, W) - w + 1;
           rr.q0 = q.q0;
           rr.row0 = j * BM;
@@ -505,7 +513,7 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
     }
   }
   if constexpr (RUNS) {
-    if (!recorded && tid == 0) rec->pieces = 0;
+    if (!recorded && !a.tile_by_item && tid == 0) rec->pieces = 0;
   }
 }
 
@@ -525,10 +533,10 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const AttnArgs 
   const bool is_few = (int)blockIdx.x < few_blocks;
   const int b = is_few ? blockIdx.x : blockIdx.x - few_blocks;
   const int per = is_few ? few_per : tile_per, lanes = is_few ? few_lanes : tile_lanes;
-  const int w = b / per;
-  const AttnRecord r = a.rec[is_few ? w : a.nw_few + w];
+  const AttnRecord r = a.rec[(is_few ? 0 : a.nw_few) + b / per];
   const int row0 = b % per * (SLOTS / lanes);
   if (r.pieces == 0 || row0 >= r.rows) return;
+  const int w = r.w;
   const int cap = is_few ? a.cap_few : BM;
   const int slot_floats = is_few ? a.part_floats : BM * (D + 2);
   const float* part = is_few ? a.part : a.part_tile;
@@ -631,12 +639,13 @@ template <typename T, int D> hipError_t join(const AttnArgs& a, hipStream_t s) {
     few_lanes = lanes_for(a.nw_few, (int64_t)a.n_seqs * a.hk);
     const int rows = (int)std::min<int64_t>(a.cap_few, (int64_t)a.max_q * a.g);
     few_per = (rows * few_lanes + SLOTS - 1) / SLOTS;
-    few = a.nw_few * few_per;
+    few = (a.few_by_item ? a.n_seqs * a.hk : a.nw_few) * few_per;
   }
   if (a.nw_tile > 0 && a.join_tile) {
     tile_lanes = lanes_for(a.nw_tile, (int64_t)a.plan_tiles * a.hk);
-    tile_per = BM * tile_lanes / SLOTS;
-    many = a.nw_tile * tile_per;
+    const int rows = (int)std::min<int64_t>(BM, (int64_t)a.max_q * a.g);
+    tile_per = (rows * tile_lanes + SLOTS - 1) / SLOTS;
+    many = (a.tile_by_item ? a.plan_tiles * a.hk : a.nw_tile) * tile_per;
   }
   if (few + many == 0) return hipSuccess;
   attn_join_kernel<T, D><<<few + many, kJoinThreads, 0, s>>>(a, few, few_per, few_lanes, tile_per, tile_lanes);
@@ -705,11 +714,19 @@ AttnPlan attn_plan(int64_t t, int64_t n_seqs, int64_t hq, int64_t hk, int d, int
   return p;
 }
 
-hipError_t launch_attn_tile(const AttnArgs& a, int dt, int d, hipStream_t s) {
+AttnArgs attn_record_kind(AttnArgs a) {
+  a.few_by_item = (int64_t)a.n_seqs * a.hk <= a.nw_few;
+  a.tile_by_item = (int64_t)a.plan_tiles * a.hk <= a.nw_tile;
+  return a;
+}
+
+hipError_t launch_attn_tile(const AttnArgs& args, int dt, int d, hipStream_t s) {
+  const AttnArgs a = attn_record_kind(args);
   if (dt == DT_BF16) return d == 64 ? tile<BF16, 64>(a, s) : d == 128 ? tile<BF16, 128>(a, s) : tile<BF16, 256>(a, s);
   return d == 64 ? tile<F16, 64>(a, s) : d == 128 ? tile<F16, 128>(a, s) : tile<F16, 256>(a, s);
 }
-hipError_t launch_attn_join(const AttnArgs& a, int dt, int d, hipStream_t s) {
+hipError_t launch_attn_join(const AttnArgs& args, int dt, int d, hipStream_t s) {
+  const AttnArgs a = attn_record_kind(args);
   if (dt == DT_BF16) return d == 64 ? join<BF16, 64>(a, s) : d == 128 ? join<BF16, 128>(a, s) : join<BF16, 256>(a, s);
   return d == 64 ? join<F16, 64>(a, s) : d == 128 ? join<F16, 128>(a, s) : join<F16, 256>(a, s);
 }
