@@ -295,3 +295,31 @@ def test_no_sequences_no_tokens_no_pages():
     out = q.qlinear_paged_attention(x, none, none, torch.zeros(2, 1, **i32), torch.arange(3, **i32), torch.ones(2, **i32),
                                     max_q=1)
     assert (out == 0).all()
+
+
+def sampled(p, got, places, **kw):
+    """Rows (sequence, token, head) of got against the oracle, each as one token of its own."""
+    for s, i, h in places:
+        n, kv = p.lens[s]
+        row, kh = int(p.cu[s]) + i, h // (p.q.shape[1] // p.k.shape[2])
+        one = Problem.__new__(Problem)
+        one.lens, one.dtype, one.cu = [(1, kv - n + i + 1)], p.dtype, np.array([0, 1], dtype=np.int32)
+        one.q, one.table = p.q[row:row + 1, h:h + 1], p.table[s:s + 1]
+        one.k, one.v = p.k[:, :, kh:kh + 1], p.v[:, :, kh:kh + 1]
+        kw_one = dict(kw, sinks=kw["sinks"][h:h + 1]) if kw.get("sinks") is not None else kw
+        try:
+            close(got[row:row + 1, h:h + 1], one.oracle(**kw_one), p.q.shape[2], p.dtype)
+        except AssertionError as e:
+            raise AssertionError(f"sequence {s}, token {i}, head {h}: {e}") from None
+
+
+@pytest.mark.parametrize("hk", [4, 16], ids=["cut into runs", "whole items"])
+def test_long_chunks_of_256_values(hk):
+    """Row tiles of 128 rows over many key tiles whose last row tile leaves waves without rows (2010 x 2
+    rows: 52 in the last): every key tile's scores are of that tile, in every call."""
+    p = Problem([(2010, 4500), (70, 2000)], 2 * hk, hk, 256, 64, BF, seed=15)
+    want = p.run()
+    places = [(0, i, h) for i, h in zip((0, 1, 777, 1983, 1984, 1990, 2008, 2009, 2009), (0, 1, 5, 0, 3, 6, 7, 2, 2 * hk - 1))]
+    sampled(p, want, places + [(1, 0, 0), (1, 69, 2 * hk - 1)])
+    for _ in range(5):  # the same bits with the keys in the caches
+        assert torch.equal(p.run(), want)

@@ -27,6 +27,7 @@
 #include <type_traits>
 
 #include "attn_common.hpp"
+#include "attn_order.hpp"
 
 namespace ql {
 namespace {
@@ -118,7 +119,7 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
   extern __shared__ __attribute__((aligned(1024))) uint8_t sm[];
   __shared__ int ssh[WAVES];
   __shared__ int sfound[4];
-  __shared__ __attribute__((aligned(8))) uint16_t sseen[4][4];  // per tile % 4: bit j: key j is loaded
+  __shared__ __attribute__((aligned(8))) uint16_t sseen[4][4];  // bit j: key j is loaded
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int h = lane >> 5, col = lane & 31;
@@ -280,18 +281,13 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
     const uint8_t* vb = a.v + (int64_t)head * a.head_stride;
     const int32_t* table = a.table + (int64_t)s * a.table_stride;
     const int n = tb - ta, kfirst = (first + ta) * BN;
-    auto stage_k = [&](int t) { return sm + (t % ST) * KB; };
-    auto stage_v = [&](int t) { return sm + (ST + t % ST) * KB; };
+    auto stage_k = [&](int t) { return sm + attn_stage<ST>(t) * KB; };
+    auto stage_v = [&](int t) { return sm + (ST + attn_stage<ST>(t)) * KB; };
     auto copy_k = [&](int t) {
       tc.resolve(a, lo, hi, lane);
-      if (lane == 0) sseen[t & 3][wave & 3] = (uint16_t)tc.seen;
+      if (lane == 0) sseen[attn_seen_at(t)][wave & 3] = (uint16_t)tc.seen;
       tc.template copy<false>(tc.now, kb, stage_k(t) + row0 * ROW, row0, lane);
       if (t + 1 < n) tc.lookup(a, table, kfirst + (t + 1) * BN + row0, lo, hi, lane, false);
-    };
-    // V of t and K of t + 1 start (their stages' last readers are a period past)
-    auto copies = [&](int t) {
-      if (t < n) tc.template copy<true>(tc.now, vb, stage_v(t) + row0 * ROW, row0, lane);
-      if (t + 1 < n) copy_k(t + 1);
     };
     auto is_cut = [&](int t) {  // whether some row does not see all of it
       const int k0 = kfirst + t * BN;
@@ -345,7 +341,7 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
         if (odd) {
           tile_nonfinite<T, D>(sv, lane, p, o);
           // every wave that meets such a tile writes the same finite copy of it before its own reads
-          uint8_t* clean = sm + (2 * ST + (t & 1)) * KB;
+          uint8_t* clean = sm + (2 * ST + attn_clean_at(t)) * KB;
 #pragma unroll 4
           for (int x = 0; x < KB / 1024; ++x) {
             u32x4_t v = *(const u32x4_t*)(sv + x * 1024 + lane * 16);
@@ -398,7 +394,7 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
           sc[x >> 4][x & 15] = ((int)(jj <= last) & (int)(jj > before)) ? sc[x >> 4][x & 15] : kNegInf;
         }
       }
-      const uint64_t seen = *(const uint64_t*)sseen[t & 3];
+      const uint64_t seen = *(const uint64_t*)sseen[attn_seen_at(t)];
       if (seen != ~(uint64_t)0) {
         asm volatile("");
         const uint32_t s0 = (uint32_t)seen >> (4 * h), s1 = (uint32_t)(seen >> 32) >> (4 * h);
@@ -434,37 +430,20 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
         }
       }
     };
-    // Every wave takes weights(t), then output(t) and scores(t + 1).  A period ends with a barrier,
-    // which the first four waves meet after the products and the others after the weights.  Copies
-    // start with a period and are waited for at its end.
-    attn_barrier();  // the last item's reads are done
-    if (copier) {
-      tc.lookup(a, table, kfirst + row0, lo, hi, lane, true);
-      copy_k(0);
-      copies(0);
-      attn_wait_vm<0>();
-    }
-    attn_barrier();
-    if (idle) {  // no rows: the copies only
-      for (int t = 0; t < n; ++t) {
-        if (copier) copies(t + 1);
+    attn_tile_order<ST>(n, copier, late, idle, [&](auto what, int t) {
+      constexpr AttnStep S = decltype(what)::value;
+      if constexpr (S == AttnStep::kBarrier) attn_barrier();
+      if constexpr (S == AttnStep::kPages) tc.lookup(a, table, kfirst + row0, lo, hi, lane, true);
+      if constexpr (S == AttnStep::kCopyK) copy_k(t);
+      if constexpr (S == AttnStep::kCopyV) tc.template copy<true>(tc.now, vb, stage_v(t) + row0 * ROW, row0, lane);
+      if constexpr (S == AttnStep::kWait) attn_wait_vm<0>();
+      if constexpr (S == AttnStep::kScores) products(t - 1, kScores, kLast);
+      if constexpr (S == AttnStep::kWeights) weights(t);
+      if constexpr (S == AttnStep::kProducts) products(t, kFirst, kLast);
+      if constexpr (S == AttnStep::kIdle) {
         if (!kClean && wg_cut(t) && found_odd(t)) clean_in_place(t);
-        if (copier) attn_wait_vm<0>();
-        attn_barrier();
       }
-    } else {
-      products(-1, kScores, kLast);
-      for (int t = 0; t < n; ++t) {
-        if (copier) copies(t + 1);
-        weights(t);
-        if (late) attn_barrier();
-        products(t, kFirst, kLast);  // (after the last tile the scores are of stale keys and unused)
-        if (!late) {
-          attn_wait_vm<0>();
-          attn_barrier();
-        }
-      }
-    }
+    });
     l = join32(l, SumF());
 
     // The lane holds its row's values 32 d + 8 y + 4 h .. + 3.
