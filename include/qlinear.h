@@ -381,8 +381,8 @@ ql_status qlinear_kv_append(const ql_heads* q, const ql_heads* q_out, const ql_h
  * block_table[s][j / page_size], place j % page_size; positions in a page outside [0, n_pages) are not
  * seen, and neither are unused slots' values, whatever they hold.
  *   out = sum_j e^(scale q.k_j) v_j / (sum_j e^(scale q.k_j) + e^(sinks[h]))
- * per query head h (sinks: fp32 [hq] or NULL for no such term); kv head h / (hq / hk).  A row that
- * sees nothing is zero.  Scores, softmax sums and the output are accumulated in fp32; the softmax
+ * per query head h (sinks: fp32 [hq] or NULL for no such term; -infinity is none for that head, and
+ * +infinity gives zero); kv head h / (hq / hk).  A row that sees nothing is zero.  Scores, softmax sums and the output are accumulated in fp32; the softmax
  * weights enter the product with v rounded to the 16-bit dtype.
  * cu_q int32 [n_seqs + 1] (not decreasing, from 0), kv_lens int32 [n_seqs] and block_table int32 [n_seqs]
  * rows of max_pages entries, table_stride apart, are DEVICE memory (4-byte aligned) and not known to the

@@ -71,9 +71,9 @@ def paged_attention(q, k_cache, v_cache, block_table, cu_q, kv_lens, scale, wind
                 v = v_cache[pages[see], place[see], h // (hq // hk)]
                 row = q[cu_q[s] + i, h]
                 x = (k @ row) * scale
-                m = x.max() if sinks is None else max(x.max(), sinks[h])
+                m = x.max() if sinks is None or np.isinf(sinks[h]) else max(x.max(), sinks[h])
                 e = np.exp(x - m)
-                z = e.sum() + (0.0 if sinks is None else np.exp(sinks[h] - m))
+                z = e.sum() + (0.0 if sinks is None else np.exp(sinks[h] - m))  # infinite sinks: 0 or infinity
                 out[cu_q[s] + i, h] = (e @ v) / z
                 mag[cu_q[s] + i, h] = (e @ np.abs(v)) / z
                 info[cu_q[s] + i, h] = ((np.abs(k) @ np.abs(row)).max() * scale, np.abs(x).max(), see.sum(),

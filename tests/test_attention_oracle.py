@@ -62,3 +62,12 @@ def test_append_skips_slots_out_of_range():
     cache = np.zeros((2, 3, 1, 1))
     out = A.kv_append(cache, np.arange(1.0, 5.0).reshape(4, 1, 1), [4, -1, 6, 0])
     assert out.reshape(-1).tolist() == [4, 0, 0, 0, 1, 0]
+
+
+def test_infinite_sinks_are_no_term_and_no_weight():
+    r = np.random.default_rng(4)
+    kc, vc = r.normal(size=(2, 4, 1, 2)), r.normal(size=(2, 4, 1, 2))
+    q = r.normal(size=(3, 2, 2))
+    args = (q, kc, vc, np.array([[1, 0]]), [0, 3], [6], 0.7)
+    out, _, _ = A.paged_attention(*args, sinks=np.array([-np.inf, np.inf]))
+    assert np.array_equal(out[:, 0], A.paged_attention(*args)[0][:, 0]) and (out[:, 1] == 0).all()

@@ -323,3 +323,27 @@ def test_long_chunks_of_256_values(hk):
     sampled(p, want, places + [(1, 0, 0), (1, 69, 2 * hk - 1)])
     for _ in range(5):  # the same bits with the keys in the caches
         assert torch.equal(p.run(), want)
+
+
+@pytest.mark.parametrize("lens", ["empty", "drafts", "chunks", "mixed", "one", "long chunk"])
+@pytest.mark.parametrize("dtype,d", [(BF, 64), (HF, 128), (BF, 256)])
+def test_infinite_sinks(lens, dtype, d):
+    """-inf is no term, +inf takes all the weight; a row that sees nothing is zero either way.  In every
+    epilogue: whole items and cut ones of few and of many rows."""
+    p = Problem({**LENS, "long chunk": [(40, 3000), (0, 0), (50, 7)]}[lens], 4, 2, d, 16, dtype, seed=16)
+    inf = float("inf")
+    for sinks in ([-inf, 0.5, inf, -inf], [-inf] * 4):
+        sinks = torch.tensor(sinks, device=DEV)
+        close(p.run(sinks=sinks), p.oracle(sinks=sinks), d, dtype)
+    assert torch.equal(p.run(sinks=torch.full((4,), -inf, device=DEV)), p.run())
+
+
+def test_infinite_sinks_of_whole_row_tiles():
+    """Row tiles that are not split, and rows before the first cached position."""
+    p = Problem([(2200, 1900), (2100, 2100)], 32, 32, 64, 64, BF, seed=17)
+    sinks = torch.zeros(32, device=DEV)
+    sinks[::3], sinks[1::3] = -float("inf"), float("inf")
+    got = p.run(sinks=sinks)
+    assert (got[:300] == 0).all() and (got[:, 1::3] == 0).all()
+    assert torch.equal(got[:, ::3], p.run()[:, ::3])
+    sampled(p, got, [(0, 300, 0), (0, 2199, 3), (1, 0, 6), (1, 1000, 2), (1, 2099, 31)], sinks=sinks)

@@ -348,13 +348,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few_kernel(const A
           if (whole) {
             const int tok = (int)a.g_div.div((uint32_t)row);
             const int hq = head * a.g + row - tok * a.g;
-            float fo = 1.f;
-            if (a.sinks) {
-              const float sk2 = a.sinks[hq] * kLog2e, mn = fmaxf(mr, sk2);
-              fo = mr == kNegInf ? 0.f : exp2_fast(mr - mn);
-              lr = lr * fo + exp2_fast(sk2 - mn);
-            }
-            const float inv = lr == 0.f ? 0.f : fo / lr;
+            const float inv = attn_scale(a.sinks, hq, mr, lr);
             uint8_t* op = a.out + ((int64_t)(q.q0 + tok) * a.out_ts + (int64_t)hq * a.out_hs) + c * 8;
             store4(T{}, op, x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
           } else {

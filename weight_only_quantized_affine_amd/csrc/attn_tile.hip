@@ -449,13 +449,7 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
     // The lane holds its row's values 32 d + 8 y + 4 h .. + 3.
     if (!RUNS || (ta == 0 && tb == nt)) {
       if (in) {
-        float fo = 1.f, lr = l;
-        if (a.sinks) {
-          const float s2 = a.sinks[hq] * kLog2e, mn = fmaxf(m, s2);
-          fo = m == kNegInf ? 0.f : exp2_fast(m - mn);
-          lr = l * fo + exp2_fast(s2 - mn);
-        }
-        const float inv = lr == 0.f ? 0.f : fo / lr;
+        const float inv = attn_scale(a.sinks, hq, m, l);
         uint8_t* op = a.out + ((int64_t)(q.q0 + i) * a.out_ts + (int64_t)hq * a.out_hs) + 8 * h;
 #pragma unroll
         for (int d = 0; d < ND; ++d)
@@ -581,13 +575,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const AttnArgs 
       const int rr = r.row0 + row;
       const int tok = (int)a.g_div.div((uint32_t)rr);
       const int hq = r.head * a.g + rr - tok * a.g;
-      float fo = 1.f;
-      if (a.sinks) {
-        const float s2 = a.sinks[hq] * kLog2e, mn = fmaxf(m, s2);
-        fo = m == kNegInf ? (l == 0.f ? 0.f : 1.f) : exp2_fast(m - mn);
-        l = l * fo + exp2_fast(s2 - mn);
-      }
-      const float inv = l == 0.f ? 0.f : fo / l;
+      const float inv = attn_scale(a.sinks, hq, m, l);
       uint8_t* op = a.out + ((int64_t)(r.q0 + tok) * a.out_ts + (int64_t)hq * a.out_hs) + c * 8;
       store4(T{}, op, x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
     }
