@@ -173,3 +173,21 @@ def test_binding_refuses_host_memory():
                                                   torch.zeros(1, **i32), max_q=2)):
         with pytest.raises(q.QLError, match="one GPU"):
             bad()
+
+
+def test_work_past_64_bits_is_refused_and_any_window_is_planned(lib):
+    size = lib.qlinear_paged_attention_workspace_size
+    big = (1 << 63) - 1
+    for args in ((2, 1, 16, 8, 128, 2), (80, 16, 32, 8, 128, 5), (4000, 3, 8, 8, 256, 4000), (9, 9, 4, 4, 64, 1)):
+        none = size(*args, 64, 16, 0)
+        assert none > 0
+        for window in (64 * 16, 1 << 40, big - 1, big):  # windows over the whole cache
+            assert size(*args, 64, 16, window) == none, (args, window)
+    # units of work past 2^31, 2^63 and 2^64: refused, whatever the products wrap to
+    h = heads(n=1 << 19, ts=1 << 26)
+    c = cache(n_pages=0, k=None, v=None, hk=1 << 19, page_size=1)
+    for n in ((1 << 13), (1 << 20), (1 << 24) + 1, (1 << 26), (1 << 29)):
+        for pages in (1 << 12, 1 << 21, (1 << 30) - 1):
+            for t, max_q in ((n, 1), (min(4 * n, (1 << 30) - 1), 100)):
+                assert attend(lib, qh=h, out=h, c=c, t=t, n=n, max_q=max_q, pages=pages, ws_bytes=(1 << 63)) == UNSUPPORTED, (n, pages, t)
+                assert size(t, n, 1 << 19, 1 << 19, 128, max_q, pages, 1, 0) < (1 << 40)

@@ -627,7 +627,10 @@ AttnPlan attn_plan(int64_t t, int64_t n_seqs, int64_t hq, int64_t hk, int d, int
   const int64_t g = hq / hk, bm = 32 * attn_tile_waves(d);
   const int64_t cap = d == 256 ? 16 : 32;  // rows whose registers fit
   const int64_t limit = int64_t(1) << 31;
-  const int64_t span = window > 0 ? std::min(max_kv, window + max_q - 1) : max_kv;  // longest span of an item
+  // a product of counts, cut at the limit (three of them pass 2^63 within what the caller accepts)
+  auto times = [&](int64_t x, int64_t y) { return y > 0 && x >= (limit + y - 1) / y ? limit : x * y; };
+  // longest span of an item; any window from max_kv on hides nothing
+  const int64_t span = window > 0 && window < max_kv ? std::min(max_kv, window + max_q - 1) : max_kv;
   auto nc_of = [](int64_t rows) { return rows <= 16 ? 1 : 2; };
   if (max_q * g <= cap) {
     p.nc = nc_of(max_q * g);
@@ -641,7 +644,7 @@ AttnPlan attn_plan(int64_t t, int64_t n_seqs, int64_t hq, int64_t hk, int d, int
   size_t at = 0;
   if (p.nc) {
     const int64_t tiles = span / kAttnFewKeys + 10;
-    const int64_t units = n_seqs * hk * tiles;
+    const int64_t units = times(times(n_seqs, hk), tiles);
     p.ok = p.ok && units < limit;
     // two resident workgroups a compute unit, one at 256 values a head (their LDS; four at 64 values
     // would fit, but the pieces cost more than they hide: 16 x 5 drafted tokens 34 against 28 us)
@@ -656,15 +659,16 @@ AttnPlan attn_plan(int64_t t, int64_t n_seqs, int64_t hq, int64_t hk, int d, int
     const int64_t seqs = std::min<int64_t>(n_seqs, t * g / (p.few_rows + 1));
     const int64_t tiles = full + seqs;
     p.plan_tiles = (int)tiles;
-    p.ok = p.ok && tiles * hk < limit;
+    const int64_t grid = times(tiles, hk);
+    p.ok = p.ok && grid < limit;
     // whole items to workgroups where that fills them: two items or more each, or a last round that
     // is four fifths full (4096 tokens, 28 heads on 4: 448 items 151 us, cut into runs 181; 1000 tokens
     // at 32767, 32 heads on 8: 128 items would leave half the chip idle)
-    const int64_t items = full * hk, rounds = (items + slots - 1) / slots;
+    const int64_t items = times(full, hk), rounds = (items + slots - 1) / slots;
     if (items >= 2 * slots || (items > 0 && 5 * items >= 4 * slots * rounds) || tiles + n_seqs > 4096) {
-      p.items_tile = (int)(tiles * hk);
+      p.items_tile = (int)std::min(grid, limit - 1);
     } else {
-      p.ok = p.ok && tiles * hk * (span / kAttnTileKeys + 16) < limit;
+      p.ok = p.ok && times(grid, span / kAttnTileKeys + 16) < limit;
       p.nw_tile = (int)slots;
       p.join_tile = max_kv > kAttnTileKeys;
     }
