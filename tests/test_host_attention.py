@@ -191,3 +191,20 @@ def test_work_past_64_bits_is_refused_and_any_window_is_planned(lib):
             for t, max_q in ((n, 1), (min(4 * n, (1 << 30) - 1), 100)):
                 assert attend(lib, qh=h, out=h, c=c, t=t, n=n, max_q=max_q, pages=pages, ws_bytes=(1 << 63)) == UNSUPPORTED, (n, pages, t)
                 assert size(t, n, 1 << 19, 1 << 19, 128, max_q, pages, 1, 0) < (1 << 40)
+
+
+def test_matrix_results_are_first_read_by_the_compilers_own_instruction():
+    """The wait between a matrix product and the reader of its result is put in for instructions that the
+    compiler knows, not for inline ones.  Each running maximum over the scores (inline max3) therefore
+    begins with fmaxf of a value of the first and of the last product, and every step depends on it."""
+    import re
+
+    csrc = os.path.join(os.path.dirname(q.lib_path()), "..", "csrc")
+    for name, last in (("attn_few.hip", "sc[n][1]"), ("attn_tile.hip", "sc[NK - 1]")):
+        with open(os.path.join(csrc, name)) as f:
+            text = f.read()
+        first = re.findall(r"float mx = (.*);", text)
+        assert len(first) == 1 and first[0].startswith("fmaxf(sc") and last in first[0], (name, first)
+        steps = [m for m in re.findall(r"max3\(([^;]*);", text) if "sc[" in m]
+        assert steps and all(m.startswith("mx,") for m in steps), (name, steps)
+        assert not re.search(r"asm[^;]*\bsc\[", text)

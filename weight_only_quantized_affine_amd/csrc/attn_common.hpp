@@ -57,7 +57,10 @@ template <typename F> __device__ __forceinline__ float join16(float x, F f) {
   const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
   return f(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
-// The larger of three, ignoring NaN (fmaxf would first quiet each operand).
+// The largest of three, ignoring NaN (fmaxf would first quiet each operand).  The compiler puts no
+// wait between a matrix product and an inline instruction that reads its result: a chain over
+// scores begins with fmaxf of a value of each product, which is waited for, and every max3 takes
+// the chain's last result.
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));

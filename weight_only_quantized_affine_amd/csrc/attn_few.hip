@@ -265,10 +265,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few_kernel(const A
       u32x4_t p[NC];
 #pragma unroll
       for (int n = 0; n < NC; ++n) {
-        float mx = max3(sc[n][0][0], sc[n][0][1], sc[n][0][2]);
-        mx = max3(mx, sc[n][0][3], sc[n][1][0]);
-        mx = max3(mx, sc[n][1][1], sc[n][1][2]);
-        mx = max3(mx, sc[n][1][3], sc[n][1][3]);
+        float mx = fmaxf(sc[n][0][0], sc[n][1][0]);
+#pragma unroll
+        for (int r = 1; r < 4; ++r) mx = max3(mx, sc[n][0][r], sc[n][1][r]);
         mx = join32(join16(mx, MaxF()), MaxF()) * a.sl;
         if (__any(mx > m[n] + kLazy)) {
           const float mn = fmaxf(m[n], mx);

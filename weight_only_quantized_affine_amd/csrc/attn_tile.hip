@@ -402,10 +402,10 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
         for (int x = 0; x < 32; ++x)
           sc[x >> 4][x & 15] = ((x < 16 ? s0 : s1) >> (8 * ((x >> 2) & 3) + (x & 3)) & 1) ? sc[x >> 4][x & 15] : kNegInf;
       }
-      float mx = max3(sc[0][0], sc[0][1], sc[0][2]);
+      static_assert(NK == 2, "two score tiles");
+      float mx = fmaxf(sc[0][0], sc[NK - 1][0]);
 #pragma unroll
-      for (int x = 3; x < 16 * NK - 1; x += 2) mx = max3(mx, sc[x >> 4][x & 15], sc[(x + 1) >> 4][(x + 1) & 15]);
-      mx = max3(mx, sc[NK - 1][15], sc[NK - 1][15]);
+      for (int x = 1; x < 16; ++x) mx = max3(mx, sc[0][x], sc[NK - 1][x]);
       mx = join32(mx, MaxF()) * a.sl;
       if (__any(mx > m + kLazy)) {
         const float mn = fmaxf(m, mx);
