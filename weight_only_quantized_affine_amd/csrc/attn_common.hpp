@@ -81,14 +81,15 @@ __device__ __forceinline__ float join_factor(float m, float l, float mt) {
 }
 
 // What a row's O is multiplied by: 1 / (l + 2^(sink - m)).  A sink of -infinity is no term, one of
-// +infinity leaves nothing for the keys, and a row that saw nothing (m = -inf, l = 0) is zero with
-// any sink: neither infinity may meet the reference in a difference.
+// +infinity leaves nothing for the keys (f = 0), and a row that saw nothing (m = -inf, l = 0) is zero
+// with any sink: neither infinity's difference from the reference is used.
 __device__ __forceinline__ float attn_scale(const float* sinks, int head, float m, float l) {
-  const float sink = sinks ? sinks[head] * kLog2e : kNegInf;
-  if (sink == kNegInf) return l == 0.f ? 0.f : 1.f / l;
-  if (sink == -kNegInf) return 0.f;
-  const float mn = fmaxf(m, sink), f = join_factor(m, l, mn);
-  return f == 0.f ? 0.f : f / (l * f + exp2_fast(sink - mn));
+  float f = 1.f, z = l;
+  if (sinks) {
+    const float sink = sinks[head] * kLog2e, mn = fmaxf(m, sink);
+    if (sink != kNegInf) f = join_factor(m, l, mn), z = l * f + exp2_fast(sink - mn);
+  }
+  return f == 0.f || z == 0.f ? 0.f : f / z;
 }
 
 // A V row that some query rows of a tile see and others do not may hold infinities or NaN, and zero
