@@ -1,14 +1,16 @@
-// Shared parts of the paged attention kernels (attn_few.hip, attn_tile.hip): the split of the work over workgroups, the copy of cache rows into LDS and
-// the register tiles of the two products.
+// Shared parts of the paged attention kernels (attn_few.hip, attn_tile.hip): the split of the work
+// over workgroups, the copy of cache rows into LDS and the register tiles of the two products.
 //
-// Mathematics.  For one query row with scores s_j (log2 units: scale * log2(e) * q.k_j) the kernels
-// hold M (a reference not below the maximum by more than 2^kLazy), l = sum 2^(s_j - M) and
-// O = sum 2^(s_j - M) v_j in fp32, the weights 2^(s_j - M) rounded once to the cache's 16-bit type
-// (the matrix cores' operand) in the sum l as in O, so that the normalized weights sum to one; pieces of a row join as
-// sum_p 2^(M_p - M) O_p / sum_p 2^(M_p - M) l_p.  Both products run transposed, S^T = K Q^T and
-// O^T = V^T P^T, so that a lane holds one query column: the maximum, the sum and the rescaling of
-// a row are per-lane scalars, and the lane's scores are already the P^T operand of the second
-// product under a permutation of the keys that the V^T reads follow.
+// Mathematics: the softmax with a running maximum (Milakov and Gimelshein 2018).  For one query row
+// with scores s_j (log2 units: scale * log2(e) * q.k_j) the kernels hold M (a reference not below the
+// maximum by more than 2^kLazy), l = sum 2^(s_j - M) and O = sum 2^(s_j - M) v_j in fp32, the weights
+// 2^(s_j - M) rounded once to the cache's 16-bit type (the matrix cores' operand) in the sum l as in O,
+// so that the normalized weights sum to one; pieces of a row join as
+//   sum_p 2^(M_p - M) O_p / sum_p 2^(M_p - M) l_p.
+// Both products run transposed, S^T = K Q^T and O^T = V^T P^T, so that a lane holds one query column:
+// the maximum, the sum and the rescaling of a row are per-lane scalars, and the lane's scores are
+// already the P^T operand of the second product under a permutation of the keys that the V^T reads
+// follow.
 #pragma once
 #include "head_common.hpp"
 
@@ -163,14 +165,18 @@ template <int N> __device__ __forceinline__ int attn_tiles(int lo, int hi, int& 
 // infinity or a NaN left in an unused slot would not be.
 __device__ __attribute__((aligned(16))) static uint32_t kZeroRow[128] = {};
 
-// Starts a copy of 16 bytes a lane into LDS, lane l's from src to dst + 16 l (dst is uniform).
-// Written as an instruction because the compiler,
-// which cannot tell the stages apart, would wait for every copy in flight at each LDS read; the
-// kernels wait by count (attn_wait_vm) for the stage they read.  The copy writes no register; the
-// wait state between m0 and its use is in the text.
 __device__ __forceinline__ uint32_t lds_at(const uint8_t* p) {
   return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(at_lds_void*)p);
 }
+// The copies set m0, which the compiler keeps for itself: it never holds a value there over other
+// instructions, and the clobber list keeps it from placing its own use of m0 around them.  It warns
+// of the name in the list.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+// Starts a copy of 16 bytes a lane into LDS, lane l's from src to dst + 16 l (dst is uniform).
+// Written as an instruction because the compiler, which cannot tell the stages apart, would wait for
+// every copy in flight at each LDS read; the kernels wait by count (attn_wait_vm) for the stage they
+// read.  The copy writes no register; the wait state between m0 and its use is in the text.
 //
 // NT: the non-temporal policy, for rows that no other workgroup reads (few-row kernel: one sequence
 // of 131071 114 -> 102 us, 64 ragged ones 163 -> 147 us; the tile kernel's row tiles share their
@@ -220,6 +226,7 @@ __device__ __forceinline__ void copy16_from(int64_t base, uint32_t off0, uint32_
                  : "s"(lds_at(dst)), "v"(off0), "s"(base)
                  : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 // The cache rows of a tile that one wave copies, U runs of R rows (positions base .. base + U R; R
 // divides 16 and base is a multiple of R), K and V alike; tiles are STEP positions apart.

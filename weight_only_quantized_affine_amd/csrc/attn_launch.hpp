@@ -6,7 +6,8 @@
 
 namespace ql {
 
-// Unsigned division of dividends below 2^31 by a fixed divisor: n / d = (mulhi(n, mul) + n) >> sh with
+// Unsigned division of dividends below 2^31 by a fixed divisor, by multiplication (Granlund and
+// Montgomery 1994): n / d = (mulhi(n, mul) + n) >> sh with
 // sh = ceil(log2 d) and mul = floor(2^32 (2^sh - d) / d) + 1.
 struct FastDiv {
   uint32_t mul, sh;
