@@ -301,11 +301,12 @@ def sampled(p, got, places, **kw):
     """Rows (sequence, token, head) of got against the oracle, each as one token of its own."""
     for s, i, h in places:
         n, kv = p.lens[s]
-        row, kh = int(p.cu[s]) + i, h // (p.q.shape[1] // p.k.shape[2])
+        row, kh, page = int(p.cu[s]) + i, h // (p.q.shape[1] // p.k.shape[2]), p.k.shape[1]
+        seen = kv - n + i + 1
         one = Problem.__new__(Problem)
-        one.lens, one.dtype, one.cu = [(1, kv - n + i + 1)], p.dtype, np.array([0, 1], dtype=np.int32)
-        one.q, one.table = p.q[row:row + 1, h:h + 1], p.table[s:s + 1]
-        one.k, one.v = p.k[:, :, kh:kh + 1], p.v[:, :, kh:kh + 1]
+        one.lens, one.dtype, one.cu = [(1, seen)], p.dtype, np.array([0, 1], dtype=np.int32)
+        one.q, pages = p.q[row:row + 1, h:h + 1], p.table[s, :-(-seen // page)].long().to(DEV)
+        one.k, one.v, one.table = p.k[pages, :, kh:kh + 1], p.v[pages, :, kh:kh + 1], torch.arange(len(pages))[None]
         kw_one = dict(kw, sinks=kw["sinks"][h:h + 1]) if kw.get("sinks") is not None else kw
         try:
             close(got[row:row + 1, h:h + 1], one.oracle(**kw_one), p.q.shape[2], p.dtype)
@@ -347,3 +348,139 @@ def test_infinite_sinks_of_whole_row_tiles():
     assert (got[:300] == 0).all() and (got[:, 1::3] == 0).all()
     assert torch.equal(got[:, ::3], p.run()[:, ::3])
     sampled(p, got, [(0, 300, 0), (0, 2199, 3), (1, 0, 6), (1, 1000, 2), (1, 2099, 31)], sinks=sinks)
+
+
+class Large(Problem):
+    """As Problem, with caches of finite values made on the GPU."""
+
+    def __init__(self, lens, hq, hk, d, page, dtype, seed=0):
+        g, c = torch.Generator(device=DEV).manual_seed(seed), torch.Generator().manual_seed(seed)
+        self.lens, self.dtype = lens, dtype
+        need = [-(-kv // page) for _, kv in lens]
+        self.table = torch.full((len(lens), max(need)), -1, dtype=torch.int32)
+        order, at = torch.randperm(sum(need), generator=c).int(), 0
+        for s, m in enumerate(need):
+            self.table[s, :m] = order[at:at + m]
+            at += m
+        self.k, self.v = (torch.randn(sum(need), page, hk, d, generator=g, device=DEV).to(dtype) for _ in range(2))
+        self.cu = np.concatenate([[0], np.cumsum([n for n, _ in lens])]).astype(np.int32)
+        self.q = (torch.randn(int(self.cu[-1]), hq, d, generator=g, device=DEV) * 2).to(dtype)
+        self.sinks = torch.randn(hq, generator=c).to(DEV)
+
+
+@pytest.mark.parametrize("n_seqs,hk,d,dtype", [(64, 8, 64, BF), (100, 8, 128, HF), (300, 3, 64, HF), (60, 4, 256, BF), (400, 1, 128, BF)])
+def test_long_runs_of_few_rows(n_seqs, hk, d, dtype):
+    """So many key tiles (20 a workgroup and more) that an item's start and end are counted in the division:
+    pieces recorded by item (up to as many as workgroups) and by workgroup, up to 256 sequences and more."""
+    r = np.random.default_rng(n_seqs)
+    tiles = 20 * (256 if d == 256 else 512) * 1.3 / hk / n_seqs
+    lens = [(1 + (s % 7 == 3), int(128 * tiles * x) + 1) for s, x in enumerate(r.uniform(0.3, 1.7, n_seqs))]
+    lens[1], lens[n_seqs // 2], lens[-1] = (1, 1), (0, 900), (2, 1)
+    assert sum(-(-kv // 128) for n, kv in lens if n) * hk >= 20 * (256 if d == 256 else 512)
+    p = Large(lens, 2 * hk, hk, d, 16, dtype, seed=18)
+    got = p.run()
+    assert torch.isfinite(got).all()
+    seqs = sorted(set(range(0, n_seqs, max(1, n_seqs // 40))) | {n_seqs - 2})
+    sampled(p, got, [(s, lens[s][0] - 1, (5 * s) % (2 * hk)) for s in seqs if lens[s][0] and lens[s][1] >= lens[s][0]])
+    assert (got[int(p.cu[-1]) - 2] == 0).all()  # two tokens, one position: the first sees nothing
+    # every (token, head) against the same sequence by itself, which is divided otherwise
+    for s in seqs[::8]:
+        if lens[s][0]:
+            a, b = int(p.cu[s]), int(p.cu[s + 1])
+            one = q.qlinear_paged_attention(p.q[a:b], p.k, p.v, p.table[s:s + 1].to(DEV), torch.tensor([0, b - a], dtype=torch.int32, device=DEV),
+                                            torch.tensor([lens[s][1]], dtype=torch.int32, device=DEV), max_q=b - a)
+            # weights rounded under two references (half a step each), then both outputs
+            assert ((one.float() - got[a:b].float()).abs() <= 4 * torch.finfo(dtype).eps).all()
+
+
+WHOLE = [(2500, 2600), (1, 700), (0, 5), (1700, 1700), (1, 1), (60, 30), (0, 0), (3, 9)]
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("dtype,page,window,sinks", [(BF, 16, 0, False), (HF, 24, 500, True), (BF, 1, 70, True), (HF, 128, 0, True)])
+def test_whole_row_tiles(d, dtype, page, window, sinks):
+    """Row tiles of two query heads a kv head, none split, with sequences that are short, empty or before
+    their first position among them, and more workgroups than row tiles."""
+    p = Problem(WHOLE, 32, 16, d, page, dtype, seed=19)
+    kw = dict(window=window, sinks=p.sinks if sinks else None)
+    got = p.run(**kw)
+    rows = [(0, i, (i // 16) % 32) for i in (0, 1, 63, 64, 127, 128, 255, 999, 1791, 2432, 2498, 2499)]
+    rows += [(3, i, (7 * i) % 32) for i in (0, 1, 2, 69, 70, 500, 1600, 1664, 1699)]
+    rows += [(1, 0, 3), (4, 0, 31), (5, 30, 8), (5, 59, 9), (7, 0, 1), (7, 2, 30)]
+    sampled(p, got, rows, **kw)
+    at = int(p.cu[5])
+    assert (got[at:at + 30] == 0).all()
+    # a NaN, then an infinity, in V of a position that is new: the rows before it do not see it
+    j = 2600 - 1 - 1200
+    where = (int(p.table[0, j // page]), j % page, 3, 5)
+    first, end = 2500 - 1 - 1200, min(2500, 2500 - 1 - 1200 + (window or 2500))
+    for value in (float("nan"), float("inf")):
+        p.v[where] = value
+        odd = p.run(**kw)
+        mask = torch.ones_like(got, dtype=torch.bool)
+        mask[first:end, 6:8, 5] = False
+        assert torch.equal(odd[mask], got[mask])
+        assert not torch.isfinite(odd[first, 6:8, 5]).any()
+
+
+def test_more_sequences_than_a_plan_holds():
+    r = np.random.default_rng(20)
+    lens = [(20, int(20 + e)) for e in r.integers(0, 60, 4100)]
+    lens[7], lens[4099] = (0, 3), (19, 30)
+    p = Large(lens, 1, 1, 64, 16, BF, seed=20)
+    got = p.run()
+    sampled(p, got, [(s, i, 0) for s, i in zip([*range(0, 4100, 205), 4098, 4099], [*range(20), 19, 18]) if lens[s][0] > i])
+    assert torch.isfinite(got).all()
+
+
+@pytest.mark.parametrize("lens", [[(1, 5000)], [(3, 900), (2, 66)], [(200, 517)], [(70, 3000), (1, 400)], [(300, 300), (40, 5000)]])
+@pytest.mark.parametrize("d,dtype", [(64, BF), (128, HF), (256, BF)])
+def test_keys_that_are_not_finite_reach_every_row_that_sees_them(lens, d, dtype):
+    p = Problem(lens, 4, 2, d, 16, dtype, seed=21)
+    want = p.run()
+    s, (n, kv) = len(lens) - 1, lens[-1]
+    j = kv - 1 - (n - 1) // 2
+    first = int(p.cu[s]) + j - (kv - n)  # first row that sees j
+    keep = p.k.clone()
+    # a whole row: q.k is NaN, since q has values of both signs
+    for value in (float("nan"), float("inf"), float("-inf")):
+        p.k[int(p.table[s, j // 16]), j % 16, 1] = value
+        got = p.run()
+        assert torch.isnan(got[first:int(p.cu[s + 1]), 2:]).all()
+        assert torch.equal(got[:, :2], want[:, :2]) and torch.equal(got[:first, 2:], want[:first, 2:])
+    # one infinite value: a score of +-infinity, NaN or no weight
+    p.k.copy_(keep)
+    p.k[int(p.table[s, j // 16]), j % 16, 1, 3] = float("inf")
+    got = p.run()
+    q3 = p.q[first:int(p.cu[s + 1]), 2:, 3]
+    rows = got[first:int(p.cu[s + 1]), 2:]
+    assert torch.isnan(rows[q3 > 0]).all() and torch.isfinite(rows[q3 < 0]).all()
+    for i in range(first - int(p.cu[s]), n, max(1, n // 9)):
+        for h in (2, 3):
+            if float(p.q[int(p.cu[s]) + i, h, 3]) < 0:
+                sampled(p, got, [(s, i, h)])
+    # every score NaN, in every piece
+    p.k.fill_(float("nan"))
+    got = p.run()
+    sees = torch.cat([torch.arange(a) >= a - b for a, b in lens]).to(DEV)
+    assert torch.isnan(got[sees]).all() and (got[~sees] == 0).all()
+
+
+@pytest.mark.parametrize("lens", [[(1, 40000)], [(3, 20000), (1, 100)], [(40, 40000)]])
+def test_fp16_weights_below_the_normal_range_count(lens):
+    """One key of weight 1 with v = 0 and many of weight 2^-17 with v = 1: the sum of the small ones, which
+    are exact in fp16, is a share of it all."""
+    p = Problem(lens, 2, 1, 64, 16, HF, seed=22)
+    p.q.zero_()
+    p.q[..., 0] = 1
+    p.k.zero_()
+    p.v.fill_(1.0)
+    for s in range(len(lens)):
+        p.k[int(p.table[s, 0]), 0, 0, 0] = 17.0
+        p.v[int(p.table[s, 0]), 0] = 0.0
+    got = f64(p.run(scale=float(np.log(2.0))))
+    for s, (n, kv) in enumerate(lens):
+        for i in range(n):
+            small = (kv - n + i) * 2.0 ** -17
+            o = small / (1 + small)
+            assert np.abs(got[int(p.cu[s]) + i] - o).max() <= (2 ** -11 + 2 ** -16) * o
