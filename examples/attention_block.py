@@ -8,9 +8,9 @@ weights are one 4-bit matrix, so a step is
     qlinear_paged_attention       the new tokens over everything cached
     qlinear_gemm / qlinear_gemv   heads -> hidden
 
-Run on a GPU: ``python examples/attention_block.py`` prefills three prompts in chunks next to a
-sequence that already decodes, then decodes all of them from one captured graph, and checks that the
-outputs equal those of each whole sequence in a single call.
+Run on a GPU: ``python examples/attention_block.py`` prefills four prompts in chunks, those that are
+through decoding next to the chunks of the others, then decodes all of them from one captured graph,
+and checks that the outputs equal those of each whole sequence in a single call.
 """
 from __future__ import annotations
 
@@ -91,7 +91,10 @@ class AttentionBlock:
 
 def main(prompts=(300, 41, 130, 7), chunk=128, steps=6, seed=1):
     block = AttentionBlock()
-    n_seqs, total = len(prompts), [p + steps for p in prompts]
+    n_seqs, rounds = len(prompts), max(-(-p // chunk) for p in prompts)
+    # a prompt that takes fewer chunks than the longest decodes a token in each round that is left
+    first = [p + rounds - -(-p // chunk) for p in prompts]
+    total = [n + steps for n in first]
     g = torch.Generator(device="cuda").manual_seed(seed)
     tokens = [torch.randn((n, 1024), generator=g, device="cuda").bfloat16() for n in total]
 
@@ -104,10 +107,10 @@ def main(prompts=(300, 41, 130, 7), chunk=128, steps=6, seed=1):
         cache = new_cache()
         whole.append(block(x, cache, *cache.extend([x.shape[0] if i == s else 0 for i in range(n_seqs)]), x.shape[0]))
 
-    # prompts in chunks, all sequences in one batch; those whose prompt is through wait
+    # prompts in chunks, all sequences in one batch; those whose prompt is through decode
     cache, got = new_cache(), [[] for _ in prompts]
-    while any(cache.lens[s] < p for s, p in enumerate(prompts)):
-        counts = [min(chunk, p - cache.lens[s]) for s, p in enumerate(prompts)]
+    for _ in range(rounds):
+        counts = [min(chunk, p - cache.lens[s]) if cache.lens[s] < p else 1 for s, p in enumerate(prompts)]
         x = torch.cat([tokens[s][cache.lens[s]:cache.lens[s] + n] for s, n in enumerate(counts)])
         y = block(x, cache, *cache.extend(counts), max(counts))
         for s, part in enumerate(y.split(counts)):
@@ -118,7 +121,7 @@ def main(prompts=(300, 41, 130, 7), chunk=128, steps=6, seed=1):
     step, graph, y = None, None, None
     for i in range(steps):
         new = cache.extend([1] * n_seqs)
-        x.copy_(torch.stack([tokens[s][p + i] for s, p in enumerate(prompts)]))
+        x.copy_(torch.stack([tokens[s][n + i] for s, n in enumerate(first)]))
         if graph is None:
             step = new
             side = torch.cuda.Stream()
