@@ -3,7 +3,7 @@
 //
 // Mathematics: the softmax with a running maximum (Milakov and Gimelshein 2018).  For one query row
 // with scores s_j (log2 units: scale * log2(e) * q.k_j) the kernels hold M (a reference not below the
-// maximum by more than 2^kLazy), l = sum 2^(s_j - M) and O = sum 2^(s_j - M) v_j in fp32, the weights
+// maximum by more than kLazy), l = sum 2^(s_j - M) and O = sum 2^(s_j - M) v_j in fp32, the weights
 // 2^(s_j - M) rounded once to the cache's 16-bit type (the matrix cores' operand) in the sum l as in O,
 // so that the normalized weights sum to one; pieces of a row join as
 //   sum_p 2^(M_p - M) O_p / sum_p 2^(M_p - M) l_p.

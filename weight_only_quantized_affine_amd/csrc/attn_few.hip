@@ -11,7 +11,7 @@
 // the scores are computed.  The waves' sums join in LDS at the end of an item.
 //
 // Measured (bf16, 32 heads on 8 of 128): one sequence of 131071 positions, 537 MB in 94 us, 5.7 TB/s
-// (a plain read of 1 GB reaches 5.9 here); 64 ragged sequences, 762 MB in 135 us, 5.6 TB/s; one
+// (a plain read of 1 GB reaches 5.9 here); 64 ragged sequences, 762 MB in 133 us, 5.7 TB/s; one
 // sequence of 1025 positions with 16 heads on 8, 12 us, the latency of two launches and of the chain
 // lengths, page ids, keys.
 #include "attn_common.hpp"

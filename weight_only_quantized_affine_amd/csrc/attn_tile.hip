@@ -9,15 +9,19 @@
 // barrier a tile, met by the first four waves after their products and by the others after their
 // weights, keeps the two groups half a tile apart, so that one multiplies while the other is on the
 // vector units.  (Left to themselves the two waves of a SIMD fall into step and wait for the same
-// unit: matrix cores 42 % busy, vector units 37 %, never together, 646 us against 490 for 1000
+// unit: matrix cores 42 % busy, vector units 37 %, never together, 646 us against 495 for 1000
 // tokens at 32767, 32 heads on 8 of 128.  A barrier at every half tile: 520.  Now 51 %, what is left
 // is each wave's own chain of weights and products; two waves a SIMD fill the registers.)  The
-// first four waves copy the K and V tiles into LDS, a period ahead of their first reader.
+// first four waves copy the K and V tiles into LDS, a period ahead of their first reader
+// (attn_order.hpp has the order of it all).
 //
-// At 256 values a head the registers hold one wave a SIMD: 4 waves, all in step.
+// At 256 values a head the registers hold one wave a SIMD, 4 waves, all in step: weights and products
+// take turns, matrix cores 34 % busy.  At 64 values the vector units bound it: a tile takes as many
+// exponentials as at 128 for half the products (matrix cores 34 % busy, vector issue 55 %).
 //
-// Measured (bf16, 32 heads on 8 of 128): 4096 tokens 146 us, 940 TFLOP/s; 1000 tokens at 32767
-// 490 us, 1080 TFLOP/s; a large bf16 library product reaches 1219 here.
+// Measured (bf16, 32 heads on 8 of 128): 4096 tokens 143 us, 960 TFLOP/s; 1000 tokens at 32767
+// 495 us, 1070 TFLOP/s; a large bf16 library product reaches 1219 here.  The same with 64 heads on 16
+// of 64: 206 us, 670 and 639 us, 830; with 16 heads on 4 of 256: 172 us, 800 and 648 us, 820.
 //
 // Work split.  With enough items (sequence, kv head, row tile) to fill the chip, one workgroup each,
 // the longest first, kv heads fastest so that a head's tiles run on one XCD and share its L2.  Else
