@@ -400,6 +400,107 @@ ql_status qlinear_paged_attention(const ql_heads* q, const ql_heads* out, ql_dty
                                   int64_t max_q, float scale, int64_t window, const float* sinks, void* workspace,
                                   size_t ws_bytes, void* stream);
 
+/* ---- The same over a cache in 4 bits.
+ *
+ * A row of d values of k or v is d/2 bytes of codes, as the affine rows at 4 bits (eight codes a word, the
+ * lowest bits first), and d / group_size words of two fp16 numbers, the group's scale in the low half and
+ * its bias in the high half: value = code * scale + bias.  Four arrays of n_pages pages of page_size slots,
+ * hk heads; k_codes and v_codes share their strides in BYTES (multiples of 16), k_groups and v_groups
+ * theirs in WORDS.  Codes 16-byte, words 4-byte aligned.  group_size 32, 64 or 128; d a multiple of it. */
+typedef struct {
+  void* k_codes;
+  void* v_codes;
+  uint32_t* k_groups;
+  uint32_t* v_groups;
+  int64_t n_pages, page_size, hk, d, group_size;
+  int64_t page_stride, token_stride, head_stride;
+  int64_t group_page_stride, group_token_stride, group_head_stride;
+} ql_paged_cache4;
+
+/* qlinear_kv_append into such a cache: the rows of norm_rope(k) and of v, in dtype, are quantized by the rule
+ * of qlinear_quantize (fp32, fp16 parameters) and stored.  A row of k is worked out in 64 bits and
+ * rounded to fp32 and from there to dtype, so that its codes do not hang on the order of a sum.  A group
+ * that holds a NaN or a magnitude past 2^15 is stored with scale 0 and bias NaN.  d a multiple of
+ * group_size up to 512; the other arguments as qlinear_kv_append. */
+ql_status qlinear_kv_append_4bit(const ql_heads* q, const ql_heads* q_out, const ql_heads* k, const ql_heads* v,
+                                 const ql_paged_cache4* cache, const int64_t* slots, ql_dtype dtype, int64_t t,
+                                 const ql_norm_rope* nr, void* stream);
+
+/* The values of cached rows: k_out[i] and v_out[i] [t, hk, d] in dtype (16 bits) get the rows at slots[i], each
+ * value code * scale + bias in fp32 rounded once; a slot outside [0, n_pages * page_size) gives zeros.  Slots
+ * may repeat.  d as in qlinear_kv_append_4bit. */
+ql_status qlinear_kv_read_4bit(const ql_paged_cache4* cache, const int64_t* slots, int64_t t, const ql_heads* k_out,
+                               const ql_heads* v_out, ql_dtype dtype, void* stream);
+
+/* qlinear_paged_attention over such a cache; arguments, masks, sinks, limits and workspace as there, dtype that of
+ * q and out.  Cached values enter the products rounded to fp16 (values past 65504 are infinite, below 2^-14
+ * they keep an absolute 2^-25), q with 11 significant bits (bf16: exact), the softmax weights rounded to fp16. */
+size_t qlinear_paged_attention_4bit_workspace_size(int64_t t, int64_t n_seqs, int64_t hq, int64_t hk, int64_t d,
+                                                   int64_t max_q, int64_t max_pages, int64_t page_size, int64_t window);
+ql_status qlinear_paged_attention_4bit(const ql_heads* q, const ql_heads* out, ql_dtype dtype, int64_t t,
+                                       const ql_paged_cache4* cache, const int32_t* block_table, int64_t table_stride,
+                                       int64_t max_pages, const int32_t* cu_q, const int32_t* kv_lens, int64_t n_seqs,
+                                       int64_t max_q, float scale, int64_t window, const float* sinks, void* workspace,
+                                       size_t ws_bytes, void* stream);
+
+/* ---- The tables of a batch, on the device.
+ *
+ * One step of a paged cache for n_seqs sequences: sequence s has lens[s] cached tokens in the pages of
+ * block_table[s] and brings counts[s] new ones (0: it rests; below 0: it is through, its pages go back and
+ * its length becomes 0).  The pages that the new tokens need are taken from a list of free ones.
+ *   released   the pages of sequences with counts[s] < 0, sequences and pages in order, are put on top of
+ *              free_pages[0 .. *free_count);
+ *   taken      sequences and pages in order, from the top of that list down, into block_table;
+ *   lens_out   lens + counts (0 where released);  free_count_out: what is left of the list;
+ *   cu_q       [n_seqs + 1]: the exclusive prefix of the new tokens;
+ *   positions, slots  [rows]: for token i of sequence s its position lens[s] + i - cu_q[s] and its slot
+ *              page * page_size + place; 0 and -1 in the rows behind the last token;
+ *   info       [4]: tokens laid out, pages taken, why (below), free pages left.
+ * A step that cannot be done changes nothing: lens_out = lens, free_count_out = free_count, cu_q zeros, positions
+ * zeros, slots -1, info = {0, 0, why, free_count}, where why is the sum of
+ *   1  more tokens than rows;                    2  fewer free pages than needed;
+ *   4  a length below 0 or past max_pages * page_size, before or after;
+ *   8  *free_count below 0, or the list with what is given back past free_cap entries.
+ * Without a list (free_pages = NULL, free_cap = 0, free_count and free_count_out NULL) block_table holds every
+ * page already: nothing is taken or given back, and info[3] is 0.
+ * counts, lens int32 [n_seqs], block_table int32 rows of max_pages table_stride apart, free_pages int32 [free_cap],
+ * free_count int32 [1]: DEVICE memory.  lens_out may be lens and free_count_out may be free_count; nothing else
+ * overlaps.  Entries of free_pages and block_table are not looked at, only moved.  n_seqs < 2^24,
+ * rows < 2^31, max_pages * page_size < 2^31. */
+ql_status qlinear_kv_extend(const int32_t* counts, const int32_t* lens, int64_t n_seqs, int32_t* block_table,
+                            int64_t table_stride, int64_t max_pages, int64_t page_size, int32_t* free_pages,
+                            int64_t free_cap, const int32_t* free_count, int32_t* lens_out, int32_t* free_count_out,
+                            int32_t* cu_q, int64_t* positions, int64_t* slots, int64_t rows, int32_t* info,
+                            void* stream);
+
+/* ---- Around routed experts (qlinear_route, qlinear_apply_experts).
+ *
+ * The experts of each token from its router logits [t, e] (any ql_dtype, rows row_stride elements apart).  In 64 bits:
+ *   p = softmax(logits) over all e, or, with sigmoid != 0, 1 / (1 + e^-logit);   c = p + bias (fp32 [e], or NULL);
+ *   the experts lie in n_groups groups of e / n_groups neighbours; a group's score is its largest c, or with
+ *   group_top = 2 the sum of its two largest; the top_groups best groups stay;
+ *   ids[t]  the k largest c among the experts of those groups, in decreasing order;
+ *   weights[t] = scale * p of them, divided by the sum of the k p where renormalize != 0 (0 where it is 0).
+ * Ties go to the lowest index.  A NaN logit counts as -infinity; where the largest logit is infinite, the infinite
+ * ones share the softmax; a row of nothing but -infinity has p = 0.  ids int64 [t, k] are what
+ * qlinear_apply_experts takes, weights fp32 [t, k].  n_rows: NULL, or a DEVICE int32: the rows from *n_rows on get
+ * ids -1 and weights 0 (the padding of a captured batch).
+ * 1 <= e <= 1024, 1 <= k <= min(64, the experts of top_groups groups), n_groups divides e and is at most 64; with
+ * one group top_groups must be 1.  logits aligned to their type, ids 8-byte, the others 4-byte. */
+ql_status qlinear_select_experts(const void* logits, ql_dtype dtype, int64_t t, int64_t e, int64_t row_stride,
+                                 const float* bias, int sigmoid, int64_t n_groups, int64_t top_groups, int group_top,
+                                 int64_t k, int renormalize, float scale, const int32_t* n_rows, int64_t* ids,
+                                 float* weights, void* stream);
+
+/* The experts' outputs of each token, weighted and summed: for y [t * k, n] (the output of
+ * qlinear_apply_experts with a token's k positions side by side), weights fp32 [t, k] and residual [t, n] or NULL,
+ *   out[i, :] = residual[i, :] + sum_j weights[i, j] y[i * k + j, :]
+ * in fp32, residual first and j in order, rounded once.  Where ids (int64 [t, k], or NULL) lies outside [0, e) the
+ * position adds nothing, whatever y and weights hold.  y, residual and out share dtype (any ql_dtype) and are
+ * contiguous, aligned to their type; out may be residual and overlaps nothing else.  1 <= k <= 64. */
+ql_status qlinear_combine_experts(const void* y, ql_dtype dtype, const float* weights, const int64_t* ids, int64_t e,
+                                  const void* residual, int64_t t, int64_t k, int64_t n, void* out, void* stream);
+
 /* Message of the last failing call on this thread ("" after a successful call).  Errors name the
  * offending argument, as the Nx_quant API docs' constructors and products name the part they
  * reject (Weights; Products, "Raises Invalid_argument ... naming the part"). */

@@ -48,6 +48,14 @@ __all__ = [
     "qlinear_kv_append",
     "qlinear_paged_attention",
     "qlinear_paged_attention_workspace_size",
+    "qlinear_paged_cache_4bit",
+    "qlinear_kv_append_4bit",
+    "qlinear_kv_read_4bit",
+    "qlinear_paged_attention_4bit",
+    "qlinear_paged_attention_4bit_workspace_size",
+    "qlinear_kv_extend",
+    "qlinear_select_experts",
+    "qlinear_combine_experts",
     "qlinear_version",
 ]
 
@@ -105,6 +113,13 @@ class _PagedCache(ctypes.Structure):
         for f in ("n_pages", "page_size", "hk", "d", "page_stride", "token_stride", "head_stride")]
 
 
+class _PagedCache4(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in ("k_codes", "v_codes", "k_groups", "v_groups")] + [
+        (f, ctypes.c_int64)
+        for f in ("n_pages", "page_size", "hk", "d", "group_size", "page_stride", "token_stride", "head_stride",
+                  "group_page_stride", "group_token_stride", "group_head_stride")]
+
+
 class _NormRope(ctypes.Structure):
     _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("w_dtype", ctypes.c_int),
                 ("eps", ctypes.c_float), ("positions", ctypes.c_void_p), ("cos_sin", ctypes.c_void_p),
@@ -140,6 +155,15 @@ _SIGNATURES = {
     "qlinear_paged_attention_workspace_size": (_SZ, [_I64] * 9),
     "qlinear_paged_attention": (_INT, [_P, _P, _INT, _I64, _P, _P, _I64, _I64, _P, _P, _I64, _I64, ctypes.c_float, _I64,
                                        _P, _P, _SZ, _P]),
+    "qlinear_kv_append_4bit": (_INT, [_P, _P, _P, _P, _P, _P, _INT, _I64, _P, _P]),
+    "qlinear_kv_read_4bit": (_INT, [_P, _P, _I64, _P, _P, _INT, _P]),
+    "qlinear_paged_attention_4bit_workspace_size": (_SZ, [_I64] * 9),
+    "qlinear_paged_attention_4bit": (_INT, [_P, _P, _INT, _I64, _P, _P, _I64, _I64, _P, _P, _I64, _I64, ctypes.c_float,
+                                            _I64, _P, _P, _SZ, _P]),
+    "qlinear_kv_extend": (_INT, [_P, _P, _I64, _P, _I64, _I64, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _I64, _P, _P]),
+    "qlinear_select_experts": (_INT, [_P, _INT, _I64, _I64, _I64, _P, _INT, _I64, _I64, _INT, _I64, _INT, ctypes.c_float,
+                                      _P, _P, _P, _P]),
+    "qlinear_combine_experts": (_INT, [_P, _INT, _P, _P, _I64, _P, _I64, _I64, _I64, _P, _P]),
     "qlinear_last_error": (ctypes.c_char_p, []),
     "qlinear_version": (ctypes.c_char_p, []),
 }
@@ -474,8 +498,8 @@ def qlinear_apply_experts_noalloc(fmt: int, w0, w1, ids, x, *, n: int, k: int, y
 class _Args(threading.local):
     def __init__(self):
         self.q, self.q_out, self.k, self.v = _Heads(), _Heads(), _Heads(), _Heads()
-        self.cache, self.nr = _PagedCache(), _NormRope()
-        self.at = {n: ctypes.addressof(getattr(self, n)) for n in ("q", "q_out", "k", "v", "cache", "nr")}
+        self.cache, self.cache4, self.nr = _PagedCache(), _PagedCache4(), _NormRope()
+        self.at = {n: ctypes.addressof(getattr(self, n)) for n in ("q", "q_out", "k", "v", "cache", "cache4", "nr")}
 
 
 _ARGS = _Args()
@@ -534,6 +558,52 @@ def _paged_cache(c: _PagedCache, k_cache, v_cache, d: int, dtype, device: int):
     c.page_stride = sk[0] if shape[0] > 1 else 0
     c.token_stride = sk[1] if shape[1] > 1 else 0
     c.head_stride = sk[2] if shape[2] > 1 else 0
+
+
+def _block_table(table, device: int):
+    """(sequences, pages of a row, stride of the rows) of a block table."""
+    if table.dim() != 2 or table.dtype is not _torch().int32:
+        raise QLError(3, "block_table must be int32 [n_seqs, max_pages]")
+    n_seqs, max_pages = table.shape
+    row, place = table.stride()
+    if place != 1 and max_pages > 1:
+        raise QLError(2, "block_table's rows must be contiguous")
+    _same_device(table, "block_table", device)
+    return n_seqs, max_pages, row if n_seqs > 1 else max_pages
+
+
+def _paged_cache4(c: _PagedCache4, cache, d: Optional[int], device: int):
+    """Fill c from (k_codes, k_groups, v_codes, v_groups)."""
+    torch = _torch()
+    if len(cache) != 4:
+        raise QLError(2, "cache must be (k_codes, k_groups, v_codes, v_groups)")
+    kc, kg, vc, vg = cache
+    if any(x.dtype is not torch.int32 for x in (kc, vc)) or any(x.dtype is not torch.float16 for x in (kg, vg)):
+        raise QLError(3, "the cache's codes must be int32 and its groups float16")
+    shape, groups = kc.shape, kg.shape
+    if len(shape) != 4 or vc.shape != shape or (d is not None and shape[3] * 8 != d):
+        raise QLError(2, f"the codes must both be [n_pages, page_size, heads, {d}/8]")
+    if len(groups) != 5 or vg.shape != groups or groups[:3] != shape[:3] or groups[3] < 1 or groups[4] != 2 or \
+            shape[3] * 8 % groups[3]:
+        raise QLError(2, f"the groups must both be {list(shape[:3])} + [groups of a row, 2]")
+    for a, b, inner, name in ((kc, vc, 1, "codes"), (kg, vg, 2, "groups")):
+        sa, sb = a.stride(), b.stride()
+        if sa != sb and any(x != y for x, y, n in zip(sa, sb, a.shape) if n > 1):
+            raise QLError(2, f"the {name} of k and v must have the same strides")
+        want = (1,) if inner == 1 else (2, 1)
+        if any(x != y for x, y, n in zip(sa[-inner:], want, a.shape[-inner:]) if n > 1):
+            raise QLError(2, f"the last dimension{'s' if inner > 1 else ''} of the {name} must be contiguous")
+    for x, name in zip(cache, ("k_codes", "k_groups", "v_codes", "v_groups")):
+        _same_device(x, name, device)
+    c.k_codes, c.k_groups, c.v_codes, c.v_groups = (x.data_ptr() for x in cache)
+    c.n_pages, c.page_size, c.hk, c.d = shape[0], shape[1], shape[2], shape[3] * 8
+    c.group_size = c.d // groups[3]
+    sk, sg = kc.stride(), kg.stride()
+    c.page_stride, c.token_stride, c.head_stride = (4 * x if n > 1 else 0 for x, n in zip(sk, shape[:3]))
+    steps = [x if n > 1 else 0 for x, n in zip(sg, shape[:3])]
+    if any(x % 2 for x in steps):
+        raise QLError(4, "the strides of the groups must be whole words")
+    c.group_page_stride, c.group_token_stride, c.group_head_stride = (x // 2 for x in steps)
 
 
 def _norm_rope(n: _NormRope, t: int, d: int, q_weight, k_weight, eps, positions, cos_sin, interleaved, device: int):
@@ -651,13 +721,7 @@ def qlinear_paged_attention(q, k_cache, v_cache, block_table, cu_q, kv_lens, *, 
     _heads(args.q, q, "q", t, d, dtype, device)
     _heads(args.q_out, out, "out", t, d, dtype, device)
     _paged_cache(args.cache, k_cache, v_cache, d, dtype, device)
-    if block_table.dim() != 2 or block_table.dtype is not torch.int32:
-        raise QLError(3, "block_table must be int32 [n_seqs, max_pages]")
-    n_seqs, max_pages = block_table.shape
-    row, place = block_table.stride()
-    if place != 1 and max_pages > 1:
-        raise QLError(2, "block_table's rows must be contiguous")
-    _same_device(block_table, "block_table", device)
+    n_seqs, max_pages, row = _block_table(block_table, device)
     cu_at = _array(cu_q, "cu_q", torch.int32, (n_seqs + 1,), device)
     lens_at = _array(kv_lens, "kv_lens", torch.int32, (n_seqs,), device)
     sinks_at = _array(sinks, "sinks", torch.float32, (hq,), device)
@@ -668,9 +732,209 @@ def qlinear_paged_attention(q, k_cache, v_cache, block_table, cu_q, kv_lens, *, 
         raise QLError(2, "workspace must be contiguous")
     _same_device(workspace, "workspace", device)
     status = lib.qlinear_paged_attention(at["q"], at["q_out"], _dt(dtype), t, at["cache"], block_table.data_ptr(),
-                                         row if n_seqs > 1 else max_pages, max_pages, cu_at, lens_at, n_seqs, max_q,
+                                         row, max_pages, cu_at, lens_at, n_seqs, max_q,
                                          d ** -0.5 if scale is None else scale, window, sinks_at, workspace.data_ptr(),
                                          workspace.nbytes, _stream_on(device))
+    if status:
+        _check(status)
+    return out
+
+
+# ---- over a cache in 4 bits: four tensors (k_codes, k_groups, v_codes, v_groups), codes int32
+# [n_pages, page_size, hk, d/8] and groups float16 [n_pages, page_size, hk, d/group_size, 2] (scale, bias).
+
+
+def qlinear_paged_cache_4bit(n_pages: int, page_size: int, heads: int, d: int, group_size: int = 64, device="cuda"):
+    """An empty cache in 4 bits -> (k_codes, k_groups, v_codes, v_groups).  Its pages are head-major in memory, so
+    that a head's rows in a page are one run, which is what reads fastest."""
+    torch = _torch()
+    if group_size not in (32, 64, 128) or d % group_size:
+        raise QLError(5, "group_size must be 32, 64 or 128 and divide d")
+    codes = [torch.zeros((n_pages, heads, page_size, d // 8), dtype=torch.int32, device=device) for _ in range(2)]
+    groups = [torch.zeros((n_pages, heads, page_size, d // group_size, 2), dtype=torch.float16, device=device)
+              for _ in range(2)]
+    return tuple(x.transpose(1, 2) for pair in zip(codes, groups) for x in pair)
+
+
+def qlinear_kv_append_4bit(k, v, cache, slots, *, q=None, q_out=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+                           positions=None, cos_sin=None, interleaved: bool = False):
+    """qlinear_kv_append into a cache in 4 bits: the rows of k (normed and rotated) and v are quantized
+    where they are stored -> q_out (None without q)."""
+    torch = _torch()
+    lib = load_library()
+    if k.dim() != 3:
+        raise QLError(2, "k must be [tokens, heads, d]")
+    t, _, d = k.shape
+    dtype, device, args = k.dtype, k.get_device(), _ARGS
+    at = args.at
+    if q is not None:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
+        _heads(args.q, q, "q", t, d, dtype, device)
+        _heads(args.q_out, q_out, "q_out", t, d, dtype, device)
+    _heads(args.k, k, "k", t, d, dtype, device)
+    _heads(args.v, v, "v", t, d, dtype, device)
+    _paged_cache4(args.cache4, cache, d, device)
+    slots_at = _array(slots, "slots", torch.int64, (t,), device)
+    _norm_rope(args.nr, t, d, q_weight, k_weight, eps, positions, cos_sin, interleaved, device)
+    status = lib.qlinear_kv_append_4bit(at["q"] if q is not None else None, at["q_out"], at["k"], at["v"], at["cache4"],
+                                        slots_at, _dt(dtype), t, at["nr"], _stream_on(device))
+    if status:
+        _check(status)
+    return q_out if q is not None else None
+
+
+def qlinear_kv_read_4bit(cache, slots, *, dtype=None, k_out=None, v_out=None):
+    """The rows at slots (int64 [t]; out of range: zeros) of a cache in 4 bits as values -> (k_out, v_out)
+    [t, hk, d] in dtype (default bfloat16, or that of k_out or v_out)."""
+    torch = _torch()
+    lib = load_library()
+    device, args = slots.get_device(), _ARGS
+    _paged_cache4(args.cache4, cache, None, device)
+    t, hk, d = slots.shape[0], args.cache4.hk, args.cache4.d
+    given = k_out if k_out is not None else v_out
+    dtype = dtype or (given.dtype if given is not None else torch.bfloat16)
+    if k_out is None:
+        k_out = torch.empty((t, hk, d), dtype=dtype, device=slots.device)
+    if v_out is None:
+        v_out = torch.empty((t, hk, d), dtype=dtype, device=slots.device)
+    _heads(args.k, k_out, "k_out", t, d, dtype, device)
+    _heads(args.v, v_out, "v_out", t, d, dtype, device)
+    slots_at = _array(slots, "slots", torch.int64, (t,), device)
+    status = lib.qlinear_kv_read_4bit(args.at["cache4"], slots_at, t, args.at["k"], args.at["v"], _dt(dtype),
+                                      _stream_on(device))
+    if status:
+        _check(status)
+    return k_out, v_out
+
+
+def qlinear_paged_attention_4bit_workspace_size(q, cache, block_table, *, max_q: int, window: int = 0) -> int:
+    t, hq, d = q.shape
+    return int(load_library().qlinear_paged_attention_4bit_workspace_size(
+        t, block_table.shape[0], hq, cache[0].shape[2], d, max_q, block_table.shape[1], cache[0].shape[1], window))
+
+
+def qlinear_paged_attention_4bit(q, cache, block_table, cu_q, kv_lens, *, max_q: int, scale=None, window: int = 0,
+                                 sinks=None, out=None, workspace=None):
+    """qlinear_paged_attention over a cache in 4 bits; q and out bfloat16 or float16 -> out [t, hq, d]."""
+    torch = _torch()
+    lib = load_library()
+    if q.dim() != 3:
+        raise QLError(2, "q must be [tokens, heads, d]")
+    t, hq, d = q.shape
+    dtype, device, args = q.dtype, q.get_device(), _ARGS
+    at = args.at
+    if out is None:
+        out = torch.empty((t, hq, d), dtype=dtype, device=q.device)
+    _heads(args.q, q, "q", t, d, dtype, device)
+    _heads(args.q_out, out, "out", t, d, dtype, device)
+    _paged_cache4(args.cache4, cache, d, device)
+    n_seqs, max_pages, row = _block_table(block_table, device)
+    cu_at = _array(cu_q, "cu_q", torch.int32, (n_seqs + 1,), device)
+    lens_at = _array(kv_lens, "kv_lens", torch.int32, (n_seqs,), device)
+    sinks_at = _array(sinks, "sinks", torch.float32, (hq,), device)
+    if workspace is None:
+        need = qlinear_paged_attention_4bit_workspace_size(q, cache, block_table, max_q=max_q, window=window)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    elif not workspace.is_contiguous():
+        raise QLError(2, "workspace must be contiguous")
+    _same_device(workspace, "workspace", device)
+    status = lib.qlinear_paged_attention_4bit(at["q"], at["q_out"], _dt(dtype), t, at["cache4"], block_table.data_ptr(), row,
+                                              max_pages, cu_at, lens_at, n_seqs, max_q, d ** -0.5 if scale is None else scale,
+                                              window, sinks_at, workspace.data_ptr(), workspace.nbytes, _stream_on(device))
+    if status:
+        _check(status)
+    return out
+
+
+def qlinear_kv_extend(counts, lens, block_table, *, page_size: int, rows: int, free_pages=None, free_count=None,
+                      lens_out=None, free_count_out=None, cu_q=None, positions=None, slots=None, info=None):
+    """One step of a paged cache's tables on the device.  Sequence s, with lens[s] cached tokens in the pages
+    block_table[s], brings counts[s] new ones (below 0: it is through, its pages go back); pages are
+    taken from the top of free_pages[:free_count] and put back there -> (cu_q [n_seqs + 1], positions
+    [rows], slots [rows], info [4] = tokens, pages taken, why refused (0: done), free pages left).
+    lens and free_count (int32, as all but positions and slots) are updated in place unless lens_out and
+    free_count_out are given.  A step that cannot be done changes nothing (see qlinear.h for why)."""
+    torch = _torch()
+    lib = load_library()
+    device, i32 = counts.get_device(), dict(dtype=torch.int32, device=counts.device)
+    if counts.dim() != 1:
+        raise QLError(2, "counts must be [n_seqs]")
+    n_seqs, max_pages, row = _block_table(block_table, device)
+    cap = 0
+    if free_pages is not None:
+        if free_pages.dim() != 1:
+            raise QLError(2, "free_pages must be [entries]")
+        cap = free_pages.shape[0]
+    lens_out = lens if lens_out is None else lens_out
+    free_count_out = free_count if free_count_out is None else free_count_out
+    cu_q = torch.empty(n_seqs + 1, **i32) if cu_q is None else cu_q
+    info = torch.empty(4, **i32) if info is None else info
+    if positions is None:
+        positions = torch.empty(rows, dtype=torch.int64, device=counts.device)
+    if slots is None:
+        slots = torch.empty(rows, dtype=torch.int64, device=counts.device)
+    at = [_array(x, name, torch.int32, (n,), device)
+          for x, name, n in ((counts, "counts", n_seqs), (lens, "lens", n_seqs), (lens_out, "lens_out", n_seqs),
+                             (free_pages, "free_pages", cap), (free_count, "free_count", 1),
+                             (free_count_out, "free_count_out", 1), (cu_q, "cu_q", n_seqs + 1), (info, "info", 4))]
+    pos_at, slots_at = (_array(x, name, torch.int64, (rows,), device)
+                        for x, name in ((positions, "positions"), (slots, "slots")))
+    status = lib.qlinear_kv_extend(at[0], at[1], n_seqs, block_table.data_ptr(), row, max_pages, page_size, at[3], cap, at[4],
+                                   at[2], at[5], at[6], pos_at, slots_at, rows, at[7], _stream_on(device))
+    if status:
+        _check(status)
+    return cu_q, positions, slots, info
+
+
+def qlinear_select_experts(logits, k: int, *, sigmoid: bool = False, bias=None, n_groups: int = 1, top_groups: int = 1,
+                           group_top: int = 1, renormalize: bool = True, scale: float = 1.0, n_rows=None, ids=None,
+                           weights=None):
+    """The k experts of each row of router logits [t, e] and their weights -> (ids int64 [t, k], weights
+    fp32 [t, k]), for qlinear_apply_experts and qlinear_combine_experts.  Softmax or sigmoid scores; bias
+    (fp32 [e]) counts in the choice only; the choice lies within the top_groups of n_groups groups with the
+    largest score (or, group_top = 2, sum of two); n_rows (int32 [1], device): rows behind it get -1 and 0."""
+    torch = _torch()
+    lib = load_library()
+    if logits.dim() != 2:
+        raise QLError(2, "logits must be [tokens, experts]")
+    t, e = logits.shape
+    device = logits.get_device()
+    row, place = logits.stride()
+    if place != 1 and e > 1:
+        raise QLError(2, "the rows of logits must be contiguous")
+    if ids is None:
+        ids = torch.empty((t, k), dtype=torch.int64, device=logits.device)
+    if weights is None:
+        weights = torch.empty((t, k), dtype=torch.float32, device=logits.device)
+    status = lib.qlinear_select_experts(logits.data_ptr(), _dt(logits), t, e, row if t > 1 else e,
+                                        _array(bias, "bias", torch.float32, (e,), device), 1 if sigmoid else 0, n_groups,
+                                        top_groups, group_top, k, 1 if renormalize else 0, scale,
+                                        _array(n_rows, "n_rows", torch.int32, (1,), device),
+                                        _array(ids, "ids", torch.int64, (t, k), device),
+                                        _array(weights, "weights", torch.float32, (t, k), device), _stream_on(device))
+    if status:
+        _check(status)
+    return ids, weights
+
+
+def qlinear_combine_experts(y, weights, *, ids=None, e: int = 0, residual=None, out=None):
+    """residual [t, n] + the sum of y's k rows of each token (y [t * k, n], as qlinear_apply_experts gives them)
+    times weights (fp32 [t, k]) -> out [t, n] in y's dtype.  Positions whose id (int64 [t, k]) lies outside
+    [0, e) add nothing.  out may be residual."""
+    torch = _torch()
+    lib = load_library()
+    if weights.dim() != 2 or y.dim() != 2:
+        raise QLError(2, "weights must be [tokens, k] and y [tokens * k, n]")
+    (t, k), n = weights.shape, y.shape[1]
+    device = y.get_device()
+    if out is None:
+        out = torch.empty((t, n), dtype=y.dtype, device=y.device)
+    status = lib.qlinear_combine_experts(_array(y, "y", y.dtype, (t * k, n), device), _dt(y),
+                                         _array(weights, "weights", torch.float32, (t, k), device),
+                                         _array(ids, "ids", torch.int64, (t, k), device), e,
+                                         _array(residual, "residual", y.dtype, (t, n), device), t, k, n,
+                                         _array(out, "out", y.dtype, (t, n), device), _stream_on(device))
     if status:
         _check(status)
     return out

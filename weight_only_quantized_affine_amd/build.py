@@ -19,7 +19,8 @@ LIB = os.path.join(LIBDIR, "libqlinear.so")
 SOURCES = ["qlinear_api.cpp", "quantize.hip", "dequant.hip", "gemv.hip", "gemv_m1.hip", "gemv_m2.hip", "gemv_m4.hip",
            "gemv_m8.hip", "gemm.hip", "experts.hip", "experts_mx.hip",
            "experts_q8.hip", "experts_kq.hip", "gemv_stream.hip", "take.hip", "transcode.hip",
-           "norm_rope.hip", "attn_few.hip", "attn_tile.hip"]
+           "norm_rope.hip", "attn_few.hip", "attn_few4.hip", "attn_tile.hip",
+           "kv_extend.hip", "select.hip"]
 FLAGS = [
     "--offload-arch=gfx950",
     "-O3",
@@ -34,7 +35,8 @@ FLAGS = [
 # GEMM's accumulators are only read in its epilogue and may live in the accumulation registers.
 FILE_FLAGS = {
     f: ["-mllvm", "-amdgpu-mfma-vgpr-form"]
-    for f in ("gemv_m1.hip", "gemv_m2.hip", "gemv_m4.hip", "gemv_m8.hip", "attn_few.hip", "attn_tile.hip")
+    for f in ("gemv_m1.hip", "gemv_m2.hip", "gemv_m4.hip", "gemv_m8.hip", "attn_few.hip", "attn_few4.hip",
+              "attn_tile.hip")
 }
 
 

@@ -14,7 +14,7 @@
 // (a plain read of 1 GB reaches 5.9 here); 64 ragged sequences, 762 MB in 133 us, 5.7 TB/s; one
 // sequence of 1025 positions with 16 heads on 8, 12 us, the latency of two launches and of the chain
 // lengths, page ids, keys.
-#include "attn_common.hpp"
+#include "attn_few.hpp"
 
 namespace ql {
 namespace {
@@ -101,71 +101,17 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few_kernel(const A
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, col = lane & 15;
 
-  // This workgroup's run of units: all sequences' tiles, head by head, end to end.
-  // Where the runs are long each item has two units for its start and end before its first tile (64
-  // ragged sequences: 146 -> 138 us); short runs are better off with the tiles spread evenly (8
-  // sequences, window 1024: 17.4 against 19.1 us).
-  int item_units = 0;
-  auto cost = [&](int s) -> int {
-    if (s >= a.n_seqs) return 0;
-    const AttnSeq q = attn_seq(a, s);
-    if (q.nq < 1 || !attn_is_few(a, q.nq)) return 0;
-    int lo, hi, first;
-    attn_span(a, q, 0, q.nq - 1, lo, hi);
-    return (item_units + attn_tiles<128>(lo, hi, first)) * a.hk;
-  };
-  int W = 0, mine = 0, before = 0;  // the thread's own sequence tid: its units and those before it
-  auto measure = [&] {
-    W = 0;
-    for (int s0 = 0; s0 < a.n_seqs; s0 += 256) {
-      int total;
-      const int c = cost(s0 + tid), e = block_scan<4>(c, ssh, total);
-      if (s0 == 0) mine = c, before = e;
-      W += total;
-    }
-  };
-  measure();
-  if (W >= 20 * a.nw_few) {
-    item_units = 2;
-    measure();
-  }
-  const int nw = min(a.nw_few, W);
-  // workgroups of one XCD (every 8th) take neighbouring runs (one sequence of 131071: 102 -> 97 us)
-  const int w = a.nw_few % 8 == 0 ? (blockIdx.x & 7) * (a.nw_few >> 3) + (blockIdx.x >> 3) : blockIdx.x;
-  AttnRecord* rec = a.rec + w;
-  if (a.few_by_item) {  // the first workgroup clears the records of sequences that are not taken here
-    if (blockIdx.x == 0)
-      for (int i = tid; i < a.n_seqs; i += 256)
-        if (cost(i) == 0)
-          for (int h = 0; h < a.hk; ++h) a.rec[i * a.hk + h].pieces = 0;
-  } else if (w >= nw && tid == 0) {
-    rec->pieces = 0;
-  }
-  if (w >= nw) return;
-  const int u0 = attn_cut(w, nw, W), u1 = attn_cut(w + 1, nw, W);
-  // sequence of unit u0 and its first unit; beyond 256 sequences the scan is run again
-  for (int s0 = 0, sum = 0; s0 < a.n_seqs && sum <= u0; s0 += 256) {
-    if (s0 > 0) {
-      int total;
-      mine = cost(s0 + tid);
-      before = sum + block_scan<4>(mine, ssh, total);
-      sum += total;
-    } else if (a.n_seqs > 256) {
-      int total;
-      block_scan<4>(mine, ssh, total);
-      sum += total;
-    }
-    if (before <= u0 && u0 < before + mine) sfound[0] = s0 + tid, sfound[1] = before;
-  }
-  __syncthreads();
-  int s = sfound[0], base = sfound[1];
+  FewRun run;
+  if (!few_run<128>(a, ssh, sfound, run)) return;
+  const int u1 = run.u1, item_units = run.item_units;
+  int s = run.s, base = run.base;
 
   uint8_t* sk = sm + wave * 2 * TILE;
   uint8_t* sv = sk + TILE;
   TileCopy<D, 16, 2, 128, true> tc;
   tc.init(a, 0, lane);
   bool recorded = false;
-  for (int u = u0; u < u1;) {
+  for (int u = run.u0; u < u1;) {
     const AttnSeq q = attn_seq(a, s);
     int lo, hi, first;
     attn_span(a, q, 0, q.nq - 1, lo, hi);
@@ -303,77 +249,12 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few_kernel(const A
       }
     }
 
-    // Join the 4 waves.
-#pragma unroll
-    for (int n = 0; n < NC; ++n) {
-      l[n] = join32(join16(l[n], SumF()), SumF());
-      if (g == 0) sml[wave][16 * n + col][0] = m[n], sml[wave][16 * n + col][1] = l[n];
-    }
-    __syncthreads();
     const bool whole = ta == 0 && tb == nt;
-    const int slot = ta == 0 ? 2 * w + 1 : 2 * w;
-    float* part = a.part + (int64_t)slot * a.part_floats;
-#pragma unroll
-    for (int n = 0; n < NC; ++n) {
-      float mt = kNegInf;
-#pragma unroll
-      for (int v = 0; v < 4; ++v) mt = fmaxf(mt, sml[v][16 * n + col][0]);
-      const float f = join_factor(m[n], l[n], mt);
-      float* so = (float*)sk;  // [16][D], 4-value chunks placed by the row
-#pragma unroll
-      for (int d = 0; d < ND; ++d) {
-        f32x4_t x = o[n][d];
-        for (int r = 0; r < 4; ++r) x[r] = f == 0.f ? 0.f : x[r] * f;
-        *(f32x4_t*)(so + col * D + 4 * ((4 * d + g) ^ col)) = x;
-      }
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < 16 * (D / 4) / 256; ++i) {
-        const int e = i * 256 + tid, r = e / (D / 4), c = e % (D / 4), row = 16 * n + r;
-        f32x4_t x = {0, 0, 0, 0};
-        float mr = kNegInf, lr = 0.f;
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          x += *(const f32x4_t*)((const float*)(sm + v * 2 * TILE) + r * D + 4 * (c ^ r));
-          mr = fmaxf(mr, sml[v][row][0]);
-        }
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const float mv = sml[v][row][0];
-          const float lv = sml[v][row][1];
-          lr += lv == 0.f ? 0.f : lv * join_factor(mv, lv, mr);
-        }
-        if (row < rows) {
-          if (whole) {
-            const int tok = (int)a.g_div.div((uint32_t)row);
-            const int hq = head * a.g + row - tok * a.g;
-            const float inv = attn_scale(a.sinks, hq, mr, lr);
-            uint8_t* op = a.out + ((int64_t)(q.q0 + tok) * a.out_ts + (int64_t)hq * a.out_hs) + c * 8;
-            store4(T{}, op, x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv);
-          } else {
-            if (c == 0) part[row] = mr, part[16 * NC + row] = lr;
-            *(f32x4_t*)(part + 32 * NC + row * D + c * 4) = x;
-          }
-        }
-      }
-      __syncthreads();
-    }
-    if (ta == 0 && (!whole || a.few_by_item)) {
-      recorded = true;
-      if (tid == 0) {
-        AttnRecord r = {};
-        if (a.few_by_item) rec = a.rec + s * a.hk + head;
-        r.pieces = whole ? 0 : attn_last(item0 + nt, nw, W) - w + 1;
-        r.w = w;
-        r.q0 = q.q0;
-        r.row0 = 0;
-        r.rows = rows;
-        r.head = head;
-        *rec = r;
-      }
-    }
+    few_finish<D, NC>(a, sm, 2 * TILE, sml, o, m, l, run.w, q, head, rows, ta == 0, whole,
+                      [](void* p, float x, float y, float z, float w) { store4(T{}, p, x, y, z, w); });
+    if (ta == 0) few_record(a, run, s, head, q.q0, rows, item0 + nt, whole, recorded);
   }
-  if (!recorded && !a.few_by_item && tid == 0) rec->pieces = 0;
+  if (!recorded && !a.few_by_item && tid == 0) run.rec->pieces = 0;
 }
 
 }  // namespace
@@ -388,7 +269,8 @@ template <typename T> static hipError_t few_d(const AttnArgs& a, int d, int nc, 
   return few<T, 256, 1>(a, s);
 }
 hipError_t launch_attn_few(const AttnArgs& args, int dt, int d, int nc, hipStream_t s) {
-  const AttnArgs a = attn_record_kind(args);
+  AttnArgs a = args;
+  attn_record_kind(a);
   return dt == DT_BF16 ? few_d<BF16>(a, d, nc, s) : few_d<F16>(a, d, nc, s);
 }
 

@@ -45,6 +45,47 @@ struct NormRopeArgs {
   int64_t max_pos;
 };
 hipError_t launch_norm_rope(const NormRopeArgs& a, int dt, hipStream_t s);
+// The append to a cache in 4 bits: k_out and v_out are the codes, with the strides of k_out.
+struct Append4Args : NormRopeArgs {
+  uint32_t *k_groups, *v_groups;
+  int64_t group_ps, group_ts, group_hs;  // words
+  int group;
+};
+hipError_t launch_append4(const Append4Args& a, int dt, hipStream_t s);
+// The values of its rows.
+struct Read4Args {
+  const uint8_t *k, *v;
+  int64_t page_stride, token_stride, head_stride;  // bytes
+  const uint32_t *kg, *vg;
+  int64_t group_ps, group_ts, group_hs;  // words
+  uint8_t *k_out, *v_out;
+  int64_t ko_ts, ko_hs, vo_ts, vo_hs;  // bytes
+  const int64_t* slots;
+  int64_t n_slots;
+  int page_size;
+  FastDiv page_div;
+  int hk, d, group;
+  int64_t t;
+};
+hipError_t launch_read4(const Read4Args& a, int dt, hipStream_t s);
+
+// The tables of a batch (kv_extend.hip).
+struct ExtendArgs {
+  const int32_t *counts, *lens;
+  int n_seqs;
+  int32_t* table;
+  int64_t table_stride, max_pages;
+  int page_size;
+  FastDiv page_div;
+  int32_t* free_pages;  // NULL: no list
+  int64_t free_cap;
+  const int32_t* free_count;
+  int32_t *lens_out, *free_count_out, *cu_q;
+  int64_t *positions, *slots;
+  int64_t rows;
+  int32_t* info;
+};
+hipError_t launch_kv_extend(const ExtendArgs& a, hipStream_t s);
 
 // Paged attention (attn_few.hip: sequences of few rows; attn_tile.hip: the others and the joining of
 // split items).  Strides in bytes.
@@ -52,6 +93,7 @@ constexpr int kAttnTileKeys = 64;  // keys of the tile kernel's unit of work
 // Waves of its workgroups, 32 query rows each (256 values a head fill a SIMD's registers).
 constexpr int attn_tile_waves(int d) { return d == 256 ? 4 : 8; }
 constexpr int kAttnFewKeys = 128;   // keys of the few-row kernel's unit
+constexpr int kAttnFewKeys4 = 256;  // the same over a cache in 4 bits
 struct AttnRecord;
 struct AttnArgs {
   const uint8_t* q;
@@ -83,6 +125,14 @@ struct AttnArgs {
   AttnRecord* rec;
   float *part, *part_tile;
 };
+// The same over a cache in 4 bits: k and v are the codes (strides of AttnArgs), kp and vp a word of scale
+// and bias (fp16) per group.
+struct AttnArgs4 : AttnArgs {
+  const uint8_t *kp, *vp;
+  int64_t p_page_stride, p_token_stride, p_head_stride;  // bytes
+  int group_log2;
+  int io;  // dtype of q and out
+};
 // How a call is run, from what the host knows (the lengths are device values).
 struct AttnPlan {
   bool ok;        // the work is within the kernels' 32-bit unit counts
@@ -93,11 +143,13 @@ struct AttnPlan {
   size_t part_off, part_tile_off, bytes;  // workspace: records, pieces of either kernel
 };
 AttnPlan attn_plan(int64_t t, int64_t n_seqs, int64_t hq, int64_t hk, int d, int64_t max_q, int64_t max_kv,
-                   int64_t window);
-// The arguments with the kind of records set.
-AttnArgs attn_record_kind(AttnArgs a);
+                   int64_t window, int few_keys = kAttnFewKeys);
+// Sets the kind of records.
+void attn_record_kind(AttnArgs& a);
 hipError_t launch_attn_few(const AttnArgs& a, int dt, int d, int nc, hipStream_t s);
 hipError_t launch_attn_tile(const AttnArgs& a, int dt, int d, hipStream_t s);
+hipError_t launch_attn_few4(const AttnArgs4& a, int d, int nc, hipStream_t s);
+hipError_t launch_attn_tile4(const AttnArgs4& a, int d, hipStream_t s);
 hipError_t launch_attn_join(const AttnArgs& a, int dt, int d, hipStream_t s);
 
 }  // namespace ql

@@ -31,6 +31,7 @@
 #include <type_traits>
 
 #include "attn_common.hpp"
+#include "attn_common4.hpp"
 #include "attn_order.hpp"
 
 namespace ql {
@@ -107,8 +108,94 @@ template <int BM> __device__ __forceinline__ int row_tiles(const AttnArgs& a, in
   return q.nq < 1 || attn_is_few(a, q.nq) ? 0 : (q.nq * a.g + BM - 1) / BM;
 }
 
-template <typename T, int D, bool RUNS>
-__global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) void attn_tile_kernel(const AttnArgs a) {
+// The 16 cache rows of a tile that one wave copies, over a cache in 4 bits: their codes and words stay in
+// registers while the copies of the 16-bit kernel would be in flight, and the decoded rows (fp16, in each
+// 8 values the order 0 4 1 5 2 6 3 7 in which a word's codes come apart) are written to the stage at the
+// period's end.  Lane l holds a quarter l / 16 of row l % 16: CH chunks of 16 bytes of codes (8 at
+// 64 values), 64 values apart.
+template <int D, int STEP> struct TileDecode {
+  static constexpr int CH = D == 256 ? 2 : 1, W = D == 64 ? 2 : 4;  // chunks, words of a chunk
+  int ids, block, id, base;     // as TileCopy
+  int64_t row, prow;            // the lane's row among the codes and words, row -1: not to be seen
+  uint32_t seen;
+  uint32_t k[CH][W], v[CH][W], kg[CH], vg[CH];
+  int k_tile, v_tile;           // uniform: tile whose rows are in flight, -1: none
+
+  __device__ __forceinline__ void init(const AttnArgs4&, int, int) { k_tile = v_tile = -1; }
+  __device__ __forceinline__ void lookup(const AttnArgs4& a, const int32_t* table, int first, int lo, int hi, int lane,
+                                         bool begins) {
+    base = first;
+    if (a.page16) {
+      if (begins || first - block >= 64 * STEP) {
+        block = first;
+        const int p = first + lane * STEP;
+        ids = -1;
+        if (p + 16 > lo && p < hi) ids = table[a.page_div.div((uint32_t)p)];
+        asm volatile("" : "+v"(ids));  // the wait for the load is here
+      }
+      id = __builtin_amdgcn_readlane(ids, (first - block) / STEP);
+    } else {
+      const int p = first + (lane & 15);
+      id = -1;
+      if (p >= lo && p < hi) id = table[a.page_div.div((uint32_t)p)];
+    }
+  }
+  __device__ __forceinline__ void resolve(const AttnArgs4& a, int lo, int hi, int lane) {
+    const int p = base + (lane & 15);
+    const int in = p - (int)a.page_div.div((uint32_t)p) * a.page_size;
+    const bool see = p >= lo && p < hi && (uint32_t)id < (uint32_t)a.n_pages;
+    seen = (uint32_t)__ballot(see) & 0xffffu;
+    row = see ? (int64_t)id * a.page_stride + (int64_t)in * a.token_stride : -1;
+    prow = (int64_t)id * a.p_page_stride + (int64_t)in * a.p_token_stride;
+  }
+  // Starts the loads of the lane's part of its row; a row that is not to be seen is zero.
+  __device__ __forceinline__ void load(const AttnArgs4& a, const uint8_t* head, const uint8_t* words, int lane,
+                                       uint32_t (*c)[W], uint32_t* group) const {
+    const int part = lane >> 4;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const uint8_t* at = row < 0 ? (const uint8_t*)kZeroRow : head + row;
+      const uint8_t* wat = row < 0 ? (const uint8_t*)kZeroRow : words + prow;
+      const int value = 128 * i + 8 * W * part;
+      if constexpr (W == 2) {
+        const u32x2_t x = *(const u32x2_t*)(at + value / 2);
+        c[i][0] = x[0], c[i][1] = x[1];
+      } else {
+        const u32x4_t x = *(const u32x4_t*)(at + value / 2);
+        for (int y = 0; y < 4; ++y) c[i][y] = x[y];
+      }
+      group[i] = *(const uint32_t*)(wat + 4 * (value >> a.group_log2));
+    }
+  }
+  // Decodes them into the stage.
+  template <bool IS_V>
+  __device__ __forceinline__ void store(uint8_t* stage, int row0, int lane, const uint32_t (*c)[W],
+                                        const uint32_t* group) const {
+    const int r = row0 + (lane & 15), part = lane >> 4;
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+#pragma unroll
+      for (int y = 0; y < W; ++y) {
+        const int chunk = 16 * i + W * part + y;
+        *(u32x4_t*)(stage + r * (D * 2) + (chunk ^ (IS_V ? swz_v<D>(r) : swz_k<D>(r))) * 16) = values4(c[i][y], group[i]);
+      }
+  }
+};
+
+// Stores 4 neighbouring output values of a row, in the type of out.
+template <typename T> __device__ __forceinline__ void store_out4(const AttnArgs&, void* p, float x, float y, float z, float w) {
+  store4(T{}, p, x, y, z, w);
+}
+template <typename T> __device__ __forceinline__ void store_out4(const AttnArgs4& a, void* p, float x, float y, float z, float w) {
+  if (a.io == DT_BF16)
+    store4(BF16{}, p, x, y, z, w);
+  else
+    store4(F16{}, p, x, y, z, w);
+}
+
+template <typename T, int D, bool RUNS, typename Args>
+__global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) void attn_tile_kernel(const Args a) {
+  constexpr bool kDecode = std::is_same_v<Args, AttnArgs4>;  // a cache in 4 bits (T: fp16)
   constexpr int WAVES = attn_tile_waves(D), BM = 32 * WAVES;
   constexpr int ROW = D * 2;
   constexpr int KB = BN * ROW;  // bytes of a K (or V) stage
@@ -189,7 +276,7 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
   const int late = wave / 4;  // the second four waves run half a tile behind
   const bool copier = wave < 4;
   const int row0 = R * (wave & 3);  // first key of a tile that a copying wave copies
-  TileCopy<D, R, 1, BN, false> tc;
+  std::conditional_t<kDecode, TileDecode<D, BN>, TileCopy<D, R, 1, BN, false>> tc;
   tc.init(a, row0, lane);
   bool recorded = false;
   for (int u = u0; u < u1;) {
@@ -255,12 +342,23 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
     const int hq = head * a.g + (in ? r - i * a.g : 0);
     const int qpos = q.kv - q.nq + i;
     u32x4_t qf[NS];
+    float row_sl = 0.f;  // kDecode: scale * log2(e) * 2^t
     {
       const uint8_t* qp = a.q + ((int64_t)(q.q0 + i) * a.q_ts + (int64_t)hq * a.q_hs);
 #pragma unroll
       for (int st = 0; st < NS; ++st) {
         const u32x4_t z = {0, 0, 0, 0};
         qf[st] = in ? *(const u32x4_t*)(qp + (2 * st + h) * 16) : z;
+      }
+      if constexpr (kDecode) {
+        float amax = 0.f;
+#pragma unroll
+        for (int st = 0; st < NS; ++st) amax = amax8(qf[st], amax);
+        const int t = a.io == DT_BF16 ? q_exponent(join32(amax, MaxF())) : 0;
+        const float factor = __builtin_ldexpf(1.f, -t);
+        row_sl = __builtin_ldexpf(a.sl, t);
+#pragma unroll
+        for (int st = 0; st < NS; ++st) qf[st] = q_pairs(qf[st], a.io, factor);
       }
     }
     // first and last position among the wave's rows
@@ -284,13 +382,35 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
     const uint8_t* kb = a.k + (int64_t)head * a.head_stride;
     const uint8_t* vb = a.v + (int64_t)head * a.head_stride;
     const int32_t* table = a.table + (int64_t)s * a.table_stride;
+    const uint8_t *kw = nullptr, *vw = nullptr;
+    if constexpr (kDecode) kw = a.kp + (int64_t)head * a.p_head_stride, vw = a.vp + (int64_t)head * a.p_head_stride;
     const int n = tb - ta, kfirst = (first + ta) * BN;
     auto stage_k = [&](int t) { return sm + attn_stage<ST>(t) * KB; };
     auto stage_v = [&](int t) { return sm + (ST + attn_stage<ST>(t)) * KB; };
+    auto copy_v = [&](int t) {
+      if constexpr (kDecode)
+        tc.v_tile = t, tc.load(a, vb, vw, lane, tc.v, tc.vg);
+      else
+        tc.template copy<true>(tc.now, vb, stage_v(t) + row0 * ROW, row0, lane);
+    };
+    auto copied = [&] {  // the wave's copies have arrived
+      if constexpr (kDecode) {
+        if (tc.v_tile >= 0) tc.template store<true>(stage_v(tc.v_tile), row0, lane, tc.v, tc.vg);
+        if (tc.k_tile >= 0) tc.template store<false>(stage_k(tc.k_tile), row0, lane, tc.k, tc.kg);
+        tc.k_tile = tc.v_tile = -1;
+      } else {
+        attn_wait_vm<0>();
+      }
+    };
     auto copy_k = [&](int t) {
       tc.resolve(a, lo, hi, lane);
       if (lane == 0) sseen[attn_seen_at(t)][wave & 3] = (uint16_t)tc.seen;
-      tc.template copy<false>(tc.now, kb, stage_k(t) + row0 * ROW, row0, lane);
+      if constexpr (kDecode) {
+        if (tc.k_tile >= 0) tc.template store<false>(stage_k(tc.k_tile), row0, lane, tc.k, tc.kg);  // an item's first
+        tc.k_tile = t, tc.load(a, kb, kw, lane, tc.k, tc.kg);
+      } else {
+        tc.template copy<false>(tc.now, kb, stage_k(t) + row0 * ROW, row0, lane);
+      }
       if (t + 1 < n) tc.lookup(a, table, kfirst + (t + 1) * BN + row0, lo, hi, lane, false);
     };
     auto is_cut = [&](int t) {  // whether some row does not see all of it
@@ -410,7 +530,7 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
       float mx = fmaxf(sc[0][0], sc[NK - 1][0]);
 #pragma unroll
       for (int x = 1; x < 16; ++x) mx = max3(mx, sc[0][x], sc[NK - 1][x]);
-      mx = join32(mx, MaxF()) * a.sl;
+      mx = join32(mx, MaxF()) * (kDecode ? row_sl : a.sl);
       if (__any(mx > m + kLazy)) {
         const float mn = fmaxf(m, mx);
         const float f = m == kNegInf ? 0.f : exp2_fast(m - mn);
@@ -426,7 +546,7 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
       for (int ks = 0; ks < NV; ++ks) {
         float e[8];
 #pragma unroll
-        for (int x = 0; x < 8; ++x) e[x] = exp2_fast(__builtin_fmaf(sc[ks >> 1][8 * (ks & 1) + x], a.sl, -mr));
+        for (int x = 0; x < 8; ++x) e[x] = exp2_fast(__builtin_fmaf(sc[ks >> 1][8 * (ks & 1) + x], kDecode ? row_sl : a.sl, -mr));
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           p[ks][x] = pack2(T{}, e[2 * x], e[2 * x + 1]);
@@ -439,8 +559,8 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
       if constexpr (S == AttnStep::kBarrier) attn_barrier();
       if constexpr (S == AttnStep::kPages) tc.lookup(a, table, kfirst + row0, lo, hi, lane, true);
       if constexpr (S == AttnStep::kCopyK) copy_k(t);
-      if constexpr (S == AttnStep::kCopyV) tc.template copy<true>(tc.now, vb, stage_v(t) + row0 * ROW, row0, lane);
-      if constexpr (S == AttnStep::kWait) attn_wait_vm<0>();
+      if constexpr (S == AttnStep::kCopyV) copy_v(t);
+      if constexpr (S == AttnStep::kWait) copied();
       if constexpr (S == AttnStep::kScores) products(t - 1, kScores, kLast);
       if constexpr (S == AttnStep::kWeights) weights(t);
       if constexpr (S == AttnStep::kProducts) products(t, kFirst, kLast);
@@ -450,6 +570,17 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
     });
     l = join32(l, SumF());
 
+    if constexpr (kDecode) {  // values 0 4 1 5 in the lower half of the lanes, 2 6 3 7 in the upper: back in order
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int y = 0; y < 16; y += 4) {
+          const auto u = __builtin_amdgcn_permlane32_swap(__float_as_uint(o[d][y]), __float_as_uint(o[d][y + 1]), false, false);
+          const auto w2 = __builtin_amdgcn_permlane32_swap(__float_as_uint(o[d][y + 2]), __float_as_uint(o[d][y + 3]), false, false);
+          o[d][y] = __uint_as_float(u[0]), o[d][y + 2] = __uint_as_float(u[1]);
+          o[d][y + 1] = __uint_as_float(w2[0]), o[d][y + 3] = __uint_as_float(w2[1]);
+        }
+    }
     // The lane holds its row's values 32 d + 8 y + 4 h .. + 3.
     if (!RUNS || (ta == 0 && tb == nt)) {
       if (in) {
@@ -459,8 +590,8 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
         for (int d = 0; d < ND; ++d)
 #pragma unroll
           for (int y = 0; y < 4; ++y)
-            store4(T{}, op + 64 * d + 16 * y, o[d][4 * y] * inv, o[d][4 * y + 1] * inv, o[d][4 * y + 2] * inv,
-                   o[d][4 * y + 3] * inv);
+            store_out4<T>(a, op + 64 * d + 16 * y, o[d][4 * y] * inv, o[d][4 * y + 1] * inv, o[d][4 * y + 2] * inv,
+                          o[d][4 * y + 3] * inv);
       }
     } else {
       float* part = a.part_tile + (int64_t)(ta == 0 ? 2 * w + 1 : 2 * w) * (BM * (D + 2));
@@ -586,14 +717,14 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(const AttnArgs 
   }
 }
 
-template <typename T, int D> hipError_t tile(const AttnArgs& a, hipStream_t s) {
+template <typename T, int D, typename Args> hipError_t tile(const Args& a, hipStream_t s) {
   const size_t lds = (size_t)2 * tile_stages(D) * BN * D * 2 + tile_clean_bytes(D);
   constexpr int threads = 64 * attn_tile_waves(D);
   if (a.nw_tile > 0) {
     const size_t plan = ((size_t)a.plan_tiles + 1 + a.n_seqs) * 4;
-    attn_tile_kernel<T, D, true><<<a.nw_tile, threads, lds + plan, s>>>(a);
+    attn_tile_kernel<T, D, true, Args><<<a.nw_tile, threads, lds + plan, s>>>(a);
   } else {
-    attn_tile_kernel<T, D, false><<<a.items_tile, threads, lds, s>>>(a);
+    attn_tile_kernel<T, D, false, Args><<<a.items_tile, threads, lds, s>>>(a);
   }
   return hipGetLastError();
 }
@@ -626,7 +757,7 @@ template <typename T, int D> hipError_t join(const AttnArgs& a, hipStream_t s) {
 }  // namespace
 
 AttnPlan attn_plan(int64_t t, int64_t n_seqs, int64_t hq, int64_t hk, int d, int64_t max_q, int64_t max_kv,
-                   int64_t window) {
+                   int64_t window, int few_keys) {
   AttnPlan p{};
   const int64_t g = hq / hk, bm = 32 * attn_tile_waves(d);
   const int64_t cap = d == 256 ? 16 : 32;  // rows whose registers fit
@@ -647,7 +778,7 @@ AttnPlan attn_plan(int64_t t, int64_t n_seqs, int64_t hq, int64_t hk, int d, int
   p.ok = true;
   size_t at = 0;
   if (p.nc) {
-    const int64_t tiles = span / kAttnFewKeys + 10;
+    const int64_t tiles = span / few_keys + 10;
     const int64_t units = times(times(n_seqs, hk), tiles);
     p.ok = p.ok && units < limit;
     // two resident workgroups a compute unit, one at 256 values a head (their LDS; four at 64 values
@@ -655,7 +786,7 @@ AttnPlan attn_plan(int64_t t, int64_t n_seqs, int64_t hq, int64_t hk, int d, int
     p.nw_few = (int)std::min<int64_t>(d == 256 ? 256 : 512, units);
     p.cap_few = 16 * p.nc;
     p.part_floats = p.cap_few * (d + 2);
-    p.join_few = max_kv > kAttnFewKeys;  // a span inside one tile is never cut
+    p.join_few = max_kv > few_keys;  // a span inside one tile is never cut
   }
   if (p.tile) {
     const int64_t slots = 256;  // resident workgroups
@@ -689,19 +820,25 @@ AttnPlan attn_plan(int64_t t, int64_t n_seqs, int64_t hq, int64_t hk, int d, int
   return p;
 }
 
-AttnArgs attn_record_kind(AttnArgs a) {
+void attn_record_kind(AttnArgs& a) {
   a.few_by_item = (int64_t)a.n_seqs * a.hk <= a.nw_few;
   a.tile_by_item = (int64_t)a.plan_tiles * a.hk <= a.nw_tile;
-  return a;
 }
 
 hipError_t launch_attn_tile(const AttnArgs& args, int dt, int d, hipStream_t s) {
-  const AttnArgs a = attn_record_kind(args);
+  AttnArgs a = args;
+  attn_record_kind(a);
   if (dt == DT_BF16) return d == 64 ? tile<BF16, 64>(a, s) : d == 128 ? tile<BF16, 128>(a, s) : tile<BF16, 256>(a, s);
   return d == 64 ? tile<F16, 64>(a, s) : d == 128 ? tile<F16, 128>(a, s) : tile<F16, 256>(a, s);
 }
+hipError_t launch_attn_tile4(const AttnArgs4& args, int d, hipStream_t s) {
+  AttnArgs4 a = args;
+  attn_record_kind(a);
+  return d == 64 ? tile<F16, 64>(a, s) : d == 128 ? tile<F16, 128>(a, s) : tile<F16, 256>(a, s);
+}
 hipError_t launch_attn_join(const AttnArgs& args, int dt, int d, hipStream_t s) {
-  const AttnArgs a = attn_record_kind(args);
+  AttnArgs a = args;
+  attn_record_kind(a);
   if (dt == DT_BF16) return d == 64 ? join<BF16, 64>(a, s) : d == 128 ? join<BF16, 128>(a, s) : join<BF16, 256>(a, s);
   return d == 64 ? join<F16, 64>(a, s) : d == 128 ? join<F16, 128>(a, s) : join<F16, 256>(a, s);
 }

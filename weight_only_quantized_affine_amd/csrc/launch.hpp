@@ -309,4 +309,30 @@ hipError_t launch_apply_experts(int fmt, const void* w0, const void* w1, int64_t
                                 void* y, int ydt, int32_t* offsets, int32_t* perm, int32_t* order, float* xfac,
                                 hipStream_t s);
 
+// The experts of each token from its router logits, and the weighted sum of their outputs (select.hip).
+struct SelectArgs {
+  const void* logits;
+  int dt;
+  int64_t t, row_stride;
+  int e, k;
+  const float* bias;
+  int sigmoid, n_groups, top_groups, group_top, renormalize;
+  float scale;
+  const int32_t* n_rows;
+  int64_t* ids;
+  float* weights;
+};
+hipError_t launch_select_experts(const SelectArgs& a, hipStream_t s);
+struct CombineArgs {
+  const void* y;
+  int dt;
+  const float* weights;
+  const int64_t* ids;
+  int64_t e;
+  const void* residual;
+  int64_t t, k, n;
+  void* out;
+};
+hipError_t launch_combine_experts(const CombineArgs& a, hipStream_t s);
+
 }  // namespace ql

@@ -13,6 +13,12 @@
 //
 // Measured (bf16, 40 heads of 128): 8192 tokens 34 us, 172 MB, 5.1 TB/s (a large copy reaches 5.1
 // here); append of 4096 tokens 19 us; one token 2.9 us.
+//
+// Append to a cache in 4 bits: the rows of k (in 64 bits up to their rounding, since a code hangs on the last
+// bits) and of v are quantized where they are, 8 values and one word of codes a lane, a group's
+// smallest and largest value by DPP within its 4, 8 or 16 lanes.
+#include <type_traits>
+
 #include "head_common.hpp"
 
 namespace ql {
@@ -54,9 +60,63 @@ __device__ __forceinline__ void weights8(const void* w, int wdt, int c, float* f
   }
 }
 
-template <typename T, int L, int ROWS>
-__global__ __launch_bounds__(256) void norm_rope_kernel(const NormRopeArgs a, FastDiv per_token, int groups,
-                                                        int64_t units) {
+// The same for sums in 64 bits.
+template <int CTRL> __device__ __forceinline__ double add_dpp(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, 0xf, 0xf, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xf, 0xf, false);
+  return x + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+template <int L> __device__ __forceinline__ double group_sum(double x) {
+  if (L >= 2) x = add_dpp<0xB1>(x);
+  if (L >= 4) x = add_dpp<0x4E>(x);
+  if (L >= 8) x = add_dpp<0x141>(x);
+  if (L >= 16) x = add_dpp<0x140>(x);
+  if (L >= 32) x += __shfl_xor(x, 16);
+  if (L >= 64) x += __shfl_xor(x, 32);
+  return x;
+}
+
+// Monotone integer key of an fp32 value (-0 < +0), and back.
+__device__ __forceinline__ int32_t order_key(float f) {
+  const int32_t i = __float_as_int(f);
+  return i ^ ((i >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float from_order_key(int32_t i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
+template <int CTRL> __device__ __forceinline__ void span_dpp(int32_t& lo, int32_t& hi) {
+  lo = min(lo, __builtin_amdgcn_update_dpp(0, lo, CTRL, 0xf, 0xf, false));
+  hi = max(hi, __builtin_amdgcn_update_dpp(0, hi, CTRL, 0xf, 0xf, false));
+}
+// The codes of a lane's 8 values and the word of their group (of `lanes` lanes): scale (max - min) / 15 and
+// bias min rounded to fp16, codes the nearest levels of those, as qlinear_quantize; magnitudes past 2^15
+// and NaN (the largest or smallest key) give scale 0 and bias NaN.
+__device__ __forceinline__ uint32_t quantize8(const float* f, int lanes, uint32_t& group) {
+  int32_t lo = order_key(f[0]), hi = lo;
+#pragma unroll
+  for (int j = 1; j < 8; ++j) lo = min(lo, order_key(f[j])), hi = max(hi, order_key(f[j]));
+  span_dpp<0xB1>(lo, hi);
+  span_dpp<0x4E>(lo, hi);
+  if (lanes >= 8) span_dpp<0x141>(lo, hi);
+  if (lanes >= 16) span_dpp<0x140>(lo, hi);
+  const float mn = from_order_key(lo), mx = from_order_key(hi);
+  const bool held = __builtin_fabsf(mn) <= 32768.f && __builtin_fabsf(mx) <= 32768.f;
+  const uint32_t sb = f32_to_f16_bits(__fdiv_rn(mx - mn, 15.f)), bb = f32_to_f16_bits(mn);
+  const float s = f16_bits_to_f32(sb), b = f16_bits_to_f32(bb);
+  group = held ? sb | (bb << 16) : 0x7e000000u;
+  if (!held || s == 0.f) return 0;
+  uint32_t word = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float r = __builtin_rintf(__fdiv_rn(f[j] - b, s));
+    r = fminf(fmaxf(r, 0.f), 15.f);
+    word |= (uint32_t)r << (4 * j);
+  }
+  return word;
+}
+
+template <typename T, int L, int ROWS, typename Args>
+__global__ __launch_bounds__(256) void norm_rope_kernel(const Args a, FastDiv per_token, int groups, int64_t units) {
+  constexpr bool kQuant = std::is_same_v<Args, Append4Args>;
   const int lane = threadIdx.x & 63;
   const int c = lane % L;  // the lane's 8 values of a row
   const int64_t unit = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
@@ -125,6 +185,56 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(const NormRopeArgs a, Fa
     const void* wp = is_q ? a.q_weight : is_v ? nullptr : a.k_weight;
     float f[8];
     unpack8<T>(x[i], f);
+    if constexpr (kQuant) {
+      if (!is_q) {
+        if (!is_v) {
+          double y[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) y[j] = f[j];
+          if (wp) {
+            double ss = 0.;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) ss += (double)(f[j] * f[j]);  // 22 bits: exact
+            const double r = 1. / __builtin_sqrt(group_sum<L>(ss) / a.d + (double)a.eps);
+            if (wp != loaded) {
+              if (on) weights8(wp, a.wdt, c, w);
+              loaded = wp;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = y[j] * r * w[j];
+          }
+          if (a.rot > 0) {
+            double z[8];
+            if (a.interleaved) {
+#pragma unroll
+              for (int j = 0; j < 8; j += 2) {
+                z[j] = y[j] * cs[j] - y[j + 1] * sn[j];
+                z[j + 1] = y[j + 1] * cs[j] + y[j] * sn[j];
+              }
+            } else {
+              const int from = (lane & ~(L - 1)) | ((second ? c - half : c + half) & (L - 1));
+#pragma unroll
+              for (int j = 0; j < 8; ++j) z[j] = y[j] * cs[j] + __shfl(y[j], from) * sn[j];  // sn holds the sign
+            }
+            if (turned) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) y[j] = z[j];
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[j] = known ? param_to_f32<T>(f32_to_bits<T>((float)y[j])) : 0.f;
+        }
+        uint32_t group;
+        const uint32_t word = quantize8(f, a.group / 8, group);
+        if (h >= heads || !on || page < 0) continue;
+        const int hh = is_v ? h - a.hq - a.hk : h - a.hq;
+        uint8_t* cp = (is_v ? a.v_out : a.k_out) + page * a.page_stride + at * a.ko_ts + hh * a.ko_hs;
+        ((uint32_t*)cp)[c] = word;
+        uint32_t* gp = (is_v ? a.v_groups : a.k_groups) + page * a.group_ps + at * a.group_ts + hh * a.group_hs;
+        if ((c & (a.group / 8 - 1)) == 0) gp[c / (a.group / 8)] = group;
+        continue;
+      }
+    }
     if (wp) {
       float ss = 0.f;
 #pragma unroll
@@ -192,14 +302,14 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(const NormRopeArgs a, Fa
   }
 }
 
-template <typename T, int L, int ROWS> hipError_t run_rows(const NormRopeArgs& a, hipStream_t s) {
+template <typename T, int L, int ROWS, typename Args> hipError_t run_rows(const Args& a, hipStream_t s) {
   const int groups = (a.hq + a.hk + a.hv + ROWS - 1) / ROWS;
   const int64_t units = a.t * groups;
   const unsigned grid = (unsigned)((units + 256 / L - 1) / (256 / L));
-  norm_rope_kernel<T, L, ROWS><<<grid, 256, 0, s>>>(a, fast_div((uint32_t)groups), groups, units);
+  norm_rope_kernel<T, L, ROWS, Args><<<grid, 256, 0, s>>>(a, fast_div((uint32_t)groups), groups, units);
   return hipGetLastError();
 }
-template <typename T, int L> hipError_t run(const NormRopeArgs& a, hipStream_t s) {
+template <typename T, int L, typename Args> hipError_t run(const Args& a, hipStream_t s) {
   // Waves when each lane holds one row: below 16 a compute unit the launch's latency counts and one
   // row a lane is shortest (1, 2, 4 rows: 1 token x 40 rows of 128 2.9, 3.3, 4.2 us; 256 tokens 3.6,
   // 3.9, 4.8); from 64 on the rows in flight count (512 tokens 4.9, 4.5, 5.3; 1024 8.5, 6.2, 6.8;
@@ -208,7 +318,7 @@ template <typename T, int L> hipError_t run(const NormRopeArgs& a, hipStream_t s
   const int64_t waves = a.t * (a.hq + a.hk + a.hv) * L / 64;
   return waves < 4096 ? run_rows<T, L, 1>(a, s) : waves < 16384 ? run_rows<T, L, 2>(a, s) : run_rows<T, L, 4>(a, s);
 }
-template <typename T> hipError_t run_l(const NormRopeArgs& a, hipStream_t s) {
+template <typename T, typename Args> hipError_t run_l(const Args& a, hipStream_t s) {
   const int n = a.d / 8;
   if (n <= 8) return run<T, 8>(a, s);
   if (n <= 16) return run<T, 16>(a, s);
@@ -220,6 +330,50 @@ template <typename T> hipError_t run_l(const NormRopeArgs& a, hipStream_t s) {
 
 hipError_t launch_norm_rope(const NormRopeArgs& a, int dt, hipStream_t s) {
   return dt == DT_BF16 ? run_l<BF16>(a, s) : run_l<F16>(a, s);
+}
+hipError_t launch_append4(const Append4Args& a, int dt, hipStream_t s) {
+  return dt == DT_BF16 ? run_l<BF16>(a, s) : run_l<F16>(a, s);
+}
+
+namespace {
+
+// One lane for 8 values of a row of k or v.
+template <typename T> __global__ __launch_bounds__(256) void read4_kernel(const Read4Args a, FastDiv per_row, FastDiv per_token, int64_t n) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n) return;
+  const int64_t unit = per_row.div((uint32_t)i);  // (token, k or v, head)
+  const int c = (int)(i - unit * (a.d / 8));
+  const int64_t tok = per_token.div((uint32_t)unit);
+  const int h2k = (int)(unit - tok * 2 * a.hk);
+  const bool is_v = h2k >= a.hk;
+  const int h = is_v ? h2k - a.hk : h2k;
+  const int64_t slot = a.slots[tok];
+  u32x4_t o = {0, 0, 0, 0};
+  if (slot >= 0 && slot < a.n_slots) {
+    const int64_t page = a.page_div.div((uint32_t)slot), at = slot - page * a.page_size;
+    const uint8_t* cp = (is_v ? a.v : a.k) + page * a.page_stride + at * a.token_stride + h * a.head_stride;
+    const uint32_t* gp = (is_v ? a.vg : a.kg) + page * a.group_ps + at * a.group_ts + h * a.group_hs;
+    const uint32_t w = ((const uint32_t*)cp)[c], g = gp[c / (a.group / 8)];
+    const float s = f16_bits_to_f32(g & 0xffffu), b = f16_bits_to_f32(g >> 16);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      o[j] = pack2(T{}, __builtin_fmaf((float)((w >> (8 * j)) & 15), s, b), __builtin_fmaf((float)((w >> (8 * j + 4)) & 15), s, b));
+  }
+  uint8_t* p = is_v ? a.v_out + tok * a.vo_ts + h * a.vo_hs : a.k_out + tok * a.ko_ts + h * a.ko_hs;
+  *(u32x4_t*)(p + 16 * c) = o;
+}
+
+}  // namespace
+
+hipError_t launch_read4(const Read4Args& a, int dt, hipStream_t s) {
+  const int64_t n = a.t * 2 * a.hk * (a.d / 8);
+  const unsigned grid = (unsigned)((n + 255) / 256);
+  const FastDiv row = fast_div((uint32_t)(a.d / 8)), tok = fast_div((uint32_t)(2 * a.hk));
+  if (dt == DT_BF16)
+    read4_kernel<BF16><<<grid, 256, 0, s>>>(a, row, tok, n);
+  else
+    read4_kernel<F16><<<grid, 256, 0, s>>>(a, row, tok, n);
+  return hipGetLastError();
 }
 
 }  // namespace ql

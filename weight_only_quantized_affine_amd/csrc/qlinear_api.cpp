@@ -111,6 +111,32 @@ ql_status check_cache(const char* fn, const ql_paged_cache* c) {
   return QL_OK;
 }
 
+ql_status check_cache4(const char* fn, const ql_paged_cache4* c) {
+  CHECK(c != nullptr, QL_ERR_NULL, "%s: cache must not be NULL", fn);
+  CHECK(c->n_pages >= 0 && c->page_size >= 1 && c->hk >= 1 && c->hk < (1 << 20), QL_ERR_SHAPE,
+        "%s: the cache needs n_pages >= 0, page_size >= 1 and hk >= 1", fn);
+  CHECK(c->n_pages < (int64_t(1) << 31) && c->page_size < (int64_t(1) << 31) &&
+            c->n_pages * c->page_size < (int64_t(1) << 31),
+        QL_ERR_UNSUPPORTED, "%s: a cache of 2^31 slots or more", fn);
+  CHECK(c->group_size == 32 || c->group_size == 64 || c->group_size == 128, QL_ERR_UNSUPPORTED,
+        "%s: group_size=%lld not supported (32, 64 or 128)", fn, (long long)c->group_size);
+  CHECK(c->d >= 32 && c->d <= 512 && c->d % c->group_size == 0, QL_ERR_UNSUPPORTED,
+        "%s: d=%lld not supported (a multiple of group_size up to 512)", fn, (long long)c->d);
+  CHECK(c->n_pages == 0 || (c->k_codes && c->v_codes && c->k_groups && c->v_groups), QL_ERR_NULL,
+        "%s: the cache's codes and groups must not be NULL", fn);
+  CHECK(aligned(c->k_codes, 16) && aligned(c->v_codes, 16), QL_ERR_ALIGN, "%s: the cache's codes must be 16-byte aligned",
+        fn);
+  CHECK(aligned(c->k_groups, 4) && aligned(c->v_groups, 4), QL_ERR_ALIGN, "%s: the cache's groups must be 4-byte aligned",
+        fn);
+  auto stride16 = [](int64_t s) { return s >= 0 && s % 16 == 0 && s < (int64_t(1) << 40); };
+  auto stride1 = [](int64_t s) { return s >= 0 && s < (int64_t(1) << 38); };
+  CHECK(stride16(c->page_stride) && stride16(c->token_stride) && stride16(c->head_stride), QL_ERR_ALIGN,
+        "%s: the strides of the cache's codes must be multiples of 16 bytes", fn);
+  CHECK(stride1(c->group_page_stride) && stride1(c->group_token_stride) && stride1(c->group_head_stride), QL_ERR_SHAPE,
+        "%s: the strides of the cache's groups must be in [0, 2^38)", fn);
+  return QL_OK;
+}
+
 // Checks of the norm and rotation, and their kernel arguments.
 ql_status norm_rope_args(const char* fn, const ql_norm_rope* nr, int64_t t, int64_t d, const ql_heads* q,
                          const ql_heads* q_out, const ql_heads* k, ql::NormRopeArgs& a) {
@@ -165,6 +191,117 @@ ql_status norm_rope_args(const char* fn, const ql_norm_rope* nr, int64_t t, int6
   a.positions = nr->positions;
   a.cos_sin = nr->cos_sin;
   a.max_pos = nr->max_pos;
+  return QL_OK;
+}
+
+// The arguments of an append that do not hang on how the cache holds its rows.
+ql_status append_args(const char* fn, const ql_heads* q, const ql_heads* q_out, const ql_heads* k, const ql_heads* v,
+                      int64_t n_pages, int64_t page_size, int64_t hk, int64_t d, const int64_t* slots, int64_t t,
+                      const ql_norm_rope* nr, ql::NormRopeArgs& a) {
+  CHECK(k && v, QL_ERR_NULL, "%s: k and v must not be NULL", fn);
+  ql_status st = norm_rope_args(fn, nr, t, d, q, q_out, k, a);
+  if (st == QL_OK) st = check_heads(fn, "v", v, true);
+  if (st != QL_OK) return st;
+  CHECK(k->heads == hk && v->heads == hk, QL_ERR_SHAPE, "%s: k and v must have the cache's %lld heads", fn,
+        (long long)hk);
+  if (t == 0) return ok();
+  CHECK(v->p, QL_ERR_NULL, "%s: v must not be NULL", fn);
+  CHECK(slots, QL_ERR_NULL, "%s: slots must not be NULL", fn);
+  CHECK(aligned(slots, 8), QL_ERR_ALIGN, "%s: slots must be 8-byte aligned", fn);
+  CHECK(t < (int64_t(1) << 31) / (a.hq + 2 * a.hk + 4), QL_ERR_UNSUPPORTED, "%s: 2^31 rows or more", fn);
+  a.v = (const uint8_t*)v->p;
+  a.v_ts = 2 * v->token_stride;
+  a.v_hs = 2 * v->head_stride;
+  a.hv = (int)v->heads;
+  a.slots = slots;
+  a.n_slots = n_pages * page_size;
+  a.page_size = (int)page_size;
+  a.page_div = ql::fast_div((uint32_t)page_size);
+  return QL_OK;
+}
+
+size_t attn_workspace(int64_t t, int64_t n_seqs, int64_t hq, int64_t hk, int64_t d, int64_t max_q, int64_t max_pages,
+                      int64_t page_size, int64_t window, int few_keys) {
+  if (t <= 0 || n_seqs <= 0 || hq <= 0 || hk <= 0 || hq >= (1 << 20) || hq % hk != 0 ||
+      (d != 64 && d != 128 && d != 256) || max_q <= 0 || max_pages < 0 || page_size <= 0 || window < 0 ||
+      t >= kAttnLimit / (hq / hk) || n_seqs >= kAttnLimit || max_pages >= kAttnLimit ||
+      page_size > INT32_MAX || max_pages * page_size >= kAttnLimit)
+    return 0;
+  return ql::attn_plan(t, n_seqs, hq, hk, (int)d, std::min(max_q, t), max_pages * page_size, window, few_keys).bytes;
+}
+
+// Checks and arguments of paged attention that do not hang on how the cache holds its rows, and the plan;
+// nothing: there is nothing to do.
+ql_status attn_args(const char* fn, const ql_heads* q, const ql_heads* out, int64_t t, int64_t n_pages,
+                    int64_t page_size, int64_t hk, int64_t d, const int32_t* block_table, int64_t table_stride,
+                    int64_t max_pages, const int32_t* cu_q, const int32_t* kv_lens, int64_t n_seqs, int64_t max_q,
+                    float scale, int64_t window, const float* sinks, void* workspace, size_t ws_bytes, int few_keys,
+                    ql::AttnArgs& a, ql::AttnPlan& p, bool& nothing) {
+  CHECK(d == 64 || d == 128 || d == 256, QL_ERR_UNSUPPORTED,
+        "%s: d=%lld not supported (64, 128 or 256)", fn, (long long)d);
+  ql_status st = check_heads(fn, "q", q, true);
+  if (st == QL_OK) st = check_heads(fn, "out", out, true);
+  if (st != QL_OK) return st;
+  CHECK(q->heads >= 1 && q->heads % hk == 0 && out->heads == q->heads, QL_ERR_SHAPE,
+        "%s: q and out must have the same heads, a multiple of the cache's %lld", fn, (long long)hk);
+  CHECK(t >= 0 && n_seqs >= 0 && max_q >= 0 && max_pages >= 0 && table_stride >= 0, QL_ERR_SHAPE,
+        "%s: t, n_seqs, max_q, max_pages and table_stride must be >= 0", fn);
+  CHECK(scale > 0.f && scale <= 3.0e38f, QL_ERR_SHAPE, "%s: scale must be finite and > 0", fn);
+  CHECK(window >= 0, QL_ERR_SHAPE, "%s: window=%lld must be >= 0", fn, (long long)window);
+  nothing = t == 0 || n_seqs == 0 || max_q == 0;
+  if (nothing) return ok();
+  CHECK(q->p && out->p, QL_ERR_NULL, "%s: q and out must not be NULL", fn);
+  CHECK(cu_q && kv_lens, QL_ERR_NULL, "%s: cu_q and kv_lens must not be NULL", fn);
+  CHECK(block_table || max_pages == 0, QL_ERR_NULL, "%s: block_table must not be NULL", fn);
+  CHECK(aligned(cu_q, 4) && aligned(kv_lens, 4) && aligned(block_table, 4) && aligned(sinks, 4), QL_ERR_ALIGN,
+        "%s: cu_q, kv_lens, block_table and sinks must be 4-byte aligned", fn);
+  const int64_t g = q->heads / hk;
+  CHECK(t < kAttnLimit / g && n_seqs < kAttnLimit && max_pages < kAttnLimit &&
+            max_pages * page_size < kAttnLimit,
+        QL_ERR_UNSUPPORTED, "%s: t times the query heads of a kv head, n_seqs and the slots of a block-table row must "
+        "be below 2^30", fn);
+  max_q = std::min(max_q, t);
+  const int64_t max_kv = max_pages * page_size;
+  p = ql::attn_plan(t, n_seqs, q->heads, hk, (int)d, max_q, max_kv, window, few_keys);
+  CHECK(p.ok, QL_ERR_UNSUPPORTED, "%s: n_seqs, heads and max_pages give 2^31 units of work or more", fn);
+  CHECK(workspace != nullptr && ws_bytes >= p.bytes, QL_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", fn,
+        workspace ? ws_bytes : (size_t)0, p.bytes);
+  CHECK(aligned(workspace, 16), QL_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
+  a.q = (const uint8_t*)q->p;
+  a.q_ts = 2 * q->token_stride;
+  a.q_hs = 2 * q->head_stride;
+  a.n_pages = (int)n_pages;
+  a.page_size = (int)page_size;
+  a.page_div = ql::fast_div((uint32_t)page_size);
+  a.table = block_table;
+  a.table_stride = table_stride;
+  a.max_kv = (int)max_kv;
+  a.cu_q = cu_q;
+  a.kv_lens = kv_lens;
+  a.n_seqs = (int)n_seqs;
+  a.t = t;
+  a.max_q = (int)max_q;
+  a.hk = (int)hk;
+  a.g = (int)g;
+  a.g_div = ql::fast_div((uint32_t)g);
+  a.sl = scale * 1.4426950408889634f;
+  a.window = window >= max_kv ? 0 : (int)window;  // a window over the whole cache hides nothing
+  a.sinks = sinks;
+  a.out = (uint8_t*)out->p;
+  a.out_ts = 2 * out->token_stride;
+  a.out_hs = 2 * out->head_stride;
+  a.few_rows = p.few_rows;
+  a.nw_few = p.nw_few;
+  a.cap_few = p.cap_few;
+  a.part_floats = p.part_floats;
+  a.join_few = p.join_few;
+  a.nw_tile = p.nw_tile;
+  a.items_tile = p.items_tile;
+  a.plan_tiles = p.plan_tiles;
+  a.join_tile = p.join_tile;
+  a.rec = (ql::AttnRecord*)workspace;
+  a.part = (float*)((uint8_t*)workspace + p.part_off);
+  a.part_tile = (float*)((uint8_t*)workspace + p.part_tile_off);
   return QL_OK;
 }
 
@@ -819,42 +956,20 @@ ql_status qlinear_kv_append(const ql_heads* q, const ql_heads* q_out, const ql_h
   CHECK(is16(dtype), QL_ERR_DTYPE, "%s: dtype must be QL_F16 or QL_BF16", fn);
   ql_status st = check_cache(fn, cache);
   if (st != QL_OK) return st;
-  CHECK(k && v, QL_ERR_NULL, "%s: k and v must not be NULL", fn);
   ql::NormRopeArgs a{};
-  st = norm_rope_args(fn, nr, t, cache->d, q, q_out, k, a);
-  if (st == QL_OK) st = check_heads(fn, "v", v, true);
-  if (st != QL_OK) return st;
-  CHECK(k->heads == cache->hk && v->heads == cache->hk, QL_ERR_SHAPE, "%s: k and v must have the cache's %lld heads",
-        fn, (long long)cache->hk);
-  if (t == 0) return ok();
-  CHECK(v->p, QL_ERR_NULL, "%s: v must not be NULL", fn);
-  CHECK(slots, QL_ERR_NULL, "%s: slots must not be NULL", fn);
-  CHECK(aligned(slots, 8), QL_ERR_ALIGN, "%s: slots must be 8-byte aligned", fn);
-  CHECK(t < (int64_t(1) << 31) / (a.hq + 2 * a.hk + 4), QL_ERR_UNSUPPORTED, "%s: 2^31 rows or more", fn);
-  a.v = (const uint8_t*)v->p;
-  a.v_ts = 2 * v->token_stride;
-  a.v_hs = 2 * v->head_stride;
-  a.hv = (int)v->heads;
+  st = append_args(fn, q, q_out, k, v, cache->n_pages, cache->page_size, cache->hk, cache->d, slots, t, nr, a);
+  if (st != QL_OK || t == 0) return st;
   a.k_out = (uint8_t*)cache->k;
   a.v_out = (uint8_t*)cache->v;
   a.ko_ts = a.vo_ts = 2 * cache->token_stride;
   a.ko_hs = a.vo_hs = 2 * cache->head_stride;
   a.page_stride = 2 * cache->page_stride;
-  a.slots = slots;
-  a.n_slots = cache->n_pages * cache->page_size;
-  a.page_size = (int)cache->page_size;
-  a.page_div = ql::fast_div((uint32_t)cache->page_size);
   return launched(ql::launch_norm_rope(a, dt(dtype), (hipStream_t)stream), fn);
 }
 
 size_t qlinear_paged_attention_workspace_size(int64_t t, int64_t n_seqs, int64_t hq, int64_t hk, int64_t d,
                                               int64_t max_q, int64_t max_pages, int64_t page_size, int64_t window) {
-  if (t <= 0 || n_seqs <= 0 || hq <= 0 || hk <= 0 || hq >= (1 << 20) || hq % hk != 0 ||
-      (d != 64 && d != 128 && d != 256) || max_q <= 0 || max_pages < 0 || page_size <= 0 || window < 0 ||
-      t >= kAttnLimit / (hq / hk) || n_seqs >= kAttnLimit || max_pages >= kAttnLimit ||
-      page_size > INT32_MAX || max_pages * page_size >= kAttnLimit)
-    return 0;
-  return ql::attn_plan(t, n_seqs, hq, hk, (int)d, std::min(max_q, t), max_pages * page_size, window).bytes;
+  return attn_workspace(t, n_seqs, hq, hk, d, max_q, max_pages, page_size, window, ql::kAttnFewKeys);
 }
 
 ql_status qlinear_paged_attention(const ql_heads* q, const ql_heads* out, ql_dtype dtype, int64_t t,
@@ -866,83 +981,227 @@ ql_status qlinear_paged_attention(const ql_heads* q, const ql_heads* out, ql_dty
   CHECK(is16(dtype), QL_ERR_DTYPE, "%s: dtype must be QL_F16 or QL_BF16", fn);
   ql_status st = check_cache(fn, cache);
   if (st != QL_OK) return st;
-  CHECK(cache->d == 64 || cache->d == 128 || cache->d == 256, QL_ERR_UNSUPPORTED,
-        "%s: d=%lld not supported (64, 128 or 256)", fn, (long long)cache->d);
-  st = check_heads(fn, "q", q, true);
-  if (st == QL_OK) st = check_heads(fn, "out", out, true);
-  if (st != QL_OK) return st;
-  CHECK(q->heads >= 1 && q->heads % cache->hk == 0 && out->heads == q->heads, QL_ERR_SHAPE,
-        "%s: q and out must have the same heads, a multiple of the cache's %lld", fn, (long long)cache->hk);
-  CHECK(t >= 0 && n_seqs >= 0 && max_q >= 0 && max_pages >= 0 && table_stride >= 0, QL_ERR_SHAPE,
-        "%s: t, n_seqs, max_q, max_pages and table_stride must be >= 0", fn);
-  CHECK(scale > 0.f && scale <= 3.0e38f, QL_ERR_SHAPE, "%s: scale must be finite and > 0", fn);
-  CHECK(window >= 0, QL_ERR_SHAPE, "%s: window=%lld must be >= 0", fn, (long long)window);
-  if (t == 0 || n_seqs == 0 || max_q == 0) return ok();
-  CHECK(q->p && out->p, QL_ERR_NULL, "%s: q and out must not be NULL", fn);
-  CHECK(cu_q && kv_lens, QL_ERR_NULL, "%s: cu_q and kv_lens must not be NULL", fn);
-  CHECK(block_table || max_pages == 0, QL_ERR_NULL, "%s: block_table must not be NULL", fn);
-  CHECK(aligned(cu_q, 4) && aligned(kv_lens, 4) && aligned(block_table, 4) && aligned(sinks, 4), QL_ERR_ALIGN,
-        "%s: cu_q, kv_lens, block_table and sinks must be 4-byte aligned", fn);
-  const int64_t g = q->heads / cache->hk;
-  CHECK(t < kAttnLimit / g && n_seqs < kAttnLimit && max_pages < kAttnLimit &&
-            max_pages * cache->page_size < kAttnLimit,
-        QL_ERR_UNSUPPORTED, "%s: t times the query heads of a kv head, n_seqs and the slots of a block-table row must "
-        "be below 2^30", fn);
-  max_q = std::min(max_q, t);
-  const int64_t max_kv = max_pages * cache->page_size;
-  const ql::AttnPlan p = ql::attn_plan(t, n_seqs, q->heads, cache->hk, (int)cache->d, max_q, max_kv, window);
-  CHECK(p.ok, QL_ERR_UNSUPPORTED, "%s: n_seqs, heads and max_pages give 2^31 units of work or more", fn);
-  CHECK(workspace != nullptr && ws_bytes >= p.bytes, QL_ERR_WORKSPACE, "%s: workspace has %zu bytes, needs %zu", fn,
-        workspace ? ws_bytes : (size_t)0, p.bytes);
-  CHECK(aligned(workspace, 16), QL_ERR_ALIGN, "%s: workspace must be 16-byte aligned", fn);
   ql::AttnArgs a{};
-  a.q = (const uint8_t*)q->p;
-  a.q_ts = 2 * q->token_stride;
-  a.q_hs = 2 * q->head_stride;
+  ql::AttnPlan p;
+  bool nothing;
+  st = attn_args(fn, q, out, t, cache->n_pages, cache->page_size, cache->hk, cache->d, block_table, table_stride,
+                 max_pages, cu_q, kv_lens, n_seqs, max_q, scale, window, sinks, workspace, ws_bytes, ql::kAttnFewKeys, a,
+                 p, nothing);
+  if (st != QL_OK || nothing) return st;
   a.k = (const uint8_t*)cache->k;
   a.v = (const uint8_t*)cache->v;
   a.page_stride = 2 * cache->page_stride;
   a.token_stride = 2 * cache->token_stride;
   a.head_stride = 2 * cache->head_stride;
-  a.n_pages = (int)cache->n_pages;
-  a.page_size = (int)cache->page_size;
   a.page16 = cache->page_size % 16 == 0 && a.token_stride < (int64_t(1) << 27);
-  a.page_div = ql::fast_div((uint32_t)cache->page_size);
-  a.table = block_table;
-  a.table_stride = table_stride;
-  a.max_kv = (int)max_kv;
-  a.cu_q = cu_q;
-  a.kv_lens = kv_lens;
-  a.n_seqs = (int)n_seqs;
-  a.t = t;
-  a.max_q = (int)max_q;
-  a.hk = (int)cache->hk;
-  a.g = (int)g;
-  a.g_div = ql::fast_div((uint32_t)g);
-  a.sl = scale * 1.4426950408889634f;
-  a.window = window >= max_kv ? 0 : (int)window;  // a window over the whole cache hides nothing
-  a.sinks = sinks;
-  a.out = (uint8_t*)out->p;
-  a.out_ts = 2 * out->token_stride;
-  a.out_hs = 2 * out->head_stride;
-  a.few_rows = p.few_rows;
-  a.nw_few = p.nw_few;
-  a.cap_few = p.cap_few;
-  a.part_floats = p.part_floats;
-  a.join_few = p.join_few;
-  a.nw_tile = p.nw_tile;
-  a.items_tile = p.items_tile;
-  a.plan_tiles = p.plan_tiles;
-  a.join_tile = p.join_tile;
-  a.rec = (ql::AttnRecord*)workspace;
-  a.part = (float*)((uint8_t*)workspace + p.part_off);
-  a.part_tile = (float*)((uint8_t*)workspace + p.part_tile_off);
   const hipStream_t s = (hipStream_t)stream;
   hipError_t e = hipSuccess;
   if (p.tile) e = ql::launch_attn_tile(a, dt(dtype), (int)cache->d, s);
   if (e == hipSuccess && p.nc) e = ql::launch_attn_few(a, dt(dtype), (int)cache->d, p.nc, s);
   if (e == hipSuccess) e = ql::launch_attn_join(a, dt(dtype), (int)cache->d, s);
   return launched(e, fn);
+}
+
+size_t qlinear_paged_attention_4bit_workspace_size(int64_t t, int64_t n_seqs, int64_t hq, int64_t hk, int64_t d,
+                                                   int64_t max_q, int64_t max_pages, int64_t page_size, int64_t window) {
+  return attn_workspace(t, n_seqs, hq, hk, d, max_q, max_pages, page_size, window, ql::kAttnFewKeys4);
+}
+
+ql_status qlinear_paged_attention_4bit(const ql_heads* q, const ql_heads* out, ql_dtype dtype, int64_t t,
+                                       const ql_paged_cache4* cache, const int32_t* block_table, int64_t table_stride,
+                                       int64_t max_pages, const int32_t* cu_q, const int32_t* kv_lens, int64_t n_seqs,
+                                       int64_t max_q, float scale, int64_t window, const float* sinks, void* workspace,
+                                       size_t ws_bytes, void* stream) {
+  const char* fn = "qlinear_paged_attention_4bit";
+  CHECK(is16(dtype), QL_ERR_DTYPE, "%s: dtype must be QL_F16 or QL_BF16", fn);
+  ql_status st = check_cache4(fn, cache);
+  if (st != QL_OK) return st;
+  ql::AttnArgs4 a{};
+  ql::AttnPlan p;
+  bool nothing;
+  st = attn_args(fn, q, out, t, cache->n_pages, cache->page_size, cache->hk, cache->d, block_table, table_stride,
+                 max_pages, cu_q, kv_lens, n_seqs, max_q, scale, window, sinks, workspace, ws_bytes, ql::kAttnFewKeys4, a,
+                 p, nothing);
+  if (st != QL_OK || nothing) return st;
+  a.k = (const uint8_t*)cache->k_codes;
+  a.v = (const uint8_t*)cache->v_codes;
+  a.page_stride = cache->page_stride;
+  a.token_stride = cache->token_stride;
+  a.head_stride = cache->head_stride;
+  a.page16 = cache->page_size % 16 == 0 && a.token_stride < (int64_t(1) << 27);
+  a.kp = (const uint8_t*)cache->k_groups;
+  a.vp = (const uint8_t*)cache->v_groups;
+  a.p_page_stride = 4 * cache->group_page_stride;
+  a.p_token_stride = 4 * cache->group_token_stride;
+  a.p_head_stride = 4 * cache->group_head_stride;
+  a.group_log2 = cache->group_size == 32 ? 5 : cache->group_size == 64 ? 6 : 7;
+  a.io = dt(dtype);
+  const hipStream_t s = (hipStream_t)stream;
+  hipError_t e = hipSuccess;
+  if (p.tile) e = ql::launch_attn_tile4(a, (int)cache->d, s);
+  if (e == hipSuccess && p.nc) e = ql::launch_attn_few4(a, (int)cache->d, p.nc, s);
+  if (e == hipSuccess) e = ql::launch_attn_join(a, dt(dtype), (int)cache->d, s);
+  return launched(e, fn);
+}
+
+ql_status qlinear_kv_append_4bit(const ql_heads* q, const ql_heads* q_out, const ql_heads* k, const ql_heads* v,
+                                 const ql_paged_cache4* cache, const int64_t* slots, ql_dtype dtype, int64_t t,
+                                 const ql_norm_rope* nr, void* stream) {
+  const char* fn = "qlinear_kv_append_4bit";
+  CHECK(is16(dtype), QL_ERR_DTYPE, "%s: dtype must be QL_F16 or QL_BF16", fn);
+  ql_status st = check_cache4(fn, cache);
+  if (st != QL_OK) return st;
+  ql::Append4Args a{};
+  st = append_args(fn, q, q_out, k, v, cache->n_pages, cache->page_size, cache->hk, cache->d, slots, t, nr, a);
+  if (st != QL_OK || t == 0) return st;
+  a.k_out = (uint8_t*)cache->k_codes;
+  a.v_out = (uint8_t*)cache->v_codes;
+  a.ko_ts = a.vo_ts = cache->token_stride;
+  a.ko_hs = a.vo_hs = cache->head_stride;
+  a.page_stride = cache->page_stride;
+  a.k_groups = cache->k_groups;
+  a.v_groups = cache->v_groups;
+  a.group_ps = cache->group_page_stride;
+  a.group_ts = cache->group_token_stride;
+  a.group_hs = cache->group_head_stride;
+  a.group = (int)cache->group_size;
+  return launched(ql::launch_append4(a, dt(dtype), (hipStream_t)stream), fn);
+}
+
+ql_status qlinear_kv_read_4bit(const ql_paged_cache4* cache, const int64_t* slots, int64_t t, const ql_heads* k_out,
+                               const ql_heads* v_out, ql_dtype dtype, void* stream) {
+  const char* fn = "qlinear_kv_read_4bit";
+  CHECK(is16(dtype), QL_ERR_DTYPE, "%s: dtype must be QL_F16 or QL_BF16", fn);
+  ql_status st = check_cache4(fn, cache);
+  if (st == QL_OK) st = check_heads(fn, "k_out", k_out, true);
+  if (st == QL_OK) st = check_heads(fn, "v_out", v_out, true);
+  if (st != QL_OK) return st;
+  CHECK(t >= 0, QL_ERR_SHAPE, "%s: t=%lld must be >= 0", fn, (long long)t);
+  CHECK(k_out->heads == cache->hk && v_out->heads == cache->hk, QL_ERR_SHAPE,
+        "%s: k_out and v_out must have the cache's %lld heads", fn, (long long)cache->hk);
+  if (t == 0) return ok();
+  CHECK(slots && k_out->p && v_out->p, QL_ERR_NULL, "%s: slots, k_out and v_out must not be NULL", fn);
+  CHECK(aligned(slots, 8), QL_ERR_ALIGN, "%s: slots must be 8-byte aligned", fn);
+  CHECK(t < (int64_t(1) << 31) / (2 * cache->hk * (cache->d / 8)) - 256, QL_ERR_UNSUPPORTED, "%s: 2^34 values or more", fn);
+  ql::Read4Args a{};
+  a.k = (const uint8_t*)cache->k_codes;
+  a.v = (const uint8_t*)cache->v_codes;
+  a.page_stride = cache->page_stride;
+  a.token_stride = cache->token_stride;
+  a.head_stride = cache->head_stride;
+  a.kg = cache->k_groups;
+  a.vg = cache->v_groups;
+  a.group_ps = cache->group_page_stride;
+  a.group_ts = cache->group_token_stride;
+  a.group_hs = cache->group_head_stride;
+  a.k_out = (uint8_t*)k_out->p;
+  a.v_out = (uint8_t*)v_out->p;
+  a.ko_ts = 2 * k_out->token_stride;
+  a.ko_hs = 2 * k_out->head_stride;
+  a.vo_ts = 2 * v_out->token_stride;
+  a.vo_hs = 2 * v_out->head_stride;
+  a.slots = slots;
+  a.n_slots = cache->n_pages * cache->page_size;
+  a.page_size = (int)cache->page_size;
+  a.page_div = ql::fast_div((uint32_t)cache->page_size);
+  a.hk = (int)cache->hk;
+  a.d = (int)cache->d;
+  a.group = (int)cache->group_size;
+  a.t = t;
+  return launched(ql::launch_read4(a, dt(dtype), (hipStream_t)stream), fn);
+}
+
+ql_status qlinear_kv_extend(const int32_t* counts, const int32_t* lens, int64_t n_seqs, int32_t* block_table,
+                            int64_t table_stride, int64_t max_pages, int64_t page_size, int32_t* free_pages,
+                            int64_t free_cap, const int32_t* free_count, int32_t* lens_out, int32_t* free_count_out,
+                            int32_t* cu_q, int64_t* positions, int64_t* slots, int64_t rows, int32_t* info,
+                            void* stream) {
+  const char* fn = "qlinear_kv_extend";
+  const int64_t limit = int64_t(1) << 31;
+  CHECK(n_seqs >= 0 && rows >= 0 && max_pages >= 0 && table_stride >= 0 && free_cap >= 0, QL_ERR_SHAPE,
+        "%s: n_seqs, rows, max_pages, table_stride and free_cap must be >= 0", fn);
+  CHECK(page_size >= 1, QL_ERR_SHAPE, "%s: page_size=%lld must be >= 1", fn, (long long)page_size);
+  CHECK(n_seqs < (int64_t(1) << 24) && rows < limit - 4096 && free_cap < limit && max_pages < limit && page_size < limit &&
+            max_pages * page_size < limit,
+        QL_ERR_UNSUPPORTED, "%s: n_seqs must be below 2^24; rows, free_cap and the slots of a block-table row below 2^31",
+        fn);
+  CHECK(table_stride < (int64_t(1) << 38), QL_ERR_SHAPE, "%s: table_stride must be below 2^38", fn);
+  CHECK(n_seqs <= 1 || table_stride >= max_pages, QL_ERR_SHAPE, "%s: rows of block_table must not overlap", fn);
+  CHECK(cu_q && info, QL_ERR_NULL, "%s: cu_q and info must not be NULL", fn);
+  CHECK(n_seqs == 0 || (counts && lens && lens_out), QL_ERR_NULL, "%s: counts, lens and lens_out must not be NULL", fn);
+  CHECK(n_seqs == 0 || max_pages == 0 || block_table, QL_ERR_NULL, "%s: block_table must not be NULL", fn);
+  CHECK(rows == 0 || (positions && slots), QL_ERR_NULL, "%s: positions and slots must not be NULL", fn);
+  CHECK(!free_pages || (free_count && free_count_out), QL_ERR_NULL,
+        "%s: free_count and free_count_out must not be NULL with free_pages", fn);
+  CHECK(free_pages || (free_cap == 0 && !free_count && !free_count_out), QL_ERR_NULL,
+        "%s: free_pages must not be NULL with free_cap, free_count or free_count_out", fn);
+  CHECK(aligned(counts, 4) && aligned(lens, 4) && aligned(block_table, 4) && aligned(free_pages, 4) &&
+            aligned(free_count, 4) && aligned(lens_out, 4) && aligned(free_count_out, 4) && aligned(cu_q, 4) &&
+            aligned(info, 4) && aligned(positions, 8) && aligned(slots, 8),
+        QL_ERR_ALIGN, "%s: positions and slots must be 8-byte aligned, the others 4-byte", fn);
+  ql::ExtendArgs a{};
+  a.counts = counts;
+  a.lens = lens;
+  a.n_seqs = (int)n_seqs;
+  a.table = block_table;
+  a.table_stride = table_stride;
+  a.max_pages = max_pages;
+  a.page_size = (int)page_size;
+  a.page_div = ql::fast_div((uint32_t)page_size);
+  a.free_pages = free_pages;
+  a.free_cap = free_cap;
+  a.free_count = free_count;
+  a.lens_out = lens_out;
+  a.free_count_out = free_count_out;
+  a.cu_q = cu_q;
+  a.positions = positions;
+  a.slots = slots;
+  a.rows = rows;
+  a.info = info;
+  return launched(ql::launch_kv_extend(a, (hipStream_t)stream), fn);
+}
+
+ql_status qlinear_select_experts(const void* logits, ql_dtype dtype, int64_t t, int64_t e, int64_t row_stride,
+                                 const float* bias, int sigmoid, int64_t n_groups, int64_t top_groups, int group_top,
+                                 int64_t k, int renormalize, float scale, const int32_t* n_rows, int64_t* ids,
+                                 float* weights, void* stream) {
+  const char* fn = "qlinear_select_experts";
+  CHECK(is_out(dtype), QL_ERR_DTYPE, "%s: dtype must be QL_F32, QL_F16 or QL_BF16", fn);
+  CHECK(t >= 0 && t < (int64_t(1) << 31), QL_ERR_SHAPE, "%s: t=%lld must be in [0, 2^31)", fn, (long long)t);
+  CHECK(e >= 1 && e <= 1024, QL_ERR_UNSUPPORTED, "%s: e=%lld not supported (1 to 1024)", fn, (long long)e);
+  CHECK(n_groups >= 1 && n_groups <= 64 && e % n_groups == 0, QL_ERR_SHAPE,
+        "%s: n_groups=%lld must be in [1, 64] and divide e=%lld", fn, (long long)n_groups, (long long)e);
+  CHECK(top_groups >= 1 && top_groups <= n_groups, QL_ERR_SHAPE, "%s: top_groups=%lld must be in [1, n_groups]", fn,
+        (long long)top_groups);
+  CHECK(group_top == 1 || group_top == 2, QL_ERR_SHAPE, "%s: group_top=%d must be 1 or 2", fn, group_top);
+  CHECK(k >= 1 && k <= 64 && k <= top_groups * (e / n_groups), QL_ERR_SHAPE,
+        "%s: k=%lld must be in [1, 64] and at most the experts of top_groups groups", fn, (long long)k);
+  CHECK(row_stride >= 0 && row_stride < (int64_t(1) << 40), QL_ERR_SHAPE, "%s: row_stride must be in [0, 2^40)", fn);
+  CHECK(scale >= -3.0e38f && scale <= 3.0e38f, QL_ERR_SHAPE, "%s: scale must be finite", fn);
+  if (t == 0) return ok();
+  CHECK(logits && ids && weights, QL_ERR_NULL, "%s: logits, ids and weights must not be NULL", fn);
+  CHECK(aligned(logits, esize(dtype)) && aligned(ids, 8) && aligned(weights, 4) && aligned(bias, 4) && aligned(n_rows, 4),
+        QL_ERR_ALIGN, "%s: logits must be aligned to their type, ids to 8 bytes, weights, bias and n_rows to 4", fn);
+  ql::SelectArgs a{logits,        dt(dtype),       t,         row_stride,       (int)e, (int)k, bias, sigmoid ? 1 : 0,
+                   (int)n_groups, (int)top_groups, group_top, renormalize ? 1 : 0, scale,  n_rows, ids,  weights};
+  return launched(ql::launch_select_experts(a, (hipStream_t)stream), fn);
+}
+
+ql_status qlinear_combine_experts(const void* y, ql_dtype dtype, const float* weights, const int64_t* ids, int64_t e,
+                                  const void* residual, int64_t t, int64_t k, int64_t n, void* out, void* stream) {
+  const char* fn = "qlinear_combine_experts";
+  CHECK(is_out(dtype), QL_ERR_DTYPE, "%s: dtype must be QL_F32, QL_F16 or QL_BF16", fn);
+  CHECK(t >= 0 && n >= 0 && e >= 0, QL_ERR_SHAPE, "%s: t, n and e must be >= 0", fn);
+  CHECK(k >= 1 && k <= 64, QL_ERR_SHAPE, "%s: k=%lld must be in [1, 64]", fn, (long long)k);
+  if (t == 0 || n == 0) return ok();
+  CHECK(t < (int64_t(1) << 31) && n < (int64_t(1) << 31) && t * n < (int64_t(1) << 31) - 256, QL_ERR_UNSUPPORTED,
+        "%s: 2^31 outputs or more", fn);
+  CHECK(y && weights && out, QL_ERR_NULL, "%s: y, weights and out must not be NULL", fn);
+  CHECK(aligned(y, esize(dtype)) && aligned(residual, esize(dtype)) && aligned(out, esize(dtype)) && aligned(weights, 4) &&
+            aligned(ids, 8),
+        QL_ERR_ALIGN, "%s: y, residual and out must be aligned to their type, weights to 4 bytes, ids to 8", fn);
+  ql::CombineArgs a{y, dt(dtype), weights, ids, e, residual, t, k, n, out};
+  return launched(ql::launch_combine_experts(a, (hipStream_t)stream), fn);
 }
 
 }  // extern "C"
