@@ -433,8 +433,9 @@ ql_status qlinear_kv_read_4bit(const ql_paged_cache4* cache, const int64_t* slot
                                const ql_heads* v_out, ql_dtype dtype, void* stream);
 
 /* qlinear_paged_attention over such a cache; arguments, masks, sinks, limits and workspace as there, dtype that of
- * q and out.  Cached values enter the products rounded to fp16 (values past 65504 are infinite, below 2^-14
- * they keep an absolute 2^-25), q with 11 significant bits (bf16: exact), the softmax weights rounded to fp16. */
+ * q and out.  Keys enter as they are or rounded to fp16 (below 2^-14 an absolute 2^-25), q with 11 significant bits
+ * (bf16: exact); values, weights, or products of a weight and a scale, round to fp16 before they are summed in fp32.
+ * A cached value past 65504 may be taken as infinite. */
 size_t qlinear_paged_attention_4bit_workspace_size(int64_t t, int64_t n_seqs, int64_t hq, int64_t hk, int64_t d,
                                                    int64_t max_q, int64_t max_pages, int64_t page_size, int64_t window);
 ql_status qlinear_paged_attention_4bit(const ql_heads* q, const ql_heads* out, ql_dtype dtype, int64_t t,

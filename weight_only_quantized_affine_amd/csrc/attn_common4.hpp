@@ -1,9 +1,11 @@
 // Paged attention over a cache in 4 bits: what the two kernels (attn_few4.hip, attn_tile.hip) share.
 //
-// Both products run in fp16 whatever the type of q and out: keys and values are decoded to fp16 (rounded
-// once, 2^-12 of the value, where bf16 would take 2^-9), q enters as fp16 after an exact scaling of each
-// row by a power of two that its scores take back, and the softmax weights round to fp16.
+// Both products run in fp16 whatever the type of q and out: q enters as fp16 after an exact scaling of each
+// row by a power of two that its scores take back, and the softmax weights round to fp16 (2^-12 of the value,
+// where bf16 would take 2^-9).
 #pragma once
+#include <type_traits>
+
 #include "attn_common.hpp"
 #include "cache4.hpp"
 
@@ -42,6 +44,27 @@ __device__ __forceinline__ void copy4(const uint8_t* src, uint8_t* dst) {
                : "s"(lds_at(dst)), "v"(src)
                : "memory", "m0");
 }
+// From a uniform base plus the lane's offset (as copy16_from).
+__device__ __forceinline__ void copy4_from(int64_t base, uint32_t off, uint8_t* dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tglobal_load_lds_dword %1, %2 nt"
+               :
+               : "s"(lds_at(dst)), "v"(off), "s"(base)
+               : "memory", "m0");
+}
 #pragma clang diagnostic pop
+
+// The largest of the wave's values, uniform.
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+  auto step = [&](auto ctrl) {
+    x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, decltype(ctrl)::value, 0xf, 0xf, false));
+  };
+  step(std::integral_constant<int, 0xB1>{});
+  step(std::integral_constant<int, 0x4E>{});
+  step(std::integral_constant<int, 0x141>{});
+  step(std::integral_constant<int, 0x140>{});
+  const uint32_t a = max(__builtin_amdgcn_readlane(x, 0), __builtin_amdgcn_readlane(x, 16));
+  const uint32_t b = max(__builtin_amdgcn_readlane(x, 32), __builtin_amdgcn_readlane(x, 48));
+  return max(a, b);
+}
 
 }  // namespace ql

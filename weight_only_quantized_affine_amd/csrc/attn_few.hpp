@@ -11,14 +11,13 @@ struct FewRun {
   int u0, u1, s, base, W, nw, w, item_units;
   AttnRecord* rec;
 };
-// False where the workgroup has nothing to do.  Units are tiles of KEYS positions; 256 threads.
-template <int KEYS>
+// False where the workgroup has nothing to do.  Units are tiles of KEYS positions; an item counts ITEM units for
+// its start and end where a workgroup has LONG tiles or more; 256 threads.
+template <int KEYS, int ITEM, int LONG>
 __device__ __forceinline__ bool few_run(const AttnArgs& a, int* ssh, int* sfound, FewRun& run) {
   const int tid = threadIdx.x;
   // This workgroup's run of units: all sequences' tiles, head by head, end to end.
-  // Where the runs are long each item has two units for its start and end before its first tile (64
-  // ragged sequences: 146 -> 138 us); short runs are better off with the tiles spread evenly (8
-  // sequences, window 1024: 17.4 against 19.1 us).
+  // Short runs are better off with the tiles spread evenly, without units for start and end.
   int& item_units = run.item_units;
   item_units = 0;
   auto cost = [&](int s) -> int {
@@ -40,8 +39,8 @@ __device__ __forceinline__ bool few_run(const AttnArgs& a, int* ssh, int* sfound
     }
   };
   measure();
-  if (W >= 20 * a.nw_few) {
-    item_units = 2;
+  if (W >= LONG * a.nw_few) {
+    item_units = ITEM;
     measure();
   }
   const int nw = min(a.nw_few, W);
@@ -77,14 +76,14 @@ __device__ __forceinline__ bool few_run(const AttnArgs& a, int* ssh, int* sfound
   return true;
 }
 
-// The end of an item: joins the waves' sums (m, l, o of the wave's columns) in LDS, wave_bytes apart from
+// The end of an item, by thread tid of 256: joins the waves' sums (m, l, o of the wave's columns) in LDS, wave_bytes apart from
 // sm, and stores the rows, or the piece where the item is not `whole`; `starts`: the piece is its first.
 template <int D, int NC, class Store>
-__device__ __forceinline__ void few_finish(const AttnArgs& a, uint8_t* sm, int wave_bytes, float (*sml)[16 * NC][2],
+__device__ __forceinline__ void few_finish(const AttnArgs& a, int tid, uint8_t* sm, int wave_bytes, float (*sml)[16 * NC][2],
                                            f32x4_t (*o)[D / 16], const float* m, float* l, int w, const AttnSeq& q,
                                            int head, int rows, bool starts, bool whole, Store&& store) {
   constexpr int ND = D / 16;
-  const int tid = threadIdx.x, lane = tid & 63;
+  const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, col = lane & 15;
 #pragma unroll

@@ -1,16 +1,26 @@
 // Paged attention over a cache in 4 bits, few rows: as attn_few.hip (whose division of the work and end of
 // an item it shares), with 64 positions a wave and 256 a workgroup's tile.
 //
-// The codes are decoded in registers, between LDS and the matrix cores.  K: a lane of the 16x16x32 product
-// holds one key and, of its row, words of eight codes under one scale, so a word becomes an operand by
-// 13 instructions (one shift, four masks under exponent bits, four exact differences, four fused products
-// with scale and bias).  V: the 4-bit transposing LDS read hands a lane the codes of 16 keys for one
-// of the d values, in any order of the keys that the reading lanes' addresses give: the order in which the
-// lane holds the scores of those keys, so that the weights are the other operand as they are.  The
-// scales and biases of a lane's 16 keys are put into pairs once per group of values.
+// No value is decoded.  A code masked into the low bits of a half is the fp16 subnormal c 2^-24, or 16 c 2^-24
+// four bits further up, so a word of eight codes becomes an operand of the 16x16x32 product by one shift and
+// four masks, and scales and biases enter in fp32:
+//   scores   q.k = sum over groups of s (q.c) + b sum(q), one accumulator a group;
+//   output   sum_j w_j v_j = sum_j (w_j s_j) (c_j - 8) + sum_j w_j (b_j + 8 s_j), the products w s rounded to
+//            fp16 (the only rounding, and as large as one of w in w v, since a group's middle is taken out),
+//            their sum taken out 8 times, the last sum on the vector units.
+// The factors 16 are taken out of q and of the weights.  So that w s stays within fp16 and keeps its small
+// values, a group's products are held times 2^(7 - E), E the exponent of its largest scale that the row has met:
+// they are below 2^15, and keys that a row does not see change no bit of it.
+// V: the 4-bit transposing LDS read hands a lane the codes of 16 keys for one of the d values, in any order
+// of the keys that the reading lanes' addresses give: the order in which the lane holds the scores.
+// (Decoding every code to fp16 by 13 instructions a word: 131071 tokens 54 us, 64 ragged sequences 105.)
 #include "attn_common4.hpp"
 #include "attn_few.hpp"
 
+#ifndef QL_IU
+#define QL_IU 3
+#define QL_TH 4
+#endif
 namespace ql {
 namespace {
 
@@ -20,41 +30,56 @@ __device__ __forceinline__ u32x2_t read_tr4(const uint8_t* p) {
   return __builtin_bit_cast(u32x2_t, __builtin_amdgcn_ds_read_tr4_b64_v2i32((at_lds_i32x2*)p));
 }
 
-// Position of 16-byte chunk c of row r (of D / 32 chunks).  K is read 16 rows at one chunk (D = 256: rows are
-// half the LDS's 256 bytes of banks); V by 16 lanes at one chunk of the rows i + 16 k, i and k = 0 .. 3.
-template <int D> __device__ __forceinline__ int swz4_k(int r) { return D == 256 ? (r & 7) : 0; }
+// Position of 16-byte chunk c of row r (of D / 32 chunks): the reads of K take 16 rows at one place, those of V
+// the rows i + 16 k, i and k = 0 .. 3; either set's positions are distinct modulo the LDS's 256 bytes of banks.
+template <int D> __device__ __forceinline__ int swz4_k(int r) {
+  return D == 256 ? ((r >> 1) & 7) : D == 128 ? ((r >> 2) & 3) : ((r >> 3) & 1);
+}
 template <int D> __device__ __forceinline__ int swz4_v(int r) {
   if (D == 256) return ((r >> 1) & 1) | (((r >> 4) & 3) << 1);
   return D == 128 ? ((r >> 4) & 3) : ((r >> 4) & 1);
 }
 
-// The 64 cache rows of a wave's tile (positions base .. base + 63, a multiple of 64), K and V alike, and
-// the words of their groups; tiles are STEP positions apart.  Lane l looks up row l.
+// The 64 cache rows of a wave's tile (positions base .. base + 63), K and V alike, and the words of their
+// groups; tiles are STEP positions apart.
+//
+// Where pages are multiples of 16 slots (a.page16) the places of the 4 runs of the next 16 tiles are worked
+// out at once, a run a lane, and a tile whose rows are all to be seen is copied from scalar bases and lane
+// offsets that never change.  Else row l is looked up by lane l and handed to the lanes that copy it.
 template <int D, int GROUP, int STEP> struct Copy4 {
   static constexpr int CH = D / 32;          // 16-byte chunks of a row
   static constexpr int RPI = 64 / CH;        // rows of an instruction (1 KB)
   static constexpr int NI = 64 / RPI;        // instructions of a tile
   static constexpr int GP = D / GROUP;       // groups of a row
-  static constexpr int COPIES = NI + GP;     // all instructions of K, and of V
-  static constexpr int BLOCK = 16;           // tiles whose page ids are read at once
-  int ids, block;   // a.page16: pages of the runs of BLOCK tiles (lane t + 16 u: tile t, run u), position of the first
-  int id, base;     // else: page of the lane's row
-  bool whole;       // uniform: every row is to be seen and pages hold runs of 16
-  int64_t at[4];    // uniform, where whole: the runs' places
-  int64_t row;      // the lane's row among the codes, -1 for a row that is not to be seen
-  int64_t prow;     // and among the words
-  uint64_t seen;    // bit r: row r is to be seen
+  static constexpr int WI = GP > 4 ? 8 : 4;  // instructions of a tile's words: 16 rows of up to 4 groups each
+  static constexpr int COPIES = NI + WI;     // all instructions of K, and of V
+  int64_t run, wrun;  // a.page16: a run's place among the codes and the words (lane t + 16 u: tile t, run u)
+  uint64_t known;     // bit of each such lane: its page is in the cache
+  int block;          // position of the first of the 16 tiles
+  int id, base;       // else: page of the lane's row; first position
+  bool whole;         // uniform: every row is to be seen and pages hold runs of 16
+  int tile;           // uniform, where whole: the tile among the 16
+  int64_t row, wrow;  // else: the lane's row, -1 for a row that is not to be seen
+  uint64_t seen;      // bit r: row r is to be seen
 
+  __device__ __forceinline__ int64_t place(const AttnArgs4& a, int id, int p) const {
+    return (int64_t)id * a.page_stride + (int64_t)(p - (int)a.page_div.div((uint32_t)p) * a.page_size) * a.token_stride;
+  }
+  __device__ __forceinline__ int64_t word_place(const AttnArgs4& a, int id, int p) const {
+    return (int64_t)id * a.p_page_stride + (int64_t)(p - (int)a.page_div.div((uint32_t)p) * a.page_size) * a.p_token_stride;
+  }
   __device__ __forceinline__ void lookup(const AttnArgs4& a, const int32_t* table, int first, int lo, int hi, int lane,
                                          bool begins) {
     base = first;
     if (a.page16) {
-      if (begins || first - block >= BLOCK * STEP) {
+      if (begins || first - block >= 16 * STEP) {
         block = first;
         const int p = first + (lane & 15) * STEP + (lane >> 4) * 16;
-        ids = -1;
-        if (p + 16 > lo && p < hi) ids = table[a.page_div.div((uint32_t)p)];
-        asm volatile("" : "+v"(ids));  // the wait for the load is here
+        int i = -1;
+        if (p + 16 > lo && p < hi) i = table[a.page_div.div((uint32_t)p)];
+        known = __ballot((uint32_t)i < (uint32_t)a.n_pages);  // the wait for the load is here
+        run = place(a, i, p);
+        wrun = word_place(a, i, p);
       }
     } else {
       const int p = first + lane;
@@ -62,96 +87,146 @@ template <int D, int GROUP, int STEP> struct Copy4 {
       if (p >= lo && p < hi) id = table[a.page_div.div((uint32_t)p)];
     }
   }
+  __device__ __forceinline__ int64_t lane64(int64_t x, int l) const {
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)x, l), hi = __builtin_amdgcn_readlane((int)(uint32_t)(x >> 32), l);
+    return (int64_t)((uint64_t)hi << 32 | lo);
+  }
   __device__ __forceinline__ void resolve(const AttnArgs4& a, int lo, int hi, int lane) {
-    const int p = base + lane;
-    const int tile = a.page16 ? (base - block) / STEP : 0;
-    if (a.page16) id = __shfl(ids, (lane & 48) + tile);
-    const int in = p - (int)a.page_div.div((uint32_t)p) * a.page_size;
-    const bool see = p >= lo && p < hi && (uint32_t)id < (uint32_t)a.n_pages;
-    seen = __ballot(see);
-    prow = see ? (int64_t)id * a.p_page_stride + (int64_t)in * a.p_token_stride : -1;
-    whole = a.page16 && seen == ~0ull;
-    if (whole) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int pu = base + 16 * u, iu = __builtin_amdgcn_readlane(ids, tile + 16 * u);
-        at[u] = (int64_t)iu * a.page_stride + (int64_t)(pu - (int)a.page_div.div((uint32_t)pu) * a.page_size) * a.token_stride;
+    whole = false;
+    if (a.page16) {
+      constexpr uint64_t kRuns = 0x0001000100010001ull;
+      tile = (base - block) / STEP;
+      whole = ((known >> tile) & kRuns) == kRuns && base >= lo && base + 64 <= hi;
+      seen = ~0ull;
+    }
+    if (!whole) {
+      const int p = base + lane;
+      bool see = p >= lo && p < hi;
+      if (a.page16) {
+        const int from = (lane & 48) + tile;
+        row = (int64_t)((uint64_t)(uint32_t)__shfl((int)(run >> 32), from) << 32 | (uint32_t)__shfl((int)(uint32_t)run, from));
+        wrow = (int64_t)((uint64_t)(uint32_t)__shfl((int)(wrun >> 32), from) << 32 | (uint32_t)__shfl((int)(uint32_t)wrun, from));
+        see = see && ((known >> from) & 1);
+        row += (int64_t)(lane & 15) * a.token_stride;
+        wrow += (int64_t)(lane & 15) * a.p_token_stride;
+      } else {
+        see = see && (uint32_t)id < (uint32_t)a.n_pages;
+        row = place(a, id, p);
+        wrow = word_place(a, id, p);
       }
-    } else {
-      row = see ? (int64_t)id * a.page_stride + (int64_t)in * a.token_stride : -1;
+      seen = __ballot(see);
+      if (!see) row = wrow = -1;
     }
   }
-  // Starts the copies of the codes to dst (rows back to back) and of the words to wdst (64 of each group).
+  // Starts the copies of the codes to dst (rows back to back) and of the words to wdst ([run][group][16 rows]).
   template <bool IS_V>
   __device__ __forceinline__ void copy(const AttnArgs4& a, const uint8_t* head, const uint8_t* words, uint8_t* dst,
                                        uint8_t* wdst, int lane) const {
+    asm volatile("" : "+v"(lane));  // the lane's places are worked out here, not kept in registers
     const int c = lane % CH, r0 = lane / CH;
+    auto chunk = [&](int r) { return (c ^ (IS_V ? swz4_v<D>(r) : swz4_k<D>(r))) * 16; };
     if (whole) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const int r = i * RPI + r0;  // its run: i * RPI / 16, where an instruction lies in one
-        const int cc = c ^ (IS_V ? swz4_v<D>(r) : swz4_k<D>(r));
+        const int r = i * RPI + r0;
         if constexpr (RPI <= 16) {
-          const uint32_t off = (uint32_t)(r & 15) * (uint32_t)a.token_stride + cc * 16;
-          copy16_from<true, false>(uniform64((int64_t)(uintptr_t)head + at[i * RPI / 16]), off, 0, dst + i * 1024);
+          const uint32_t off = (uint32_t)(r & 15) * (uint32_t)a.token_stride + chunk(r);
+          copy16_from<true, false>((int64_t)(uintptr_t)head + lane64(run, tile + i * RPI / 16 * 16), off, 0, dst + i * 1024);
         } else {
-          const int64_t b = (lane < 32 ? at[2 * i] : at[2 * i + 1]) + (int64_t)((r & 15) * (int)a.token_stride + cc * 16);
-          copy16<true>(head + b, dst + i * 1024);
+          const int64_t b0 = lane64(run, tile + 32 * i), b1 = lane64(run, tile + 32 * i + 16);
+          copy16<true>(head + (lane < 32 ? b0 : b1) + ((r & 15) * (int)a.token_stride + chunk(r)), dst + i * 1024);
+        }
+      }
+      const uint32_t woff = (uint32_t)(lane & 15) * (uint32_t)a.p_token_stride + (lane >> 4) * 4;
+      int64_t b[4];  // read from other lanes while all lanes are active
+#pragma unroll
+      for (int u = 0; u < 4; ++u) b[u] = (int64_t)(uintptr_t)words + lane64(wrun, tile + 16 * u);
+      if (GP >= 4 || lane < 16 * GP) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          copy4_from(b[u], woff, wdst + u * GP * 64);
+          if (GP > 4) copy4_from(b[u], woff + 16, wdst + u * GP * 64 + 256);
         }
       }
     } else {
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         const int r = i * RPI + r0;
-        const int cc = c ^ (IS_V ? swz4_v<D>(r) : swz4_k<D>(r));
         const int lo = __shfl((int)row, r), hi = __shfl((int)(row >> 32), r);
         const int64_t o = ((int64_t)hi << 32) | (uint32_t)lo;
-        copy16<true>((hi < 0 ? (const uint8_t*)kZeroRow : head + o) + cc * 16, dst + i * 1024);
+        copy16<true>((hi < 0 ? (const uint8_t*)kZeroRow : head + o) + chunk(r), dst + i * 1024);
+      }
+      const uint8_t* p[4];  // read from other lanes while all lanes are active
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int r = 16 * u + (lane & 15);
+        const int lo = __shfl((int)wrow, r), hi = __shfl((int)(wrow >> 32), r);
+        const int64_t o = ((int64_t)hi << 32) | (uint32_t)lo;
+        p[u] = (hi < 0 ? (const uint8_t*)kZeroRow : words + o) + (lane >> 4) * 4;
+      }
+      if (GP >= 4 || lane < 16 * GP) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          copy4(p[u], wdst + u * GP * 64);
+          if (GP > 4) copy4(p[u] + 16, wdst + u * GP * 64 + 256);
+        }
       }
     }
-    const uint8_t* pw = prow < 0 ? (const uint8_t*)kZeroRow : words + prow;
-#pragma unroll
-    for (int i = 0; i < GP; ++i) copy4(pw + 4 * i, wdst + i * 256);
   }
 };
 
-// Adds the values of the keys in `odd` (whose groups fp16 may not hold) to the columns whose weight is
-// not zero, and clears their words, so that the products take zeros there.
+// The codes of a word as fp16 subnormals, pairs (i, i + 4): c 2^-24 for even i, 16 c 2^-24 for odd i.
+__device__ __forceinline__ u32x4_t codes_as_fp16(uint32_t w) {
+  const uint32_t v = w >> 8;
+  return u32x4_t{w & 0x000f000fu, w & 0x00f000f0u, v & 0x000f000fu, v & 0x00f000f0u};
+}
+
+// Whether a group's scale or bias is infinite or NaN.
+__device__ __forceinline__ bool odd_word(uint32_t w) { return (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u; }
+
+// Adds the values of the groups that hold an infinity or a NaN, of the keys in `odd`, to the columns whose
+// weight is not zero, and clears their words, so that the products take zeros there.  w: the weights as they are
+// held, e[n][kt][i] of key 16 kt + 4 g + i.
 template <int D, int GROUP, int NC>
-__device__ __forceinline__ void few4_odd(const uint8_t* sv, uint8_t* swv, uint64_t odd, int lane,
-                                         const u32x4_t (*p)[2], f32x4_t (*o)[D / 16]) {
+__device__ __forceinline__ void few4_odd(const uint8_t* sv, uint8_t* swv, uint64_t odd, int lane, const float (*e)[4][4],
+                                         const int (*up)[D / GROUP], f32x4_t (*o)[D / 16]) {
   asm volatile("" : "+v"(lane));  // the addresses stay in this rare path
+  constexpr int GP = D / GROUP;
   const int g = lane >> 4, col = lane & 15;
 #pragma unroll 1
   while (odd) {
     const int j = __builtin_ctzll(odd);
     odd &= odd - 1;
-    // the weight of key j = 16 k + 4 q + i: lanes of q, half k & 1 of word i of product k >> 1
     float w[NC];
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
-      uint32_t x = 0;
+      float x = 0.f;
 #pragma unroll
-      for (int y = 0; y < 8; ++y) x = y == 4 * (j >> 5) + (j & 3) ? p[n][y >> 2][y & 3] : x;
-      x = __shfl(x, 16 * ((j >> 2) & 3) + col);
-      w[n] = param_to_f32<F16>((j >> 4) & 1 ? x >> 16 : x & 0xffffu);
+      for (int y = 0; y < 16; ++y) x = y == 4 * (j >> 4) + (j & 3) ? e[n][y >> 2][y & 3] : x;
+      w[n] = __shfl(x, 16 * ((j >> 2) & 3) + col);
     }
+    uint8_t* words = swv + (j >> 4) * GP * 64 + (j & 15) * 4;
 #pragma unroll 1
     for (int dt = 0; dt < D / 16; ++dt) {
-      const f16x2_t gr = h2(*(const uint32_t*)(swv + (16 * dt / GROUP) * 256 + 4 * j));
+      const uint32_t word = *(const uint32_t*)(words + (16 * dt / GROUP) * 64);
+      if (!odd_word(word)) continue;
+      const f16x2_t gr = h2(word);
       const uint32_t c = *(const uint16_t*)(sv + j * (D / 2) + (((dt >> 1) ^ swz4_v<D>(j)) * 16) + 8 * (dt & 1) + 2 * g);
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const _Float16 v = __builtin_fmaf16((_Float16)(float)((c >> (4 * r)) & 15), gr[0], gr[1]);
+        const float v = __builtin_fmaf((float)((c >> (4 * r)) & 15), (float)gr[0], (float)gr[1]);
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
-          const float add = w[n] != 0.f ? w[n] * (float)v : 0.f;
+          int u = up[n][0];
+#pragma unroll
+          for (int x = 1; x < D / GROUP; ++x) u = 16 * dt / GROUP == x ? up[n][x] : u;
+          const float add = w[n] != 0.f ? __builtin_ldexpf(w[n] * v, 7 - u - 24) : 0.f;
 #pragma unroll
           for (int d = 0; d < D / 16; ++d) o[n][d][r] += d == dt ? add : 0.f;
         }
       }
     }
-    if (lane < D / GROUP) *(uint32_t*)(swv + lane * 256 + 4 * j) = 0;
+    if (lane < GP && odd_word(*(uint32_t*)(words + lane * 64))) *(uint32_t*)(words + lane * 64) = 0;
   }
 }
 
@@ -161,28 +236,31 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few4_kernel(const 
   constexpr int ROW = D / 2;            // bytes of a row's codes
   constexpr int TILE = 64 * ROW;        // of a wave's tile
   constexpr int GP = Copy::GP, WORDS = GP * 256;
-  constexpr int WAVE = 2 * (TILE + WORDS);
-  constexpr int NS = D / 32;            // k-steps of the scores
+  constexpr int WAVE = 2 * TILE + 3 * WORDS;
+  constexpr int WPL = GROUP / 32;       // words of a group that a lane holds of a key's row
   constexpr int ND = D / 16;            // output tiles
-  constexpr int NP = D == 256 ? 2 : 1;  // groups that a lane's part of a key's row may lie in
+  // The queries' operands lie in LDS where the registers are full: a spilled register's reload waits for the
+  // copies in flight.
+  constexpr bool kSumInRow = GP * NC <= 4;
+  constexpr bool kQInLds = D == 256 || (D == 128 && (NC == 2 || GROUP == 32));
   static_assert(WAVE >= 16 * D * 4, "the joining of the waves takes the tiles' place");
   __shared__ __attribute__((aligned(1024))) uint8_t sm[4 * WAVE];
+  __shared__ u32x4_t sq[kQInLds ? NC * GP * WPL * 64 : 1];
   __shared__ float sml[4][16 * NC][2];
   __shared__ int ssh[8];
   __shared__ int sfound[4];
-  const int tid = threadIdx.x, lane = tid & 63;
+  const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int g = lane >> 4, col = lane & 15;
 
   FewRun run;
-  if (!few_run<256>(a, ssh, sfound, run)) return;
+  if (!few_run<256, QL_IU, QL_TH>(a, ssh, sfound, run)) return;
   const int u1 = run.u1, item_units = run.item_units;
   int s = run.s, base = run.base;
 
   uint8_t* sk = sm + wave * WAVE;
   uint8_t* sv = sk + TILE;
-  uint8_t* swk = sv + TILE;
-  uint8_t* swv = swk + WORDS;
+  uint8_t* swv = sv + TILE;
+  uint8_t* swk = swv + WORDS;  // two of them: of this tile and the next
   Copy tc;
   bool recorded = false;
   for (int u = run.u0; u < u1;) {
@@ -202,6 +280,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few4_kernel(const 
     u = item0 + nt;
     if (tb <= ta) continue;  // the run ends before the item's first tile
     const int rows = q.nq * a.g;
+    int lane = tid & 63;  // places are worked out in each item, not kept in registers
+    asm volatile("" : "+v"(lane));
 
     const uint8_t* kb = a.k + (int64_t)head * a.head_stride;
     const uint8_t* vb = a.v + (int64_t)head * a.head_stride;
@@ -215,11 +295,13 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few4_kernel(const 
     tc.template copy<true>(a, vb, vw, sv, swv, lane);
     uint64_t seen = tc.seen;
 
+    const int g = lane >> 4, col = lane & 15;
     // The wave's queries: column c of tile n is row 16 n + c; a lane holds the values that meet its part
-    // of the keys' rows, word by word.
-    u32x4_t qf[NC][NS];
+    // of the keys' rows, word by word, and the sums of each group's values.
+    u32x4_t qf[NC][GP * WPL];
+    float qs[NC][GP];
     int qpos[NC];
-    float sl[NC];  // scale * log2(e) * 2^t
+    float sl[NC];  // scale * log2(e) * 2^(t + 24)
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
       const int r = 16 * n + col;
@@ -229,73 +311,121 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few4_kernel(const 
       const uint8_t* qp = a.q + ((int64_t)(q.q0 + (in ? i : 0)) * a.q_ts + (int64_t)(head * a.g + (in ? r - i * a.g : 0)) * a.q_hs);
       float amax = 0.f;
 #pragma unroll
-      for (int st = 0; st < NS; ++st) {
+      for (int x = 0; x < GP * WPL; ++x) {
         const u32x4_t z = {0, 0, 0, 0};
-        const int word = D == 64 ? 2 * g + st : 16 * (st / 4) + 4 * g + st % 4;
-        qf[n][st] = in ? *(const u32x4_t*)(qp + word * 16) : z;
-        amax = amax8(qf[n][st], amax);
+        const int word = (x / WPL) * (GROUP / 8) + g * WPL + x % WPL;
+        qf[n][x] = in ? *(const u32x4_t*)(qp + word * 16) : z;
+        amax = amax8(qf[n][x], amax);
       }
       const int t = a.io == DT_BF16 ? q_exponent(join32(join16(amax, MaxF()), MaxF())) : 0;
       const float factor = __builtin_ldexpf(1.f, -t);
-      sl[n] = __builtin_ldexpf(a.sl, t);
+      sl[n] = __builtin_ldexpf(a.sl, t + 24);
 #pragma unroll
-      for (int st = 0; st < NS; ++st) qf[n][st] = q_pairs(qf[n][st], a.io, factor);
+      for (int x = 0; x < GP * WPL; ++x) {
+        u32x4_t w = q_pairs(qf[n][x], a.io, factor);
+        float sum = x % WPL == 0 ? 0.f : qs[n][x / WPL];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) sum = add2(F16{}, w[y], sum);
+        qs[n][x / WPL] = sum;
+        const f16x2_t sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
+        w[1] = w2(h2(w[1]) * sixteenth), w[3] = w2(h2(w[3]) * sixteenth);
+        if constexpr (kQInLds)
+          sq[(n * GP * WPL + x) * 64 + lane] = w;  // each wave the same
+        else
+          qf[n][x] = w;
+      }
+#pragma unroll
+      for (int x = 0; x < GP; ++x) qs[n][x] = join32(join16(qs[n][x], SumF()), SumF()) * 0x1p-24f;
     }
     const int pos_lo = q.kv - q.nq, pos_hi = q.kv - 1;  // first and last query's position
 
-    f32x4_t o[NC][ND];
-    float m[NC], l[NC];
+    f32x4_t o[NC][ND], ps[NC][GP];  // ps: the sums of the groups' products, one value in the lane's registers or four alike
+    float m[NC], l[NC], bs[NC][GP];
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
       m[n] = kNegInf;
       l[n] = 0.f;
 #pragma unroll
       for (int d = 0; d < ND; ++d) o[n][d] = f32x4_t{0, 0, 0, 0};
+#pragma unroll
+      for (int x = 0; x < GP; ++x) bs[n][x] = 0.f, ps[n][x] = f32x4_t{0, 0, 0, 0};
     }
+    int up[NC][GP];
+#pragma unroll
+    for (int n = 0; n < NC; ++n)
+#pragma unroll
+      for (int x = 0; x < GP; ++x) up[n][x] = -14;
     if (ta + 1 < tb) tc.lookup(a, table, k00 + 256, lo, hi, lane, false);
 
     for (int t = ta; t < tb; ++t) {
+      int ln = lane;  // LDS places are worked out in each tile, not kept in registers
+      asm volatile("" : "+v"(ln));
+      const int g = ln >> 4, col = ln & 15;
       const int k0 = (first + t) * 256 + wave * 64;
       const bool more = t + 1 < tb;
       attn_wait_vm<Copy::COPIES>();  // K of this tile
-      uint32_t kf[4][NS];
-      uint32_t kg[4][NP];
+      uint32_t kf[4][GP * WPL];
 #pragma unroll
       for (int kt = 0; kt < 4; ++kt) {
         const int row = 16 * kt + col;
-        if constexpr (D == 64) {
-          const u32x2_t w = *(const u32x2_t*)(sk + row * ROW + g * 8);
-          kf[kt][0] = w[0], kf[kt][1] = w[1];
-          kg[kt][0] = *(const uint32_t*)(swk + (16 * g / GROUP) * 256 + row * 4);
-        } else {
 #pragma unroll
-          for (int c = 0; c < NP; ++c) {
-            const u32x4_t w = *(const u32x4_t*)(sk + row * ROW + ((4 * c + g) ^ swz4_k<D>(row)) * 16);
-            for (int x = 0; x < 4; ++x) kf[kt][4 * c + x] = w[x];
-            kg[kt][c] = *(const uint32_t*)(swk + ((128 * c + 32 * g) / GROUP) * 256 + row * 4);
+        for (int x = 0; x < GP; ++x) {
+          const int byte = x * (GROUP / 2) + g * WPL * 4;
+          const uint8_t* at = sk + row * ROW + ((byte >> 4) ^ swz4_k<D>(row)) * 16 + (byte & 15);
+          if constexpr (WPL == 4) {
+            const u32x4_t w = *(const u32x4_t*)at;
+            for (int y = 0; y < 4; ++y) kf[kt][4 * x + y] = w[y];
+          } else if constexpr (WPL == 2) {
+            const u32x2_t w = *(const u32x2_t*)at;
+            kf[kt][2 * x] = w[0], kf[kt][2 * x + 1] = w[1];
+          } else {
+            kf[kt][x] = *(const uint32_t*)at;
           }
         }
       }
       const uint64_t seen_now = seen;
+      const uint8_t* kwords = swk + ((t - ta) & 1) * WORDS;
       if (more) {
-        tc.resolve(a, lo, hi, lane);
+        tc.resolve(a, lo, hi, ln);
         seen = tc.seen;
         attn_wait_lds();
-        tc.template copy<false>(a, kb, kw, sk, swk, lane);
+        tc.template copy<false>(a, kb, kw, sk, swk + ((t - ta + 1) & 1) * WORDS, ln);
       }
+      auto query = [&](int n, int x) {
+        if constexpr (kQInLds)
+          return sq[(n * GP * WPL + x) * 64 + ln];
+        else
+          return qf[n][x];
+      };
       f32x4_t sc[NC][4];
 #pragma unroll
-      for (int n = 0; n < NC; ++n)
+      for (int kt = 0; kt < 4; ++kt) {
+        u32x4_t w[GP];
 #pragma unroll
-        for (int kt = 0; kt < 4; ++kt) sc[n][kt] = f32x4_t{0, 0, 0, 0};
+        for (int x = 0; x < GP; ++x) w[x] = *(const u32x4_t*)(kwords + (kt * GP + x) * 64 + g * 16);
+        f32x4_t acc[NC][GP];
 #pragma unroll
-      for (int kt = 0; kt < 4; ++kt)
+        for (int x = 0; x < GP; ++x)
 #pragma unroll
-        for (int st = 0; st < NS; ++st) {
-          const u32x4_t kv = values4(kf[kt][st], kg[kt][st / 4]);
+          for (int y = 0; y < WPL; ++y) {
+            const u32x4_t c = codes_as_fp16(kf[kt][x * WPL + y]);
 #pragma unroll
-          for (int n = 0; n < NC; ++n) sc[n][kt] = mfma16(F16{}, kv, qf[n][st], sc[n][kt]);
-        }
+            for (int n = 0; n < NC; ++n)
+              acc[n][x] = mfma16(F16{}, c, query(n, x * WPL + y), y == 0 ? f32x4_t{0, 0, 0, 0} : acc[n][x]);
+          }
+#pragma unroll
+        for (int x = 0; x < GP; ++x)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float ks = (float)h2(w[x][r])[0], kbias = (float)h2(w[x][r])[1];
+#pragma unroll
+            for (int n = 0; n < NC; ++n) {
+              const float y = x == 0 ? kbias * qs[n][x] : __builtin_fmaf(kbias, qs[n][x], sc[n][kt][r]);
+              sc[n][kt][r] = __builtin_fmaf(ks, acc[n][x][r], y);
+            }
+          }
+        __builtin_amdgcn_sched_barrier(0);  // one key tile at a time: its words and sums fit in the registers
+      }
       // masks: rows that are not loaded, keys past a column's query, keys before its window
       const bool cut = k0 + 63 > pos_lo || (a.window > 0 && k0 <= pos_hi - a.window);
       if (cut || seen_now != ~0ull) {
@@ -311,80 +441,162 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few4_kernel(const 
           }
         }
       }
-      u32x4_t p[NC][2];
+      if (more)
+        attn_wait_vm<Copy::COPIES>();  // V of this tile; the next K may be in flight
+      else
+        attn_wait_vm<0>();
+      // the exponents of the groups' largest scales so far: a group's products are held times 2^(7 - up)
+      int up_now[NC][GP];
+      if (cut && q.nq > 1) {  // of the keys that the column sees
+#pragma unroll
+        for (int x = 0; x < GP; ++x) {
+          uint32_t big[NC];
+#pragma unroll
+          for (int n = 0; n < NC; ++n) big[n] = 0x400u;
+#pragma unroll
+          for (int kt = 0; kt < 4; ++kt) {
+            const u32x4_t w = *(const u32x4_t*)(swv + (kt * GP + x) * 64 + g * 16);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+              for (int n = 0; n < NC; ++n)
+                if (sc[n][kt][r] != kNegInf && !odd_word(w[r])) big[n] = max(big[n], w[r] & 0x7fffu);
+          }
+#pragma unroll
+          for (int n = 0; n < NC; ++n) {
+            const float all = join32(join16(__uint_as_float(big[n]), MaxF()), MaxF());  // ordered as their bits
+            up_now[n][x] = max(up[n][x], (int)(__float_as_uint(all) >> 10) - 14);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int x = 0; x < GP; ++x) {
+          const uint32_t w = *(const uint32_t*)(swv + (g * GP + x) * 64 + col * 4);
+          const int all = (int)(wave_max(odd_word(w) ? 0x400u : max(0x400u, w & 0x7fffu)) >> 10) - 14;
+#pragma unroll
+          for (int n = 0; n < NC; ++n) up_now[n][x] = max(up[n][x], all);
+        }
+      }
+      float e[NC][4][4];
 #pragma unroll
       for (int n = 0; n < NC; ++n) {
         float mx = fmaxf(fmaxf(sc[n][0][0], sc[n][1][0]), fmaxf(sc[n][2][0], sc[n][3][0]));
 #pragma unroll
         for (int r = 1; r < 4; ++r) mx = max3(max3(mx, sc[n][0][r], sc[n][1][r]), sc[n][2][r], sc[n][3][r]);
         mx = join32(join16(mx, MaxF()), MaxF()) * sl[n];
-        if (__any(mx > m[n] + kLazy)) {
-          const float mn = fmaxf(m[n], mx);
+        bool raise = mx > m[n] + kLazy;
+#pragma unroll
+        for (int x = 0; x < GP; ++x) raise |= up_now[n][x] > up[n][x];
+        if (__any(raise)) {
+          const float mn = mx > m[n] + kLazy ? mx : m[n];
           const float f = m[n] == kNegInf ? 0.f : exp2_fast(m[n] - mn);
           m[n] = mn;
           l[n] *= f;
 #pragma unroll
-          for (int d = 0; d < ND; ++d)
-            for (int r = 0; r < 4; ++r) o[n][d][r] *= f;
+          for (int x = 0; x < GP; ++x) {
+            const float fx = __builtin_ldexpf(f, up[n][x] - up_now[n][x]);
+            up[n][x] = up_now[n][x];
+            bs[n][x] *= f;
+            for (int r = 0; r < (kSumInRow ? 4 : 1); ++r) ps[n][x][r] *= fx;
+#pragma unroll
+            for (int d = x * (GROUP / 16); d < (x + 1) * (GROUP / 16); ++d)
+              for (int r = 0; r < 4; ++r) o[n][d][r] *= fx;
+          }
         }
         const float mr = m[n] == kNegInf ? 0.f : m[n];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int kt = 0; kt < 4; ++kt) {
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            p[n][h][r] = pack2(F16{}, exp2_fast(__builtin_fmaf(sc[n][2 * h][r], sl[n], -mr)),
-                               exp2_fast(__builtin_fmaf(sc[n][2 * h + 1][r], sl[n], -mr)));
-            l[n] = add2(F16{}, p[n][h][r], l[n]);
-          }
+          for (int r = 0; r < 4; ++r) e[n][kt][r] = exp2_fast(__builtin_fmaf(sc[n][kt][r], sl[n], -mr));
+          l[n] += (e[n][kt][0] + e[n][kt][1]) + (e[n][kt][2] + e[n][kt][3]);
+        }
       }
-      if (more)
-        attn_wait_vm<Copy::COPIES>();  // V of this tile; the next K may be in flight
-      else
-        attn_wait_vm<0>();
       // a key that only some columns see may stand for an infinity or a NaN
       if (cut && q.nq > 1) {
         bool mine = false;
 #pragma unroll
-        for (int i = 0; i < GP; ++i) mine |= odd_group(*(const uint32_t*)(swv + i * 256 + lane * 4));
-        const uint64_t odd = __ballot(mine);
-        if (odd) few4_odd<D, GROUP, NC>(sv, swv, odd, lane, p, o);
+        for (int x = 0; x < GP; ++x) {
+          mine |= odd_word(*(const uint32_t*)(swv + (g * GP + x) * 64 + col * 4));
+        }
+        const uint64_t keys = __ballot(mine);
+        if (keys) few4_odd<D, GROUP, NC>(sv, swv, keys, ln, e, up, o);
       }
       const int vrow = 16 * (col >> 2) + 4 * g + (col & 3);
 #pragma unroll
-      for (int gr = 0; gr < GP; ++gr) {
-        // scales and biases of the lane's keys 16 k + 4 g + i, as pairs k = (0, 1) and (2, 3)
-        f16x2_t vs[2][4], vbias[2][4];
+      for (int x = 0; x < GP; ++x) {
+        // the weights times the keys' scales, pairs of keys 16 k + 4 g + i with k = (0, 1) and (2, 3); and
+        // times the values of code 8
+        u32x4_t p[NC][2];
+        u32x4_t w[4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const u32x4_t x = *(const u32x4_t*)(swv + gr * 256 + (32 * h + 4 * g) * 4);
-          const u32x4_t y = *(const u32x4_t*)(swv + gr * 256 + (32 * h + 16 + 4 * g) * 4);
+        for (int kt = 0; kt < 4; ++kt) w[kt] = *(const u32x4_t*)(swv + (kt * GP + x) * 64 + g * 16);
+        float even[NC], odd[NC];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            vs[h][i] = h2(perm(y[i], x[i], 0x05040100u));
-            vbias[h][i] = h2(perm(y[i], x[i], 0x07060302u));
-          }
-        }
+        for (int n = 0; n < NC; ++n) even[n] = __builtin_ldexpf(1.f, 7 - up[n][x]), odd[n] = 0.0625f * even[n];
 #pragma unroll
-        for (int dd = 0; dd < GROUP / 16; ++dd) {
-          const int d = gr * (GROUP / 16) + dd;
-          const u32x2_t w = read_tr4(sv + vrow * ROW + (((d >> 1) ^ swz4_v<D>(vrow)) * 16) + 8 * (d & 1));
+        for (int r = 0; r < 4; ++r)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const u32x4_t v = values4(w[h], vs[h], vbias[h]);
+            const f16x2_t w0 = h2(w[2 * h][r]), w1 = h2(w[2 * h + 1][r]);
+            const float m0 = __builtin_fmaf(8.f, (float)w0[0], (float)w0[1]), m1 = __builtin_fmaf(8.f, (float)w1[0], (float)w1[1]);
+#pragma unroll
+            for (int n = 0; n < NC; ++n) {
+              const float e0 = e[n][2 * h][r], e1 = e[n][2 * h + 1][r], up1 = r & 1 ? odd[n] : even[n];
+              p[n][h][r] = pack2(F16{}, (e0 * up1) * (float)w0[0], (e1 * up1) * (float)w1[0]);
+              bs[n][x] = __builtin_fmaf(e0, m0, bs[n][x]);
+              bs[n][x] = __builtin_fmaf(e1, m1, bs[n][x]);
+            }
+          }
+        // the sums of those products: times 2^-24 by a row of ones, or in one register each
+#pragma unroll
+        for (int n = 0; n < NC; ++n)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if constexpr (kSumInRow) {
+              ps[n][x] = mfma16(F16{}, u32x4_t{0x00010001u, 0x00100010u, 0x00010001u, 0x00100010u}, p[n][h], ps[n][x]);
+            } else {
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                ps[n][x][0] = dot2(F16{}, p[n][h][r], r & 1 ? 0x4c004c00u : 0x3c003c00u, ps[n][x][0]);  // 16 or 1
+            }
+          }
+#pragma unroll
+        for (int dd = 0; dd < GROUP / 16; ++dd) {
+          const int d = x * (GROUP / 16) + dd;
+          const u32x2_t c = read_tr4(sv + vrow * ROW + (((d >> 1) ^ swz4_v<D>(vrow)) * 16) + 8 * (d & 1));
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const u32x4_t v = codes_as_fp16(c[h]);
 #pragma unroll
             for (int n = 0; n < NC; ++n) o[n][d] = mfma16(F16{}, v, p[n][h], o[n][d]);
           }
         }
+        __builtin_amdgcn_sched_barrier(0);
       }
       if (more) {
         attn_wait_lds();
-        tc.template copy<true>(a, vb, vw, sv, swv, lane);
-        if (t + 2 < tb) tc.lookup(a, table, k0 + 512, lo, hi, lane, false);
+        tc.template copy<true>(a, vb, vw, sv, swv, ln);
+        if (t + 2 < tb) tc.lookup(a, table, k0 + 512, lo, hi, ln, false);
       }
     }
 
+    // to the units of the sums: the factors of the weights and of the codes, and the groups' middles
+#pragma unroll
+    for (int n = 0; n < NC; ++n)
+#pragma unroll
+      for (int x = 0; x < GP; ++x) {
+        const float held = __builtin_ldexpf(1.f, up[n][x] + 24 - 7);
+        float sum = ps[n][x][0];
+        if (!kSumInRow) sum = join32(join16(sum, SumF()), SumF()) * 0x1p-24f;
+        const float b = join32(join16(bs[n][x], SumF()), SumF()) - 8.f * (sum * held);
+#pragma unroll
+        for (int d = x * (GROUP / 16); d < (x + 1) * (GROUP / 16); ++d)
+          for (int r = 0; r < 4; ++r) o[n][d][r] = __builtin_fmaf(o[n][d][r], held, b);
+      }
     const bool whole = ta == 0 && tb == nt;
-    few_finish<D, NC>(a, sm, WAVE, sml, o, m, l, run.w, q, head, rows, ta == 0, whole,
+    int end_tid = tid;  // its places are worked out here, not kept in registers over the tiles
+    asm volatile("" : "+v"(end_tid));
+    few_finish<D, NC>(a, end_tid, sm, WAVE, sml, o, m, l, run.w, q, head, rows, ta == 0, whole,
                       [io = a.io](void* p, float x, float y, float z, float w) {
                         if (io == DT_BF16)
                           store4(BF16{}, p, x, y, z, w);
