@@ -11,27 +11,33 @@
 
 namespace ql {
 
-// The exponent t for which a row of largest magnitude amax (of bf16 values) has amax 2^-t in [2^14, 2^15).
+// The exponent t for which a row of largest magnitude amax has amax 2^-t in [2^14, 2^15).
 __device__ __forceinline__ int q_exponent(float amax) {
-  const int e = (int)(__float_as_uint(amax) >> 23) - 127 - 14;
-  return amax == 0.f ? 0 : min(100, max(-100, e));
+  return amax == 0.f ? 0 : (int)(__float_as_uint(amax) >> 23) - 127 - 14;
 }
-// Eight bf16 or fp16 values as fp16 pairs (i, i + 4), the order in which a word's codes are decoded;
-// bf16 values times 2^-t.
-__device__ __forceinline__ u32x4_t q_pairs(u32x4_t w, int dt, float factor) {
-  uint32_t lo[4] = {w[0] & 0xffffu, w[0] >> 16, w[1] & 0xffffu, w[1] >> 16};
-  uint32_t hi[4] = {w[2] & 0xffffu, w[2] >> 16, w[3] & 0xffffu, w[3] >> 16};
+__device__ __forceinline__ void q_values(u32x4_t w, int dt, float* f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = dt == DT_BF16 ? bf16_bits_to_f32(w[i] & 0xffffu) : f16_bits_to_f32(w[i] & 0xffffu);
+    f[2 * i + 1] = dt == DT_BF16 ? bf16_bits_to_f32(w[i] >> 16) : f16_bits_to_f32(w[i] >> 16);
+  }
+}
+// Its scores' factor 2^t, cut where it passes fp32 (the scores then differ by more than weights can show).
+__device__ __forceinline__ float q_scale(float sl, int t) { return fminf(__builtin_ldexpf(sl, t), 3.0e38f); }
+// Eight bf16 or fp16 values times 2^-t as fp16 pairs (i, i + 4), the order in which a word's codes come apart.
+__device__ __forceinline__ u32x4_t q_pairs(u32x4_t w, int dt, int t) {
+  float f[8];
+  q_values(w, dt, f);
   u32x4_t r;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    r[i] = dt == DT_BF16 ? pack2(F16{}, bf16_bits_to_f32(lo[i]) * factor, bf16_bits_to_f32(hi[i]) * factor)
-                         : lo[i] | (hi[i] << 16);
+  for (int i = 0; i < 4; ++i) r[i] = pack2(F16{}, __builtin_ldexpf(f[i], -t), __builtin_ldexpf(f[i + 4], -t));
   return r;
 }
-__device__ __forceinline__ float amax8(u32x4_t w, float m) {
+__device__ __forceinline__ float amax8(u32x4_t w, int dt, float m) {
+  float f[8];
+  q_values(w, dt, f);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    m = fmaxf(m, fmaxf(__builtin_fabsf(__uint_as_float(w[i] << 16)), __builtin_fabsf(__uint_as_float(w[i] & 0xffff0000u))));
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, __builtin_fabsf(f[i]));
   return m;
 }
 

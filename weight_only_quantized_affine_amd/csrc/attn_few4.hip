@@ -18,7 +18,7 @@
 #include "attn_few.hpp"
 
 #ifndef QL_IU
-#define QL_IU 3
+#define QL_IU 2
 #define QL_TH 4
 #endif
 namespace ql {
@@ -236,12 +236,12 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few4_kernel(const 
   constexpr int ROW = D / 2;            // bytes of a row's codes
   constexpr int TILE = 64 * ROW;        // of a wave's tile
   constexpr int GP = Copy::GP, WORDS = GP * 256;
-  constexpr int WAVE = 2 * TILE + 3 * WORDS;
+  constexpr int WAVE = 3 * TILE + 4 * WORDS;  // K, V of two tiles, words of two tiles each
   constexpr int WPL = GROUP / 32;       // words of a group that a lane holds of a key's row
   constexpr int ND = D / 16;            // output tiles
   // The queries' operands lie in LDS where the registers are full: a spilled register's reload waits for the
   // copies in flight.
-  constexpr bool kSumInRow = GP * NC <= 4;
+  constexpr bool kSumInRow = GP * NC <= 2;
   constexpr bool kQInLds = D == 256 || (D == 128 && (NC == 2 || GROUP == 32));
   static_assert(WAVE >= 16 * D * 4, "the joining of the waves takes the tiles' place");
   __shared__ __attribute__((aligned(1024))) uint8_t sm[4 * WAVE];
@@ -258,9 +258,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few4_kernel(const 
   int s = run.s, base = run.base;
 
   uint8_t* sk = sm + wave * WAVE;
-  uint8_t* sv = sk + TILE;
-  uint8_t* swv = sv + TILE;
-  uint8_t* swk = swv + WORDS;  // two of them: of this tile and the next
+  uint8_t* svs = sk + TILE;
+  uint8_t* swvs = svs + 2 * TILE;
+  uint8_t* swks = swvs + 2 * WORDS;
   Copy tc;
   bool recorded = false;
   for (int u = run.u0; u < u1;) {
@@ -291,15 +291,16 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few4_kernel(const 
     const int k00 = (first + ta) * 256 + wave * 64;
     tc.lookup(a, table, k00, lo, hi, lane, true);
     tc.resolve(a, lo, hi, lane);
-    tc.template copy<false>(a, kb, kw, sk, swk, lane);
-    tc.template copy<true>(a, vb, vw, sv, swv, lane);
+    tc.template copy<false>(a, kb, kw, sk, swks, lane);
+    tc.template copy<true>(a, vb, vw, svs, swvs, lane);
     uint64_t seen = tc.seen;
 
     const int g = lane >> 4, col = lane & 15;
     // The wave's queries: column c of tile n is row 16 n + c; a lane holds the values that meet its part
-    // of the keys' rows, word by word, and the sums of each group's values.
+    // of the keys' rows, word by word; and, for the keys' biases, the sums of each group's values as two fp16
+    // numbers a group (four groups a lane; every lane group takes part, with its share of the sum).
     u32x4_t qf[NC][GP * WPL];
-    float qs[NC][GP];
+    u32x4_t qb[NC];
     int qpos[NC];
     float sl[NC];  // scale * log2(e) * 2^(t + 24)
 #pragma unroll
@@ -315,18 +316,18 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few4_kernel(const 
         const u32x4_t z = {0, 0, 0, 0};
         const int word = (x / WPL) * (GROUP / 8) + g * WPL + x % WPL;
         qf[n][x] = in ? *(const u32x4_t*)(qp + word * 16) : z;
-        amax = amax8(qf[n][x], amax);
+        amax = amax8(qf[n][x], a.io, amax);
       }
-      const int t = a.io == DT_BF16 ? q_exponent(join32(join16(amax, MaxF()), MaxF())) : 0;
-      const float factor = __builtin_ldexpf(1.f, -t);
-      sl[n] = __builtin_ldexpf(a.sl, t + 24);
+      const int t = q_exponent(join32(join16(amax, MaxF()), MaxF()));
+      sl[n] = q_scale(a.sl, t + 24);
+      float qs[GP];
 #pragma unroll
       for (int x = 0; x < GP * WPL; ++x) {
-        u32x4_t w = q_pairs(qf[n][x], a.io, factor);
-        float sum = x % WPL == 0 ? 0.f : qs[n][x / WPL];
+        u32x4_t w = q_pairs(qf[n][x], a.io, t);
+        float sum = x % WPL == 0 ? 0.f : qs[x / WPL];
 #pragma unroll
         for (int y = 0; y < 4; ++y) sum = add2(F16{}, w[y], sum);
-        qs[n][x / WPL] = sum;
+        qs[x / WPL] = sum;
         const f16x2_t sixteenth = {(_Float16)0.0625f, (_Float16)0.0625f};
         w[1] = w2(h2(w[1]) * sixteenth), w[3] = w2(h2(w[3]) * sixteenth);
         if constexpr (kQInLds)
@@ -335,12 +336,19 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few4_kernel(const 
           qf[n][x] = w;
       }
 #pragma unroll
-      for (int x = 0; x < GP; ++x) qs[n][x] = join32(join16(qs[n][x], SumF()), SumF()) * 0x1p-24f;
+      for (int x = 0; x < GP; ++x) qs[x] = join32(join16(qs[x], SumF()), SumF()) * (GP == 8 ? 0x1p-25f : 0x1p-26f);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        float v = x < GP ? qs[x % GP] : 0.f;
+        if (GP == 8 && (g & 1)) v = qs[(x + 4) % GP];
+        const float hi = f16_bits_to_f32(f32_to_f16_bits(v));
+        qb[n][x] = pack2(F16{}, hi, v - hi);
+      }
     }
     const int pos_lo = q.kv - q.nq, pos_hi = q.kv - 1;  // first and last query's position
 
-    f32x4_t o[NC][ND], ps[NC][GP];  // ps: the sums of the groups' products, one value in the lane's registers or four alike
-    float m[NC], l[NC], bs[NC][GP];
+    f32x4_t o[NC][ND], bs[NC][GP], ps[NC][GP];
+    float m[NC], l[NC];
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
       m[n] = kNegInf;
@@ -348,13 +356,16 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few4_kernel(const 
 #pragma unroll
       for (int d = 0; d < ND; ++d) o[n][d] = f32x4_t{0, 0, 0, 0};
 #pragma unroll
-      for (int x = 0; x < GP; ++x) bs[n][x] = 0.f, ps[n][x] = f32x4_t{0, 0, 0, 0};
+      for (int x = 0; x < GP; ++x) bs[n][x] = ps[n][x] = f32x4_t{0, 0, 0, 0};
     }
     int up[NC][GP];
 #pragma unroll
     for (int n = 0; n < NC; ++n)
 #pragma unroll
       for (int x = 0; x < GP; ++x) up[n][x] = -14;
+    uint32_t top[GP];  // uniform: every column's exponents cover scales (fp16 bits) below it
+#pragma unroll
+    for (int x = 0; x < GP; ++x) top[x] = 0x400u;
     if (ta + 1 < tb) tc.lookup(a, table, k00 + 256, lo, hi, lane, false);
 
     for (int t = ta; t < tb; ++t) {
@@ -363,6 +374,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few4_kernel(const 
       const int g = ln >> 4, col = ln & 15;
       const int k0 = (first + t) * 256 + wave * 64;
       const bool more = t + 1 < tb;
+      const int now = (t - ta) & 1, next = now ^ 1;
+      uint8_t* sv = svs + now * TILE;
+      uint8_t* swv = swvs + now * WORDS;
       attn_wait_vm<Copy::COPIES>();  // K of this tile
       uint32_t kf[4][GP * WPL];
 #pragma unroll
@@ -384,12 +398,14 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few4_kernel(const 
         }
       }
       const uint64_t seen_now = seen;
-      const uint8_t* kwords = swk + ((t - ta) & 1) * WORDS;
+      const uint8_t* kwords = swks + now * WORDS;
       if (more) {
         tc.resolve(a, lo, hi, ln);
         seen = tc.seen;
         attn_wait_lds();
-        tc.template copy<false>(a, kb, kw, sk, swk + ((t - ta + 1) & 1) * WORDS, ln);
+        tc.template copy<false>(a, kb, kw, sk, swks + next * WORDS, ln);
+        tc.template copy<true>(a, vb, vw, svs + next * TILE, swvs + next * WORDS, ln);
+        if (t + 2 < tb) tc.lookup(a, table, k0 + 512, lo, hi, ln, false);
       }
       auto query = [&](int n, int x) {
         if constexpr (kQInLds)
@@ -403,7 +419,15 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few4_kernel(const 
         u32x4_t w[GP];
 #pragma unroll
         for (int x = 0; x < GP; ++x) w[x] = *(const u32x4_t*)(kwords + (kt * GP + x) * 64 + g * 16);
+        u32x4_t kb2 = {0, 0, 0, 0};  // the biases of the lane's key, twice each
+#pragma unroll
+        for (int x = 0; x < (GP < 4 ? GP : 4); ++x) {
+          const uint32_t b = *(const uint32_t*)(kwords + (kt * GP + x + (GP == 8 ? 4 * (g & 1) : 0)) * 64 + col * 4);
+          kb2[x] = perm(b, b, 0x07060706u);
+        }
         f32x4_t acc[NC][GP];
+#pragma unroll
+        for (int n = 0; n < NC; ++n) sc[n][kt] = mfma16(F16{}, kb2, qb[n], f32x4_t{0, 0, 0, 0});
 #pragma unroll
         for (int x = 0; x < GP; ++x)
 #pragma unroll
@@ -417,12 +441,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few4_kernel(const 
         for (int x = 0; x < GP; ++x)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const float ks = (float)h2(w[x][r])[0], kbias = (float)h2(w[x][r])[1];
+            const float ks = (float)h2(w[x][r])[0];
 #pragma unroll
-            for (int n = 0; n < NC; ++n) {
-              const float y = x == 0 ? kbias * qs[n][x] : __builtin_fmaf(kbias, qs[n][x], sc[n][kt][r]);
-              sc[n][kt][r] = __builtin_fmaf(ks, acc[n][x][r], y);
-            }
+            for (int n = 0; n < NC; ++n) sc[n][kt][r] = __builtin_fmaf(ks, acc[n][x][r], sc[n][kt][r]);
           }
         __builtin_amdgcn_sched_barrier(0);  // one key tile at a time: its words and sums fit in the registers
       }
@@ -442,7 +463,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few4_kernel(const 
         }
       }
       if (more)
-        attn_wait_vm<Copy::COPIES>();  // V of this tile; the next K may be in flight
+        attn_wait_vm<2 * Copy::COPIES>();  // V of this tile; the next K and V may be in flight
       else
         attn_wait_vm<0>();
       // the exponents of the groups' largest scales so far: a group's products are held times 2^(7 - up)
@@ -469,15 +490,27 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few4_kernel(const 
           }
         }
       } else {
+        uint32_t w[GP];
+        bool more_up = false;
 #pragma unroll
         for (int x = 0; x < GP; ++x) {
-          const uint32_t w = *(const uint32_t*)(swv + (g * GP + x) * 64 + col * 4);
-          const int all = (int)(wave_max(odd_word(w) ? 0x400u : max(0x400u, w & 0x7fffu)) >> 10) - 14;
+          w[x] = *(const uint32_t*)(swv + (g * GP + x) * 64 + col * 4) & 0x7fffu;
+          more_up |= w[x] >= top[x];
 #pragma unroll
-          for (int n = 0; n < NC; ++n) up_now[n][x] = max(up[n][x], all);
+          for (int n = 0; n < NC; ++n) up_now[n][x] = up[n][x];
+        }
+        if (__any(more_up)) {
+#pragma unroll
+          for (int x = 0; x < GP; ++x) {
+            const int all = (int)(wave_max(w[x] >= 0x7c00u ? 0u : w[x]) >> 10);
+            top[x] = max(top[x], (uint32_t)(all + 1) << 10);
+#pragma unroll
+            for (int n = 0; n < NC; ++n) up_now[n][x] = max(up[n][x], all - 14);
+          }
         }
       }
       float e[NC][4][4];
+      u32x4_t ew[NC][2];  // the same in fp16, pairs of keys 16 k + 4 g + i with k = (0, 1) and (2, 3)
 #pragma unroll
       for (int n = 0; n < NC; ++n) {
         float mx = fmaxf(fmaxf(sc[n][0][0], sc[n][1][0]), fmaxf(sc[n][2][0], sc[n][3][0]));
@@ -496,7 +529,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few4_kernel(const 
           for (int x = 0; x < GP; ++x) {
             const float fx = __builtin_ldexpf(f, up[n][x] - up_now[n][x]);
             up[n][x] = up_now[n][x];
-            bs[n][x] *= f;
+            for (int r = 0; r < (kSumInRow ? 4 : 2); ++r) bs[n][x][r] *= f;
             for (int r = 0; r < (kSumInRow ? 4 : 1); ++r) ps[n][x][r] *= fx;
 #pragma unroll
             for (int d = x * (GROUP / 16); d < (x + 1) * (GROUP / 16); ++d)
@@ -505,11 +538,16 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few4_kernel(const 
         }
         const float mr = m[n] == kNegInf ? 0.f : m[n];
 #pragma unroll
-        for (int kt = 0; kt < 4; ++kt) {
+        for (int kt = 0; kt < 4; ++kt)
 #pragma unroll
           for (int r = 0; r < 4; ++r) e[n][kt][r] = exp2_fast(__builtin_fmaf(sc[n][kt][r], sl[n], -mr));
-          l[n] += (e[n][kt][0] + e[n][kt][1]) + (e[n][kt][2] + e[n][kt][3]);
-        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            ew[n][h][r] = pack2(F16{}, e[n][2 * h][r], e[n][2 * h + 1][r]);
+            l[n] = add2(F16{}, ew[n][h][r], l[n]);
+          }
       }
       // a key that only some columns see may stand for an infinity or a NaN
       if (cut && q.nq > 1) {
@@ -524,42 +562,52 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few4_kernel(const 
       const int vrow = 16 * (col >> 2) + 4 * g + (col & 3);
 #pragma unroll
       for (int x = 0; x < GP; ++x) {
-        // the weights times the keys' scales, pairs of keys 16 k + 4 g + i with k = (0, 1) and (2, 3); and
-        // times the values of code 8
+        // the weights times the keys' scales, in the same pairs
         u32x4_t p[NC][2];
         u32x4_t w[4];
 #pragma unroll
         for (int kt = 0; kt < 4; ++kt) w[kt] = *(const u32x4_t*)(swv + (kt * GP + x) * 64 + g * 16);
-        float even[NC], odd[NC];
 #pragma unroll
-        for (int n = 0; n < NC; ++n) even[n] = __builtin_ldexpf(1.f, 7 - up[n][x]), odd[n] = 0.0625f * even[n];
+        for (int n = 0; n < NC; ++n) {
+          const float even = __builtin_ldexpf(1.f, 7 - up[n][x]), odd = 0.0625f * even;
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const f16x2_t w0 = h2(w[2 * h][r]), w1 = h2(w[2 * h + 1][r]);
-            const float m0 = __builtin_fmaf(8.f, (float)w0[0], (float)w0[1]), m1 = __builtin_fmaf(8.f, (float)w1[0], (float)w1[1]);
+            for (int r = 0; r < 4; ++r) {
+              // one instruction each: a fused product whose operand and result are halves
+              f16x2_t y;
+              y[0] = (_Float16)__builtin_fmaf(e[n][2 * h][r] * (r & 1 ? odd : even), (float)h2(w[2 * h][r])[0], 0.f);
+              y[1] = (_Float16)__builtin_fmaf(e[n][2 * h + 1][r] * (r & 1 ? odd : even), (float)h2(w[2 * h + 1][r])[0], 0.f);
+              p[n][h][r] = w2(y);
+            }
+        }
+        // the sums of weight times scale (even rows) and times bias (odd rows), and of those products times
+        // 2^-24 by a row of ones; where that takes too many registers on the vector units
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if constexpr (kSumInRow) {
+            u32x4_t sb;
+            const uint32_t half = ln & 1 ? 0x07060302u : 0x05040100u;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sb[r] = perm(w[2 * h + 1][r], w[2 * h][r], half);
 #pragma unroll
             for (int n = 0; n < NC; ++n) {
-              const float e0 = e[n][2 * h][r], e1 = e[n][2 * h + 1][r], up1 = r & 1 ? odd[n] : even[n];
-              p[n][h][r] = pack2(F16{}, (e0 * up1) * (float)w0[0], (e1 * up1) * (float)w1[0]);
-              bs[n][x] = __builtin_fmaf(e0, m0, bs[n][x]);
-              bs[n][x] = __builtin_fmaf(e1, m1, bs[n][x]);
-            }
-          }
-        // the sums of those products: times 2^-24 by a row of ones, or in one register each
-#pragma unroll
-        for (int n = 0; n < NC; ++n)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if constexpr (kSumInRow) {
+              bs[n][x] = mfma16(F16{}, sb, ew[n][h], bs[n][x]);
               ps[n][x] = mfma16(F16{}, u32x4_t{0x00010001u, 0x00100010u, 0x00010001u, 0x00100010u}, p[n][h], ps[n][x]);
-            } else {
+            }
+          } else {
 #pragma unroll
-              for (int r = 0; r < 4; ++r)
+            for (int r = 0; r < 4; ++r) {
+              const uint32_t s = perm(w[2 * h + 1][r], w[2 * h][r], 0x05040100u), b = perm(w[2 * h + 1][r], w[2 * h][r], 0x07060302u);
+#pragma unroll
+              for (int n = 0; n < NC; ++n) {
+                bs[n][x][0] = dot2(F16{}, ew[n][h][r], s, bs[n][x][0]);
+                bs[n][x][1] = dot2(F16{}, ew[n][h][r], b, bs[n][x][1]);
                 ps[n][x][0] = dot2(F16{}, p[n][h][r], r & 1 ? 0x4c004c00u : 0x3c003c00u, ps[n][x][0]);  // 16 or 1
+              }
             }
           }
+        }
 #pragma unroll
         for (int dd = 0; dd < GROUP / 16; ++dd) {
           const int d = x * (GROUP / 16) + dd;
@@ -573,11 +621,6 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few4_kernel(const 
         }
         __builtin_amdgcn_sched_barrier(0);
       }
-      if (more) {
-        attn_wait_lds();
-        tc.template copy<true>(a, vb, vw, sv, swv, ln);
-        if (t + 2 < tb) tc.lookup(a, table, k0 + 512, lo, hi, ln, false);
-      }
     }
 
     // to the units of the sums: the factors of the weights and of the codes, and the groups' middles
@@ -586,9 +629,13 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few4_kernel(const 
 #pragma unroll
       for (int x = 0; x < GP; ++x) {
         const float held = __builtin_ldexpf(1.f, up[n][x] + 24 - 7);
-        float sum = ps[n][x][0];
-        if (!kSumInRow) sum = join32(join16(sum, SumF()), SumF()) * 0x1p-24f;
-        const float b = join32(join16(bs[n][x], SumF()), SumF()) - 8.f * (sum * held);
+        float sum = ps[n][x][0], ss = bs[n][x][0], sb = bs[n][x][1];
+        if (!kSumInRow) {
+          sum = join32(join16(sum, SumF()), SumF()) * 0x1p-24f;
+          ss = join32(join16(ss, SumF()), SumF());
+          sb = join32(join16(sb, SumF()), SumF());
+        }
+        const float b = sb + 8.f * (ss - sum * held);
 #pragma unroll
         for (int d = x * (GROUP / 16); d < (x + 1) * (GROUP / 16); ++d)
           for (int r = 0; r < 4; ++r) o[n][d][r] = __builtin_fmaf(o[n][d][r], held, b);

@@ -143,7 +143,7 @@ struct AttnPlan {
   size_t part_off, part_tile_off, bytes;  // workspace: records, pieces of either kernel
 };
 AttnPlan attn_plan(int64_t t, int64_t n_seqs, int64_t hq, int64_t hk, int d, int64_t max_q, int64_t max_kv,
-                   int64_t window, int few_keys = kAttnFewKeys);
+                   int64_t window, int few_keys);
 // Sets the kind of records.
 void attn_record_kind(AttnArgs& a);
 hipError_t launch_attn_few(const AttnArgs& a, int dt, int d, int nc, hipStream_t s);

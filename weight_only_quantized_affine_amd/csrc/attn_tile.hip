@@ -353,12 +353,11 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
       if constexpr (kDecode) {
         float amax = 0.f;
 #pragma unroll
-        for (int st = 0; st < NS; ++st) amax = amax8(qf[st], amax);
-        const int t = a.io == DT_BF16 ? q_exponent(join32(amax, MaxF())) : 0;
-        const float factor = __builtin_ldexpf(1.f, -t);
-        row_sl = __builtin_ldexpf(a.sl, t);
+        for (int st = 0; st < NS; ++st) amax = amax8(qf[st], a.io, amax);
+        const int t = q_exponent(join32(amax, MaxF()));
+        row_sl = q_scale(a.sl, t);
 #pragma unroll
-        for (int st = 0; st < NS; ++st) qf[st] = q_pairs(qf[st], a.io, factor);
+        for (int st = 0; st < NS; ++st) qf[st] = q_pairs(qf[st], a.io, t);
       }
     }
     // first and last position among the wave's rows
