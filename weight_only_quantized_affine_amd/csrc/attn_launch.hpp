@@ -45,11 +45,14 @@ struct NormRopeArgs {
   int64_t max_pos;
 };
 hipError_t launch_norm_rope(const NormRopeArgs& a, int dt, hipStream_t s);
-// The append to a cache in 4 bits: k_out and v_out are the codes, with the strides of k_out.
+// The append to a cache in 4 bits: k_out and v_out are the codes, with the strides of k_out.  hk and hv are 0 (what
+// the norm and rotation of q goes by); the rows of k and v are cache_heads each.
 struct Append4Args : NormRopeArgs {
+  int cache_heads;
   uint32_t *k_groups, *v_groups;
   int64_t group_ps, group_ts, group_hs;  // words
   int group;
+  double inv_d;  // 1 / d
 };
 hipError_t launch_append4(const Append4Args& a, int dt, hipStream_t s);
 // The values of its rows.

@@ -6,21 +6,23 @@
 // list, page j that it takes entry F + back - 1 - (need_before[s] + j).  All of it is a few words a
 // sequence and 16 bytes a token, so what bounds it is latency: one workgroup decides and lays out the
 // sequences, and the tokens follow in the same workgroup where they are few, else in a second launch over
-// all of the chip.
+// all of the chip.  Pages are moved one a thread, whose sequence it finds in the prefix (a wave taking sequence
+// after sequence: 300 of them, 100 with chunks, 14 us against 12).
+//
+// Measured (in a graph): 64 single tokens 5 us, 300 sequences, 20 of which give back all their pages, and 13000
+// tokens 15.
 #include "attn_launch.hpp"
 #include "device_common.hpp"
 
 namespace ql {
 namespace {
 
-constexpr int kThreads = 1024, kWaves = kThreads / 64;
-
 // The exclusive prefixes of x and y over the workgroup's threads; sh holds a pair per wave.  The sums are
 // within 2^31: the batch has been found to fit.
 struct Pair {
   int x, y;
 };
-__device__ __forceinline__ Pair block_scan2(Pair v, Pair* sh, Pair& total) {
+template <int kWaves> __device__ __forceinline__ Pair block_scan2(Pair v, Pair* sh, Pair& total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   Pair p = v;
 #pragma unroll
@@ -67,55 +69,50 @@ __device__ __forceinline__ Ask ask(const ExtendArgs& a, int s) {
   return k;
 }
 
-// Moves the n pages of each lane's sequence: move(s, x, y, j) its page j.  Few pages are moved by their own
-// lane, more by all lanes of the wave, sequence after sequence.
-template <class Move> __device__ __forceinline__ void move_pages(int s, int n, int x, int y, Move&& move) {
-  const bool few = n <= 4;
-  if (few)
-    for (int j = 0; j < n; ++j) move(s, x, y, j);
-  uint64_t many = __ballot(!few);
-  while (many) {
-    const int from = __builtin_ctzll(many);
-    many &= many - 1;
-    const int s1 = __builtin_amdgcn_readlane(s, from), n1 = __builtin_amdgcn_readlane(n, from);
-    const int x1 = __builtin_amdgcn_readlane(x, from), y1 = __builtin_amdgcn_readlane(y, from);
-    for (int j = threadIdx.x & 63; j < n1; j += 64) move(s1, x1, y1, j);
+// The last of n ascending numbers that is at most i (the first is).
+__device__ __forceinline__ int last_at_most(const int* x, int n, int64_t i) {
+  int b = 0, e = n;
+  while (e - b > 1) {
+    const int m = (b + e) / 2;
+    if (x[m] <= i) b = m; else e = m;
   }
+  return b;
 }
 
-// Rows [first, last) of positions and slots, by the threads of this workgroup.
-__device__ __forceinline__ void tokens(const ExtendArgs& a, int64_t first, int64_t last) {
-  const int total = a.cu_q[a.n_seqs];
-  for (int64_t i = first + threadIdx.x; i < last; i += kThreads) {
-    int64_t pos = 0, slot = -1;
-    if (i < total) {
-      int b = 0, e = a.n_seqs;  // the last sequence with cu_q <= i
-      while (e - b > 1) {
-        const int m = (b + e) / 2;
-        if (a.cu_q[m] <= i) b = m; else e = m;
-      }
-      pos = (int64_t)a.lens_out[b] - a.cu_q[b + 1] + i;  // its length before, and the tokens before this one
-      const int64_t page = a.page_div.div((uint32_t)pos);
-      slot = (int64_t)a.table[b * a.table_stride + page] * a.page_size + (pos - page * a.page_size);
-    }
-    a.positions[i] = pos;
-    a.slots[i] = slot;
+// Row i of positions and slots, cu and lens the prefix and the lengths after of the sequences [0, n).
+__device__ __forceinline__ void token(const ExtendArgs& a, int64_t i, int total, const int* cu, const int* lens) {
+  int64_t pos = 0, slot = -1;
+  if (i < total) {
+    const int b = last_at_most(cu, a.n_seqs, i);
+    pos = (int64_t)lens[b] - cu[b + 1] + i;  // its length before, and the tokens before this one
+    const int64_t page = a.page_div.div((uint32_t)pos);
+    slot = (int64_t)a.table[b * a.table_stride + page] * a.page_size + (pos - page * a.page_size);
   }
+  a.positions[i] = pos;
+  a.slots[i] = slot;
 }
 
-__global__ __launch_bounds__(kThreads) void extend_kernel(const ExtendArgs a, int with_tokens) {
+// Sequences whose prefix and lengths are searched in LDS.
+constexpr int kHeld = 4096;
+
+// THREADS: one workgroup.  Where the sequences are at most as many as the threads each thread asks once.
+template <int THREADS> __global__ __launch_bounds__(THREADS) void extend_kernel(const ExtendArgs a, int with_tokens) {
+  constexpr int kWaves = THREADS / 64;
   __shared__ Pair sh[kWaves];
   __shared__ int64_t sums[kWaves][3];
+  __shared__ int scu[THREADS + 1], slen[THREADS], spre[THREADS], shave[THREADS];
   const int tid = threadIdx.x;
-  const bool list = a.free_pages != nullptr;
+  const bool list = a.free_pages != nullptr, once = a.n_seqs <= THREADS;
   const int64_t f0 = list ? a.free_count[0] : 0;
   // what the whole batch asks for
   int64_t tok = 0, back = 0, need = 0;
   bool fits = true;
-  for (int s = tid; s < a.n_seqs; s += kThreads) {
-    const Ask k = ask(a, s);
-    tok += k.now, back += k.back, need += k.need;
-    fits &= k.fits;
+  Ask mine = {};
+  mine.fits = true;
+  for (int s = tid; s < a.n_seqs; s += THREADS) {
+    mine = ask(a, s);
+    tok += mine.now, back += mine.back, need += mine.need;
+    fits &= mine.fits;
   }
   tok = wave_sum(tok), back = wave_sum(back), need = wave_sum(need);
   if ((tid & 63) == 0) sums[tid >> 6][0] = tok, sums[tid >> 6][1] = back, sums[tid >> 6][2] = need;
@@ -124,43 +121,59 @@ __global__ __launch_bounds__(kThreads) void extend_kernel(const ExtendArgs a, in
   for (int w = 0; w < kWaves; ++w) tok += sums[w][0], back += sums[w][1], need += sums[w][2];
   int why = (tok > a.rows ? 1 : 0) | (misfit ? 4 : 0);
   if (list) why |= (need > f0 + back ? 2 : 0) | (f0 < 0 || f0 + back > a.free_cap ? 8 : 0);
+  auto asked = [&](int s) {
+    if (once) return mine;
+    return ask(a, s);
+  };
   // pages that come back
   if (why == 0 && back > 0) {
     int before = (int)f0;
-    for (int s0 = 0; s0 < a.n_seqs; s0 += kThreads) {
+    for (int s0 = 0; s0 < a.n_seqs; s0 += THREADS) {
       const int s = s0 + tid;
       Pair v = {0, 0}, total;
-      if (s < a.n_seqs) v.x = ask(a, s).back;
-      const Pair e = block_scan2(v, sh, total);
-      move_pages(s, v.x, before + e.x, 0,
-                 [&](int s, int to, int, int j) { a.free_pages[to + j] = a.table[s * a.table_stride + j]; });
+      if (s < a.n_seqs) v.x = asked(s).back;
+      spre[tid] = block_scan2<kWaves>(v, sh, total).x;
+      __syncthreads();
+      for (int i = tid; i < total.x; i += THREADS) {
+        const int b = last_at_most(spre, min(THREADS, a.n_seqs - s0), i);
+        a.free_pages[before + i] = a.table[(s0 + b) * a.table_stride + i - spre[b]];
+      }
+      __syncthreads();
       before += total.x;
     }
-    __syncthreads();
   }
   // lengths, prefix and pages that are taken
   int row = 0, taken = 0;
-  for (int s0 = 0; s0 < a.n_seqs; s0 += kThreads) {
+  for (int s0 = 0; s0 < a.n_seqs; s0 += THREADS) {
     const int s = s0 + tid;
     Pair v = {0, 0}, total;
     Ask k = {};
     if (s < a.n_seqs && why == 0) {
-      k = ask(a, s);
+      k = asked(s);
       v = {k.now, k.need};
     }
-    const Pair e = block_scan2(v, sh, total);
+    const Pair e = block_scan2<kWaves>(v, sh, total);
     if (s < a.n_seqs) {
-      a.cu_q[s] = row + e.x;
       const int len = why == 0 ? k.old + k.now : a.lens[s];
+      a.cu_q[s] = row + e.x;
       a.lens_out[s] = len;
+      if (once) scu[tid] = row + e.x, slen[tid] = len;
     }
-    move_pages(s, v.y, (int)(f0 + back) - 1 - (taken + e.y), k.have,
-               [&](int s, int top, int have, int j) { a.table[s * a.table_stride + have + j] = a.free_pages[top - j]; });
+    if (total.y > 0) {  // uniform
+      spre[tid] = e.y, shave[tid] = k.have;
+      __syncthreads();
+      for (int i = tid; i < total.y; i += THREADS) {
+        const int b = last_at_most(spre, min(THREADS, a.n_seqs - s0), i);
+        a.table[(s0 + b) * a.table_stride + shave[b] + i - spre[b]] = a.free_pages[(int)(f0 + back) - 1 - taken - i];
+      }
+      __syncthreads();
+    }
     row += total.x, taken += total.y;
   }
   if (tid == 0) {
     const int left = (int)(why ? f0 : f0 + back - need);
     a.cu_q[a.n_seqs] = row;
+    if (once) scu[a.n_seqs] = row;
     if (list) a.free_count_out[0] = left;
     a.info[0] = row;
     a.info[1] = taken;
@@ -169,23 +182,41 @@ __global__ __launch_bounds__(kThreads) void extend_kernel(const ExtendArgs a, in
   }
   if (with_tokens) {
     __syncthreads();
-    tokens(a, 0, a.rows);
+    for (int64_t i = tid; i < a.rows; i += THREADS)
+      if (once)
+        token(a, i, row, scu, slen);
+      else
+        token(a, i, row, a.cu_q, a.lens_out);
   }
 }
 
-__global__ __launch_bounds__(kThreads) void extend_tokens_kernel(const ExtendArgs a) {
-  const int64_t first = (int64_t)blockIdx.x * kThreads;
-  tokens(a, first, min(first + kThreads, a.rows));
+__global__ __launch_bounds__(1024) void extend_tokens_kernel(const ExtendArgs a) {
+  __shared__ int scu[kHeld + 1], slen[kHeld];
+  const int64_t i = (int64_t)blockIdx.x * 1024 + threadIdx.x;
+  if (a.n_seqs <= kHeld) {
+    for (int s = threadIdx.x; s <= a.n_seqs; s += 1024) {
+      scu[s] = a.cu_q[s];
+      if (s < a.n_seqs) slen[s] = a.lens_out[s];
+    }
+    __syncthreads();
+    if (i < a.rows) token(a, i, scu[a.n_seqs], scu, slen);
+  } else if (i < a.rows) {
+    token(a, i, a.cu_q[a.n_seqs], a.cu_q, a.lens_out);
+  }
 }
 
 }  // namespace
 
 hipError_t launch_kv_extend(const ExtendArgs& a, hipStream_t s) {
-  const bool one = a.rows <= 4 * kThreads;
-  extend_kernel<<<1, kThreads, 0, s>>>(a, one ? 1 : 0);
+  // small steps in one launch, by as few waves as hold a sequence a thread (their barriers cost most)
+  const bool one = a.rows <= 4096;
+  if (a.n_seqs <= 256 && (a.rows <= 1024 || !one))
+    extend_kernel<256><<<1, 256, 0, s>>>(a, one ? 1 : 0);
+  else
+    extend_kernel<1024><<<1, 1024, 0, s>>>(a, one ? 1 : 0);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || one) return e;
-  extend_tokens_kernel<<<(unsigned)((a.rows + kThreads - 1) / kThreads), kThreads, 0, s>>>(a);
+  extend_tokens_kernel<<<(unsigned)((a.rows + 1023) / 1024), 1024, 0, s>>>(a);
   return hipGetLastError();
 }
 

@@ -17,8 +17,6 @@
 // Append to a cache in 4 bits: the rows of k (in 64 bits up to their rounding, since a code hangs on the last
 // bits) and of v are quantized where they are, 8 values and one word of codes a lane, a group's
 // smallest and largest value by DPP within its 4, 8 or 16 lanes.
-#include <type_traits>
-
 #include "head_common.hpp"
 
 namespace ql {
@@ -67,6 +65,13 @@ template <int CTRL> __device__ __forceinline__ double add_dpp(double x) {
   const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, 0xf, 0xf, false);
   return x + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
+// The value 8 lanes further in 16.
+__device__ __forceinline__ double turn8(double x) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, 0x128, 0xf, 0xf, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), 0x128, 0xf, 0xf, false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
 template <int L> __device__ __forceinline__ double group_sum(double x) {
   if (L >= 2) x = add_dpp<0xB1>(x);
   if (L >= 4) x = add_dpp<0x4E>(x);
@@ -75,6 +80,13 @@ template <int L> __device__ __forceinline__ double group_sum(double x) {
   if (L >= 32) x += __shfl_xor(x, 16);
   if (L >= 64) x += __shfl_xor(x, 32);
   return x;
+}
+
+// 1 / sqrt(x) within 2^-50 of its value: the approximate one (2^-26 and better) after one step of third order.
+__device__ __forceinline__ double rsqrt64(double x) {
+  const double r = __builtin_amdgcn_rsq(x);
+  const double e = __builtin_fma(-x * r, r, 1.);
+  return __builtin_fma(r * e, __builtin_fma(0.375, e, 0.5), r);
 }
 
 // Monotone integer key of an fp32 value (-0 < +0), and back.
@@ -104,22 +116,53 @@ __device__ __forceinline__ uint32_t quantize8(const float* f, int lanes, uint32_
   const float s = f16_bits_to_f32(sb), b = f16_bits_to_f32(bb);
   group = held ? sb | (bb << 16) : 0x7e000000u;
   if (!held || s == 0.f) return 0;
-  uint32_t word = 0;
+  // rint of the rounded quotient: an approximate one and its residual tell it, but next to a half
+  const float inv = __builtin_amdgcn_rcpf(s), edge = s * (0.5f - 0x1p-18f);
+  float d[8], r[8];
+  bool near_half = false;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    float r = __builtin_rintf(__fdiv_rn(f[j] - b, s));
-    r = fminf(fmaxf(r, 0.f), 15.f);
-    word |= (uint32_t)r << (4 * j);
+    d[j] = f[j] - b;
+    r[j] = __builtin_rintf(d[j] * inv);
+    near_half |= !(__builtin_fabsf(__builtin_fmaf(-r[j], s, d[j])) < edge);
   }
+  if (near_half) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] = __builtin_rintf(__fdiv_rn(d[j], s));
+  }
+  uint32_t word = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) word |= (uint32_t)__builtin_amdgcn_fmed3f(r[j], 0.f, 15.f) << (4 * j);
   return word;
 }
 
-template <typename T, int L, int ROWS, typename Args>
-__global__ __launch_bounds__(256) void norm_rope_kernel(const Args a, FastDiv per_token, int groups, int64_t units) {
-  constexpr bool kQuant = std::is_same_v<Args, Append4Args>;
+// The cosines and sines of a position's row for the 8 values of chunk c; second: of the pairs' second values
+// (not interleaved: sn holds the sign).
+__device__ __forceinline__ void cos_sin8(const float* at, int rot, bool interleaved, int c, bool second, float* cs, float* sn) {
+  const f32x4_t* row = (const f32x4_t*)at;
+  const int n = rot / 8;  // 4-value words of the cosines
+  if (interleaved) {
+    const f32x4_t u = row[c], v = row[n + c];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) cs[2 * i] = cs[2 * i + 1] = u[i], sn[2 * i] = sn[2 * i + 1] = v[i];
+  } else {
+    const int b = 2 * (second ? c - rot / 16 : c);
+    const f32x4_t u0 = row[b], u1 = row[b + 1], v0 = row[n + b], v1 = row[n + b + 1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      cs[i] = u0[i], cs[4 + i] = u1[i];
+      sn[i] = second ? v0[i] : -v0[i], sn[4 + i] = second ? v1[i] : -v1[i];
+    }
+  }
+}
+
+// Rows of unit (block `block`): ROWS heads of one token.
+template <typename T, int L, int ROWS>
+__device__ __forceinline__ void norm_rope_rows(const NormRopeArgs& a, int block, FastDiv per_token, int groups,
+                                               int64_t units) {
   const int lane = threadIdx.x & 63;
   const int c = lane % L;  // the lane's 8 values of a row
-  const int64_t unit = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+  const int64_t unit = (int64_t)block * (256 / L) + threadIdx.x / L;
   if (unit >= units) return;  // whole groups of lanes
   const int64_t tok = (int64_t)per_token.div((uint32_t)unit);
   const int h0 = (int)(unit - tok * groups) * ROWS;
@@ -185,56 +228,6 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(const Args a, FastDiv pe
     const void* wp = is_q ? a.q_weight : is_v ? nullptr : a.k_weight;
     float f[8];
     unpack8<T>(x[i], f);
-    if constexpr (kQuant) {
-      if (!is_q) {
-        if (!is_v) {
-          double y[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] = f[j];
-          if (wp) {
-            double ss = 0.;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) ss += (double)(f[j] * f[j]);  // 22 bits: exact
-            const double r = 1. / __builtin_sqrt(group_sum<L>(ss) / a.d + (double)a.eps);
-            if (wp != loaded) {
-              if (on) weights8(wp, a.wdt, c, w);
-              loaded = wp;
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = y[j] * r * w[j];
-          }
-          if (a.rot > 0) {
-            double z[8];
-            if (a.interleaved) {
-#pragma unroll
-              for (int j = 0; j < 8; j += 2) {
-                z[j] = y[j] * cs[j] - y[j + 1] * sn[j];
-                z[j + 1] = y[j + 1] * cs[j] + y[j] * sn[j];
-              }
-            } else {
-              const int from = (lane & ~(L - 1)) | ((second ? c - half : c + half) & (L - 1));
-#pragma unroll
-              for (int j = 0; j < 8; ++j) z[j] = y[j] * cs[j] + __shfl(y[j], from) * sn[j];  // sn holds the sign
-            }
-            if (turned) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j) y[j] = z[j];
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] = known ? param_to_f32<T>(f32_to_bits<T>((float)y[j])) : 0.f;
-        }
-        uint32_t group;
-        const uint32_t word = quantize8(f, a.group / 8, group);
-        if (h >= heads || !on || page < 0) continue;
-        const int hh = is_v ? h - a.hq - a.hk : h - a.hq;
-        uint8_t* cp = (is_v ? a.v_out : a.k_out) + page * a.page_stride + at * a.ko_ts + hh * a.ko_hs;
-        ((uint32_t*)cp)[c] = word;
-        uint32_t* gp = (is_v ? a.v_groups : a.k_groups) + page * a.group_ps + at * a.group_ts + hh * a.group_hs;
-        if ((c & (a.group / 8 - 1)) == 0) gp[c / (a.group / 8)] = group;
-        continue;
-      }
-    }
     if (wp) {
       float ss = 0.f;
 #pragma unroll
@@ -302,14 +295,110 @@ __global__ __launch_bounds__(256) void norm_rope_kernel(const Args a, FastDiv pe
   }
 }
 
-template <typename T, int L, int ROWS, typename Args> hipError_t run_rows(const Args& a, hipStream_t s) {
+template <typename T, int L, int ROWS>
+__global__ __launch_bounds__(256) void norm_rope_kernel(const NormRopeArgs a, FastDiv per_token, int groups,
+                                                        int64_t units) {
+  norm_rope_rows<T, L, ROWS>(a, blockIdx.x, per_token, groups, units);
+}
+
+// One row of k or v: normed, rotated (k) and quantized, 8 values and a word of codes a lane.
+template <typename T, int L>
+__device__ __forceinline__ void quantized_row(const Append4Args& a, int64_t tok, int h, bool is_v) {
+  const int lane = threadIdx.x & 63;
+  const int c = lane % L;
+  const bool on = 8 * c < a.d;
+  const int64_t slot = a.slots[tok];
+  const uint8_t* p = is_v ? a.v + tok * a.v_ts + h * a.v_hs : a.k + tok * a.k_ts + h * a.k_hs;
+  u32x4_t x = {0, 0, 0, 0};
+  if (on) x = *(const u32x4_t*)(p + 16 * c);
+  float f[8];
+  unpack8<T>(x, f);
+  if (!is_v) {
+    const int half = a.rot / 16;  // lanes between the two values of a pair
+    const bool turned = 8 * c < a.rot, second = !a.interleaved && c >= half;
+    bool known = true;
+    float cs[8] = {}, sn[8] = {};
+    if (a.rot > 0) {
+      const int64_t pos = a.positions[tok];
+      known = pos >= 0 && pos < a.max_pos;
+      if (turned) cos_sin8(a.cos_sin + (known ? pos : 0) * a.rot, a.rot, a.interleaved, c, second, cs, sn);
+    }
+    double y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = f[j];
+    if (a.k_weight) {
+      float w[8] = {};
+      if (on) weights8(a.k_weight, a.wdt, c, w);
+      double ss = 0.;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss += (double)(f[j] * f[j]);  // 22 bits: exact
+      const double r = rsqrt64(__builtin_fma(group_sum<L>(ss), a.inv_d, (double)a.eps));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = y[j] * r * w[j];
+    }
+    if (a.rot > 0) {
+      double z[8];
+      if (a.interleaved) {
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          z[j] = y[j] * cs[j] - y[j + 1] * sn[j];
+          z[j + 1] = y[j + 1] * cs[j] + y[j] * sn[j];
+        }
+      } else {
+        const int from = (lane & ~(L - 1)) | ((second ? c - half : c + half) & (L - 1));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const double o = L == 16 && half == 8 ? turn8(y[j]) : __shfl(y[j], from);
+          z[j] = y[j] * cs[j] + o * sn[j];  // sn holds the sign
+        }
+      }
+      if (turned) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = z[j];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const uint32_t two = known ? pack2(T{}, (float)y[j], (float)y[j + 1]) : 0u;
+      f[j] = param_to_f32<T>(two & 0xffffu), f[j + 1] = param_to_f32<T>(two >> 16);
+    }
+  }
+  uint32_t group;
+  const uint32_t word = quantize8(f, a.group / 8, group);
+  if (!on || slot < 0 || slot >= a.n_slots) return;  // a token without a slot is not stored
+  const int64_t page = a.page_div.div((uint32_t)slot), at = slot - page * a.page_size;
+  uint8_t* cp = (is_v ? a.v_out : a.k_out) + page * a.page_stride + at * a.ko_ts + h * a.ko_hs;
+  ((uint32_t*)cp)[c] = word;
+  const int per = a.group / 8;
+  uint32_t* gp = (is_v ? a.v_groups : a.k_groups) + page * a.group_ps + at * a.group_ts + h * a.group_hs;
+  if ((c & (per - 1)) == 0) gp[c / per] = group;
+}
+
+// The rows of q as above in the first q_blocks blocks; then those of k and v, a head's tokens side by side, so
+// that a wave's rows are neighbours in a page (4096 tokens, 32 heads on 8: 25 us; with a token's rows
+// side by side 31, and 41 where a wave held q next to k and v).
+template <typename T, int L, int ROWS>
+__global__ __launch_bounds__(256) void append4_kernel(const Append4Args a, FastDiv per_token, int groups, int64_t q_units,
+                                                      int q_blocks, FastDiv per_head) {
+  if ((int)blockIdx.x < q_blocks) {
+    norm_rope_rows<T, L, ROWS>(a, blockIdx.x, per_token, groups, q_units);
+  } else {
+    const int64_t unit = (int64_t)(blockIdx.x - q_blocks) * (256 / L) + threadIdx.x / L;
+    if (unit >= a.t * 2 * a.cache_heads) return;  // whole groups of lanes
+    const int h = (int)per_head.div((uint32_t)unit);
+    const bool is_v = h >= a.cache_heads;
+    quantized_row<T, L>(a, unit - (int64_t)h * a.t, is_v ? h - a.cache_heads : h, is_v);
+  }
+}
+
+template <typename T, int L, int ROWS> hipError_t run_rows(const NormRopeArgs& a, hipStream_t s) {
   const int groups = (a.hq + a.hk + a.hv + ROWS - 1) / ROWS;
   const int64_t units = a.t * groups;
   const unsigned grid = (unsigned)((units + 256 / L - 1) / (256 / L));
-  norm_rope_kernel<T, L, ROWS, Args><<<grid, 256, 0, s>>>(a, fast_div((uint32_t)groups), groups, units);
+  norm_rope_kernel<T, L, ROWS><<<grid, 256, 0, s>>>(a, fast_div((uint32_t)groups), groups, units);
   return hipGetLastError();
 }
-template <typename T, int L, typename Args> hipError_t run(const Args& a, hipStream_t s) {
+template <typename T, int L> hipError_t run(const NormRopeArgs& a, hipStream_t s) {
   // Waves when each lane holds one row: below 16 a compute unit the launch's latency counts and one
   // row a lane is shortest (1, 2, 4 rows: 1 token x 40 rows of 128 2.9, 3.3, 4.2 us; 256 tokens 3.6,
   // 3.9, 4.8); from 64 on the rows in flight count (512 tokens 4.9, 4.5, 5.3; 1024 8.5, 6.2, 6.8;
@@ -317,6 +406,20 @@ template <typename T, int L, typename Args> hipError_t run(const Args& a, hipStr
   // to memory (non-temporal stores, 8192 tokens: 41 -> 35 us; what reads them next is not slower).
   const int64_t waves = a.t * (a.hq + a.hk + a.hv) * L / 64;
   return waves < 4096 ? run_rows<T, L, 1>(a, s) : waves < 16384 ? run_rows<T, L, 2>(a, s) : run_rows<T, L, 4>(a, s);
+}
+// Rows a lane of q as above, by the rows of q alone.
+template <typename T, int L, int ROWS> hipError_t append_rows(const Append4Args& a, hipStream_t s) {
+  const int groups = (a.hq + ROWS - 1) / ROWS;
+  const int64_t units = a.t * groups, rows = a.t * 2 * a.cache_heads;
+  const int per = 256 / L, q_blocks = (int)((units + per - 1) / per);
+  const unsigned grid = (unsigned)(q_blocks + (rows + per - 1) / per);
+  append4_kernel<T, L, ROWS><<<grid, 256, 0, s>>>(a, fast_div((uint32_t)(groups > 0 ? groups : 1)), groups, units, q_blocks,
+                                                  fast_div((uint32_t)a.t));
+  return hipGetLastError();
+}
+template <typename T, int L> hipError_t run(const Append4Args& a, hipStream_t s) {
+  const int64_t waves = a.t * a.hq * L / 64;
+  return waves < 4096 ? append_rows<T, L, 1>(a, s) : waves < 16384 ? append_rows<T, L, 2>(a, s) : append_rows<T, L, 4>(a, s);
 }
 template <typename T, typename Args> hipError_t run_l(const Args& a, hipStream_t s) {
   const int n = a.d / 8;

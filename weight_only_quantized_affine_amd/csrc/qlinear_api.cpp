@@ -1065,6 +1065,9 @@ ql_status qlinear_kv_append_4bit(const ql_heads* q, const ql_heads* q_out, const
   a.group_ts = cache->group_token_stride;
   a.group_hs = cache->group_head_stride;
   a.group = (int)cache->group_size;
+  a.inv_d = 1. / (double)cache->d;
+  a.cache_heads = (int)cache->hk;
+  a.hk = a.hv = 0;
   return launched(ql::launch_append4(a, dt(dtype), (hipStream_t)stream), fn);
 }
 

@@ -1,5 +1,7 @@
 // Around routed experts: the choice of each token's experts from its router logits, and the weighted sum of
 // their outputs.
+#include <type_traits>
+
 #include "attn_launch.hpp"
 #include "head_common.hpp"
 #include "launch.hpp"
@@ -39,12 +41,51 @@ template <typename F> __device__ __forceinline__ double wave64(double x, F f) {
   // rows of 16 lanes hold their value in every lane
   return f(f(lane64(x, 0), lane64(x, 16)), f(lane64(x, 32), lane64(x, 48)));
 }
+// The largest over the wave, uniform.
+__device__ __forceinline__ int wave_max(int x) {
+  auto step = [&](auto ctrl) { x = max(x, __builtin_amdgcn_update_dpp(x, x, decltype(ctrl)::value, 0xf, 0xf, false)); };
+  step(std::integral_constant<int, 0xB1>{});
+  step(std::integral_constant<int, 0x4E>{});
+  step(std::integral_constant<int, 0x141>{});
+  step(std::integral_constant<int, 0x140>{});
+  return max(max(__builtin_amdgcn_readlane(x, 0), __builtin_amdgcn_readlane(x, 16)),
+             max(__builtin_amdgcn_readlane(x, 32), __builtin_amdgcn_readlane(x, 48)));
+}
 struct Max64 {
   __device__ __forceinline__ double operator()(double a, double b) const { return fmax(a, b); }
 };
 struct Add64 {
   __device__ __forceinline__ double operator()(double a, double b) const { return a + b; }
 };
+
+// e^x for x <= 709.7, within some 2^-52 of its value: 2^k e^r with |r| <= ln 2 / 2, e^r by its series (the
+// first term left out is below 2^-57).
+__device__ __forceinline__ double exp64(double x) {
+  const double k = __builtin_rint(x * 1.4426950408889634074);
+  // ln 2 in two parts, the first with 32 bits, so that k times it is exact
+  const double r = __builtin_fma(-k, 0x1.473de6af278edp-34, __builtin_fma(-k, 0x1.62e42fefp-1, x));
+  double p = 1. / 6227020800.;
+  p = __builtin_fma(p, r, 1. / 479001600.);
+  p = __builtin_fma(p, r, 1. / 39916800.);
+  p = __builtin_fma(p, r, 1. / 3628800.);
+  p = __builtin_fma(p, r, 1. / 362880.);
+  p = __builtin_fma(p, r, 1. / 40320.);
+  p = __builtin_fma(p, r, 1. / 5040.);
+  p = __builtin_fma(p, r, 1. / 720.);
+  p = __builtin_fma(p, r, 1. / 120.);
+  p = __builtin_fma(p, r, 1. / 24.);
+  p = __builtin_fma(p, r, 1. / 6.);
+  p = __builtin_fma(p, r, 0.5);
+  p = __builtin_fma(p, r, 1.);
+  p = __builtin_fma(p, r, 1.);
+  return __builtin_ldexp(p, (int)fmax(k, -1100.));
+}
+// 1 / x for 1 <= x < 2^1023, by Newton's steps.
+__device__ __forceinline__ double inverse64(double x) {
+  double r = __builtin_amdgcn_rcp(x);
+  r = __builtin_fma(__builtin_fma(-x, r, 1.), r, r);
+  return __builtin_fma(__builtin_fma(-x, r, 1.), r, r);
+}
 
 __device__ __forceinline__ float logit_at(const void* row, int dt, int64_t i) {
   if (dt == DT_F32) return ((const float*)row)[i];
@@ -77,7 +118,7 @@ template <int EPL> __global__ __launch_bounds__(256) void select_kernel(const Se
   double p[EPL], c[EPL];
   if (a.sigmoid) {
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) p[j] = 1. / (1. + exp(-(double)x[j]));
+    for (int j = 0; j < EPL; ++j) p[j] = x[j] < -709.5f ? 0. : inverse64(1. + exp64(-(double)fminf(x[j], 800.f)));
   } else {
     float mx = x[0];
 #pragma unroll
@@ -86,7 +127,7 @@ template <int EPL> __global__ __launch_bounds__(256) void select_kernel(const Se
     double z = 0.;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
-      p[j] = m == kOut ? 0. : (double)x[j] == m ? 1. : exp((double)x[j] - m);
+      p[j] = m == kOut ? 0. : (double)x[j] == m ? 1. : exp64(fmax((double)x[j] - m, -800.));
       z += p[j];
     }
     z = wave64(z, Add64());
@@ -104,18 +145,22 @@ template <int EPL> __global__ __launch_bounds__(256) void select_kernel(const Se
   }
   if (a.n_groups > 1) {
     const int m = a.e / a.n_groups;
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) sc[wave][lane * EPL + j] = c[j];
-    __builtin_amdgcn_wave_barrier();
     // lpg lanes a group: the two largest of its c
     const int gi = lane / lpg, sub = lane % lpg;
     double b1 = kOut, b2 = kOut;
-    if (gi < a.n_groups) {
-      for (int i = sub; i < m; i += lpg) {
-        const double v = sc[wave][gi * m + i];
-        b2 = fmax(b2, fmin(b1, v));
-        b1 = fmax(b1, v);
-      }
+    auto take = [&](double v) {
+      b2 = fmax(b2, fmin(b1, v));
+      b1 = fmax(b1, v);
+    };
+    if (m == lpg * EPL) {  // a group's experts are its lanes' own
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) take(c[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) sc[wave][lane * EPL + j] = c[j];
+      __builtin_amdgcn_wave_barrier();
+      if (gi < a.n_groups)
+        for (int i = sub; i < m; i += lpg) take(sc[wave][gi * m + i]);
     }
     for (int o = 1; o < lpg; o <<= 1) {
       const double y1 = __shfl_xor(b1, o), y2 = __shfl_xor(b2, o);
@@ -137,24 +182,37 @@ template <int EPL> __global__ __launch_bounds__(256) void select_kernel(const Se
       if (i < a.e && !((stay >> ((int)group_div.div((uint32_t)i) * lpg)) & 1)) c[j] = kOut;
     }
   }
+  // a round: the lanes' largest, the wave's among them rounded to fp32 (which keeps their order), and where that
+  // leaves more than one lane the wave's in 64 bits
   int my_id = -1;
   double my_p = 0., sum = 0.;
-  for (int r = 0; r < a.k; ++r) {
-    double best = c[0];
+  double best;
+  int at;
+  auto lane_best = [&] {
+    best = c[0], at = 0;
 #pragma unroll
-    for (int j = 1; j < EPL; ++j) best = fmax(best, c[j]);
-    const double top = wave64(best, Max64());
-    const int from = __builtin_ctzll(__ballot(best == top));
-    int at = 0;
+    for (int j = 1; j < EPL; ++j)
+      if (c[j] > best) best = c[j], at = j;
+  };
+  lane_best();
+  for (int r = 0; r < a.k; ++r) {
+    int key = __float_as_int((float)best);
+    key ^= (key >> 31) & 0x7fffffff;  // ordered as the values
+    uint64_t tied = __ballot(key == wave_max(key));
+    if (tied & (tied - 1)) {
+      const double top = wave64(best, Max64());
+      tied = __ballot(best == top);
+    }
+    const int from = __builtin_ctzll(tied);
+    const int j0 = __builtin_amdgcn_readlane(at, from);
     double pv = p[0];
 #pragma unroll
-    for (int j = EPL - 1; j >= 0; --j)
-      if (c[j] == top) at = j, pv = p[j];
-    const int j0 = __builtin_amdgcn_readlane(at, from);
+    for (int j = 1; j < EPL; ++j) pv = j == j0 ? p[j] : pv;
     const double chosen = lane64(pv, from);
     if (lane == from) {
 #pragma unroll
       for (int j = 0; j < EPL; ++j) c[j] = j == j0 ? kOut : c[j];
+      lane_best();
     }
     if (lane == r) my_id = from * EPL + j0, my_p = chosen;
     sum += chosen;
@@ -189,18 +247,25 @@ template <> struct Elem<DT_BF16> {
   static __device__ __forceinline__ uint16_t put(float v) { return (uint16_t)f32_to_bf16_bits(v); }
 };
 
-// V values a thread (16 bytes, or 1 where rows are not multiples of 16 bytes); JB positions at a time.
-template <int DT, int V> __global__ __launch_bounds__(256) void combine_kernel(const CombineArgs a, FastDiv row_div, int64_t units) {
+// V values a thread (16 bytes, or 1 where rows are not multiples of 16 bytes); JB positions at a time, all of their
+// loads in flight, those of positions that are not wanted too.  UNIFORM: a wave lies within one token, whose
+// ids and weights are then scalar loads.
+template <int DT, int V, bool UNIFORM>
+__global__ __launch_bounds__(256) void combine_kernel(const CombineArgs a, FastDiv row_div, int64_t units) {
   using E = Elem<DT>;
   using Raw = typename E::Raw;
   struct __attribute__((aligned(V * sizeof(Raw)))) Vec {
     Raw v[V];
   };
-  constexpr int JB = 8;
+  constexpr int JB = V == 1 ? 8 : 4;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= units) return;
   const int64_t per = a.n / V;
-  const int64_t tok = row_div.div((uint32_t)i), c = i - tok * per;
+  int64_t tok = row_div.div((uint32_t)i);
+  if (UNIFORM) tok = __builtin_amdgcn_readfirstlane((int)tok);
+  const int64_t c = i - tok * per;
+  const Vec* y = (const Vec*)a.y + tok * a.k * per + c;
+  const int k = (int)a.k;
   float acc[V];
 #pragma unroll
   for (int x = 0; x < V; ++x) acc[x] = 0.f;
@@ -209,20 +274,20 @@ template <int DT, int V> __global__ __launch_bounds__(256) void combine_kernel(c
 #pragma unroll
     for (int x = 0; x < V; ++x) acc[x] = E::get(r.v[x]);
   }
-  const Vec* y = (const Vec*)a.y + tok * a.k * per + c;
-  for (int64_t j0 = 0; j0 < a.k; j0 += JB) {
+  for (int j0 = 0; j0 < k; j0 += JB) {
     Vec r[JB];
     float w[JB];
     bool on[JB];
 #pragma unroll
     for (int j = 0; j < JB; ++j) {
-      on[j] = j0 + j < a.k;
-      if (on[j] && a.ids) {
-        const int64_t id = a.ids[tok * a.k + j0 + j];
-        on[j] = id >= 0 && id < a.e;
+      const int jj = min(j0 + j, k - 1);
+      r[j] = y[jj * per];
+      w[j] = a.weights[tok * k + jj];
+      on[j] = j0 + j < k;
+      if (a.ids) {
+        const int64_t id = a.ids[tok * k + jj];
+        on[j] = on[j] && id >= 0 && id < a.e;
       }
-      w[j] = 0.f;
-      if (on[j]) w[j] = a.weights[tok * a.k + j0 + j], r[j] = y[(j0 + j) * per];
     }
 #pragma unroll
     for (int j = 0; j < JB; ++j)
@@ -240,13 +305,16 @@ template <int DT, int V> __global__ __launch_bounds__(256) void combine_kernel(c
 template <int DT> hipError_t combine(const CombineArgs& a, hipStream_t s) {
   constexpr int V = DT == DT_F32 ? 4 : 8;
   auto whole = [](const void* p) { return (uintptr_t)p % 16 == 0; };
-  if (a.n % V == 0 && whole(a.y) && whole(a.out) && whole(a.residual)) {
-    const int64_t units = a.t * (a.n / V);
-    combine_kernel<DT, V><<<(unsigned)((units + 255) / 256), 256, 0, s>>>(a, fast_div((uint32_t)(a.n / V)), units);
-  } else {
-    const int64_t units = a.t * a.n;
-    combine_kernel<DT, 1><<<(unsigned)((units + 255) / 256), 256, 0, s>>>(a, fast_div((uint32_t)a.n), units);
-  }
+  const bool wide = a.n % V == 0 && whole(a.y) && whole(a.out) && whole(a.residual);
+  const int64_t per = wide ? a.n / V : a.n, units = a.t * per;
+  const unsigned grid = (unsigned)((units + 255) / 256);
+  const FastDiv div = fast_div((uint32_t)per);
+  if (!wide)
+    combine_kernel<DT, 1, false><<<grid, 256, 0, s>>>(a, div, units);
+  else if (per % 64 == 0)
+    combine_kernel<DT, V, true><<<grid, 256, 0, s>>>(a, div, units);
+  else
+    combine_kernel<DT, V, false><<<grid, 256, 0, s>>>(a, div, units);
   return hipGetLastError();
 }
 
