@@ -17,10 +17,6 @@
 #include "attn_common4.hpp"
 #include "attn_few.hpp"
 
-#ifndef QL_IU
-#define QL_IU 2
-#define QL_TH 4
-#endif
 namespace ql {
 namespace {
 
@@ -253,7 +249,9 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few4_kernel(const 
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
   FewRun run;
-  if (!few_run<256, QL_IU, QL_TH>(a, ssh, sfound, run)) return;
+  // An item's start and end take about as long as two tiles: with 0, 2, 3 or 4 units for them 64 ragged
+  // sequences (8 heads, 128 values, 16-slot pages) take 91, 61, 64, 67 us.
+  if (!few_run<256, 2, 4>(a, ssh, sfound, run)) return;
   const int u1 = run.u1, item_units = run.item_units;
   int s = run.s, base = run.base;
 

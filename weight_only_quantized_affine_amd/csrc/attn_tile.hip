@@ -23,6 +23,15 @@
 // 495 us, 1070 TFLOP/s; a large bf16 library product reaches 1219 here.  The same with 64 heads on 16
 // of 64: 206 us, 670 and 639 us, 830; with 16 heads on 4 of 256: 172 us, 800 and 648 us, 820.
 //
+// Over a cache in 4 bits (AttnArgs4) the stages hold fp16 decoded on the way: a copying wave has a tile's codes
+// in registers and decodes a word of them between every two products of the scores, whose matrix instructions
+// leave the vector units free (all of it at the period's end: 1000 tokens at 32767 628 us, 577 so; by all
+// eight waves, half a tile each: 643; at 256 values a head, where the waves are in step, 882 and 757).  13
+// instructions decode a word of 8 values, once for 256 rows.  Measured, groups of 64: 4096 tokens 178 us, 1000
+// tokens at 32767 577 us, 920 TFLOP/s, 64 and 256 values a head 825 and 757 us.  It has the matrix cores'
+// floor over it by a third, since the vector units take a quarter more than for 16 bits.  (Decoding the
+// sequences to a 16-bit copy first would take a workspace four times their cache.)
+//
 // Work split.  With enough items (sequence, kv head, row tile) to fill the chip, one workgroup each,
 // the longest first, kv heads fastest so that a head's tiles run on one XCD and share its L2.  Else
 // all items are laid end to end in units of one row tile x 64 keys and cut into equal runs, one
@@ -108,20 +117,34 @@ template <int BM> __device__ __forceinline__ int row_tiles(const AttnArgs& a, in
   return q.nq < 1 || attn_is_few(a, q.nq) ? 0 : (q.nq * a.g + BM - 1) / BM;
 }
 
-// The 16 cache rows of a tile that one wave copies, over a cache in 4 bits: their codes and words stay in
-// registers while the copies of the 16-bit kernel would be in flight, and the decoded rows (fp16, in each
-// 8 values the order 0 4 1 5 2 6 3 7 in which a word's codes come apart) are written to the stage at the
-// period's end.  Lane l holds a quarter l / 16 of row l % 16: CH chunks of 16 bytes of codes (8 at
-// 64 values), 64 values apart.
-template <int D, int STEP> struct TileDecode {
-  static constexpr int CH = D == 256 ? 2 : 1, W = D == 64 ? 2 : 4;  // chunks, words of a chunk
+// The KEYS cache rows of a tile that one wave copies, over a cache in 4 bits: their codes and words stay in
+// registers until the period's products, between which they are decoded into the stage (fp16, in each 8
+// values the order 0 4 1 5 2 6 3 7 in which a word's codes come apart).  Lane l holds part l / KEYS of row
+// l % KEYS: CH chunks of W words, 8 W PARTS values apart, each within one group.
+template <int D, int STEP, int KEYS> struct TileDecode {
+  static constexpr int PARTS = 64 / KEYS, WORDS = D / 8 / PARTS;  // words of a lane, of K and of V
+  static constexpr int W = WORDS < 4 ? WORDS : 4, CH = WORDS / W;
   int ids, block, id, base;     // as TileCopy
-  int64_t row, prow;            // the lane's row among the codes and words, row -1: not to be seen
+  bool whole;                   // uniform: every row is to be seen and they lie one after the other
+  int64_t first, pfirst;        // uniform, where whole: the first row among the codes and words
+  int64_t row, prow;            // else: the lane's row, row -1: not to be seen
+  uint32_t off, poff;           // the lane's place from the first row
+  int at_k, at_v;               // and in a stage
   uint32_t seen;
-  uint32_t k[CH][W], v[CH][W], kg[CH], vg[CH];
-  int k_tile, v_tile;           // uniform: tile whose rows are in flight, -1: none
+  uint32_t k[WORDS], v[WORDS], kg[CH], vg[CH];
+  int k_tile, v_tile;           // uniform: tile whose rows are in registers, -1: none
 
-  __device__ __forceinline__ void init(const AttnArgs4&, int, int) { k_tile = v_tile = -1; }
+  static __device__ __forceinline__ int value(int lane, int i) { return 8 * W * (PARTS * i + lane / KEYS); }
+  __device__ __forceinline__ void init(const AttnArgs4& a, int row0, int lane) {
+    k_tile = v_tile = -1;
+    for (int i = 0; i < WORDS; ++i) k[i] = v[i] = 0;
+    for (int i = 0; i < CH; ++i) kg[i] = vg[i] = 0;
+    off = (uint32_t)(lane % KEYS) * (uint32_t)a.token_stride;
+    poff = (uint32_t)(lane % KEYS) * (uint32_t)a.p_token_stride;
+    const int r = row0 + lane % KEYS, chunk = W * (lane / KEYS);
+    at_k = r * (D * 2) + (chunk ^ swz_k<D>(r)) * 16;
+    at_v = r * (D * 2) + (chunk ^ swz_v<D>(r)) * 16;
+  }
   __device__ __forceinline__ void lookup(const AttnArgs4& a, const int32_t* table, int first, int lo, int hi, int lane,
                                          bool begins) {
     base = first;
@@ -133,52 +156,56 @@ template <int D, int STEP> struct TileDecode {
         if (p + 16 > lo && p < hi) ids = table[a.page_div.div((uint32_t)p)];
         asm volatile("" : "+v"(ids));  // the wait for the load is here
       }
-      id = __builtin_amdgcn_readlane(ids, (first - block) / STEP);
     } else {
-      const int p = first + (lane & 15);
+      const int p = first + lane % KEYS;
       id = -1;
       if (p >= lo && p < hi) id = table[a.page_div.div((uint32_t)p)];
     }
   }
   __device__ __forceinline__ void resolve(const AttnArgs4& a, int lo, int hi, int lane) {
-    const int p = base + (lane & 15);
-    const int in = p - (int)a.page_div.div((uint32_t)p) * a.page_size;
-    const bool see = p >= lo && p < hi && (uint32_t)id < (uint32_t)a.n_pages;
-    seen = (uint32_t)__ballot(see) & 0xffffu;
-    row = see ? (int64_t)id * a.page_stride + (int64_t)in * a.token_stride : -1;
-    prow = (int64_t)id * a.p_page_stride + (int64_t)in * a.p_token_stride;
+    whole = false;
+    if (a.page16) {
+      const int page = __builtin_amdgcn_readlane(ids, (base - block) / STEP);
+      const int in = base - (int)a.page_div.div((uint32_t)base) * a.page_size;
+      whole = base >= lo && base + KEYS <= hi && (uint32_t)page < (uint32_t)a.n_pages;
+      first = (int64_t)page * a.page_stride + (int64_t)in * a.token_stride;
+      pfirst = (int64_t)page * a.p_page_stride + (int64_t)in * a.p_token_stride;
+      id = page;
+    }
+    seen = (1u << KEYS) - 1;
+    if (!whole) {
+      const int p = base + lane % KEYS;
+      const int in = p - (int)a.page_div.div((uint32_t)p) * a.page_size;
+      const bool see = p >= lo && p < hi && (uint32_t)id < (uint32_t)a.n_pages;
+      seen &= (uint32_t)__ballot(see);
+      row = see ? (int64_t)id * a.page_stride + (int64_t)in * a.token_stride : -1;
+      prow = (int64_t)id * a.p_page_stride + (int64_t)in * a.p_token_stride;
+    }
   }
   // Starts the loads of the lane's part of its row; a row that is not to be seen is zero.
   __device__ __forceinline__ void load(const AttnArgs4& a, const uint8_t* head, const uint8_t* words, int lane,
-                                       uint32_t (*c)[W], uint32_t* group) const {
-    const int part = lane >> 4;
+                                       uint32_t* c, uint32_t* group) const {
+    struct __attribute__((aligned(4 * W))) Chunk {
+      uint32_t w[W];
+    };
+    auto take = [&](const uint8_t* at, uint32_t o, const uint8_t* wat, uint32_t wo) {
 #pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const uint8_t* at = row < 0 ? (const uint8_t*)kZeroRow : head + row;
-      const uint8_t* wat = row < 0 ? (const uint8_t*)kZeroRow : words + prow;
-      const int value = 128 * i + 8 * W * part;
-      if constexpr (W == 2) {
-        const u32x2_t x = *(const u32x2_t*)(at + value / 2);
-        c[i][0] = x[0], c[i][1] = x[1];
-      } else {
-        const u32x4_t x = *(const u32x4_t*)(at + value / 2);
-        for (int y = 0; y < 4; ++y) c[i][y] = x[y];
+      for (int i = 0; i < CH; ++i) {
+        const Chunk x = *(const Chunk*)(at + (o + value(lane, i) / 2));
+        for (int y = 0; y < W; ++y) c[W * i + y] = x.w[y];
+        group[i] = *(const uint32_t*)(wat + (wo + 4 * (value(lane, i) >> a.group_log2)));
       }
-      group[i] = *(const uint32_t*)(wat + 4 * (value >> a.group_log2));
-    }
+    };
+    if (whole)
+      take(head + first, off, words + pfirst, poff);
+    else
+      take(row < 0 ? (const uint8_t*)kZeroRow : head + row, 0, row < 0 ? (const uint8_t*)kZeroRow : words + prow, 0);
   }
-  // Decodes them into the stage.
-  template <bool IS_V>
-  __device__ __forceinline__ void store(uint8_t* stage, int row0, int lane, const uint32_t (*c)[W],
-                                        const uint32_t* group) const {
-    const int r = row0 + (lane & 15), part = lane >> 4;
-#pragma unroll
-    for (int i = 0; i < CH; ++i)
-#pragma unroll
-      for (int y = 0; y < W; ++y) {
-        const int chunk = 16 * i + W * part + y;
-        *(u32x4_t*)(stage + r * (D * 2) + (chunk ^ (IS_V ? swz_v<D>(r) : swz_k<D>(r))) * 16) = values4(c[i][y], group[i]);
-      }
+  // Decodes word x into the stage.
+  template <bool IS_V> __device__ __forceinline__ void store(uint8_t* stage, int x) const {
+    // its chunk is the first of the lane's with other bits set, above and below the part's
+    const int other = (W * PARTS * (x / W) + x % W) * 16;
+    *(u32x4_t*)(stage + ((IS_V ? at_v : at_k) ^ other)) = IS_V ? values4(v[x], vg[x / W]) : values4(k[x], kg[x / W]);
   }
 };
 
@@ -276,7 +303,7 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
   const int late = wave / 4;  // the second four waves run half a tile behind
   const bool copier = wave < 4;
   const int row0 = R * (wave & 3);  // first key of a tile that a copying wave copies
-  std::conditional_t<kDecode, TileDecode<D, BN>, TileCopy<D, R, 1, BN, false>> tc;
+  std::conditional_t<kDecode, TileDecode<D, BN, R>, TileCopy<D, R, 1, BN, false>> tc;
   tc.init(a, row0, lane);
   bool recorded = false;
   for (int u = u0; u < u1;) {
@@ -383,19 +410,27 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
     const int32_t* table = a.table + (int64_t)s * a.table_stride;
     const uint8_t *kw = nullptr, *vw = nullptr;
     if constexpr (kDecode) kw = a.kp + (int64_t)head * a.p_head_stride, vw = a.vp + (int64_t)head * a.p_head_stride;
-    const int n = tb - ta, kfirst = (first + ta) * BN;
+    int n = tb - ta, kfirst = (first + ta) * BN;
+    if constexpr (kDecode) {
+      n = __builtin_amdgcn_readfirstlane(n), kfirst = __builtin_amdgcn_readfirstlane(kfirst);
+      lo = __builtin_amdgcn_readfirstlane(lo), hi = __builtin_amdgcn_readfirstlane(hi);
+    }
     auto stage_k = [&](int t) { return sm + attn_stage<ST>(t) * KB; };
     auto stage_v = [&](int t) { return sm + (ST + attn_stage<ST>(t)) * KB; };
     auto copy_v = [&](int t) {
-      if constexpr (kDecode)
+      if constexpr (kDecode) {
+        asm volatile("" : "+v"(tc.id));  // the wait for the page id of K's rows is here, before there are loads to wait for
         tc.v_tile = t, tc.load(a, vb, vw, lane, tc.v, tc.vg);
-      else
+      } else {
         tc.template copy<true>(tc.now, vb, stage_v(t) + row0 * ROW, row0, lane);
+      }
     };
     auto copied = [&] {  // the wave's copies have arrived
       if constexpr (kDecode) {
-        if (tc.v_tile >= 0) tc.template store<true>(stage_v(tc.v_tile), row0, lane, tc.v, tc.vg);
-        if (tc.k_tile >= 0) tc.template store<false>(stage_k(tc.k_tile), row0, lane, tc.k, tc.kg);
+        if (tc.v_tile >= 0)
+          for (int x = 0; x < tc.WORDS; ++x) tc.template store<true>(stage_v(tc.v_tile), x);
+        if (tc.k_tile >= 0)
+          for (int x = 0; x < tc.WORDS; ++x) tc.template store<false>(stage_k(tc.k_tile), x);
         tc.k_tile = tc.v_tile = -1;
       } else {
         attn_wait_vm<0>();
@@ -405,7 +440,8 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
       tc.resolve(a, lo, hi, lane);
       if (lane == 0) sseen[attn_seen_at(t)][wave & 3] = (uint16_t)tc.seen;
       if constexpr (kDecode) {
-        if (tc.k_tile >= 0) tc.template store<false>(stage_k(tc.k_tile), row0, lane, tc.k, tc.kg);  // an item's first
+        if (tc.k_tile >= 0)  // an item's first
+          for (int x = 0; x < tc.WORDS; ++x) tc.template store<false>(stage_k(tc.k_tile), x);
         tc.k_tile = t, tc.load(a, kb, kw, lane, tc.k, tc.kg);
       } else {
         tc.template copy<false>(tc.now, kb, stage_k(t) + row0 * ROW, row0, lane);
@@ -499,7 +535,20 @@ __global__ __launch_bounds__(64 * attn_tile_waves(D), attn_tile_waves(D) / 4) vo
         else
           sc[(i - NO) % NK] = mfma32(T{}, f[i], qf[(i - NO) / NK], sc[(i - NO) % NK]);
         if (i + kAhead < B) f[i + kAhead] = load(i + kAhead);
+        if constexpr (kDecode) {  // between the scores' products, V of the next tile and K of the one behind
+          constexpr int every = (NP - NO) / (2 * tc.WORDS);
+          if (A < NO && i >= NO && i % every == every / 2 && (WAVES == 4 || copier)) {
+            const int x = (i - NO) / every;
+            if (x < tc.WORDS)
+              tc.template store<true>(stage_v(t + 1), x);
+            else
+              tc.template store<false>(stage_k(t + 2), x - tc.WORDS);
+          }
+        }
         __builtin_amdgcn_sched_barrier(0);
+      }
+      if constexpr (kDecode) {
+        if (A < NO) tc.k_tile = tc.v_tile = -1;
       }
     };
     constexpr std::integral_constant<int, 0> kFirst{};

@@ -9,39 +9,18 @@ namespace ql {
 __device__ __forceinline__ f16x2_t h2(uint32_t w) { return __builtin_bit_cast(f16x2_t, w); }
 __device__ __forceinline__ uint32_t w2(f16x2_t h) { return __builtin_bit_cast(uint32_t, h); }
 
-// The codes of a word as pairs (i, i + 4), i = 0 .. 3, in fp16: a code under the exponent bits of 1024 (its
-// low bits) or of 64 (four bits further up) is 1024 + c or 64 + c, and the difference is exact.
-__device__ __forceinline__ void codes4(uint32_t w, f16x2_t* c) {
-  const f16x2_t k1024 = h2(0x64006400u), k64 = h2(0x54005400u);
-  const uint32_t v = w >> 8;
-  c[0] = h2((w & 0x000f000fu) | 0x64006400u) - k1024;
-  c[1] = h2((w & 0x00f000f0u) | 0x54005400u) - k64;
-  c[2] = h2((v & 0x000f000fu) | 0x64006400u) - k1024;
-  c[3] = h2((v & 0x00f000f0u) | 0x54005400u) - k64;
-}
-// Their values, each rounded to fp16 once: pair i with the scales s[i] and biases b[i].
-__device__ __forceinline__ u32x4_t values4(uint32_t w, const f16x2_t* s, const f16x2_t* b) {
-  f16x2_t c[4];
-  codes4(w, c);
-  u32x4_t r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = w2(__builtin_elementwise_fma(c[i], s[i], b[i]));
-  return r;
-}
-// All with the scale and bias of one group.
+// The values of a word as fp16 pairs (i, i + 4), i = 0 .. 3, each rounded once.  A code under the exponent bits
+// of 1024 (its low bits) or of 64 (four bits further up) is 1024 + c or 64 + c, and the difference is exact.
 __device__ __forceinline__ u32x4_t values4(uint32_t w, uint32_t group) {
   const f16x2_t p = h2(group), s = {p[0], p[0]}, b = {p[1], p[1]};
-  f16x2_t c[4];
-  codes4(w, c);
+  const f16x2_t k1024 = h2(0x64006400u), k64 = h2(0x54005400u);
+  const uint32_t v = w >> 8;
+  const f16x2_t c[4] = {h2((w & 0x000f000fu) | 0x64006400u) - k1024, h2((w & 0x00f000f0u) | 0x54005400u) - k64,
+                        h2((v & 0x000f000fu) | 0x64006400u) - k1024, h2((v & 0x00f000f0u) | 0x54005400u) - k64};
   u32x4_t r;
 #pragma unroll
   for (int i = 0; i < 4; ++i) r[i] = w2(__builtin_elementwise_fma(c[i], s, b));
   return r;
-}
-// Whether some code of the group may stand for a value that fp16 does not hold.
-__device__ __forceinline__ bool odd_group(uint32_t group) {
-  const f16x2_t p = h2(group);
-  return !(__builtin_fabsf((float)p[1]) + 15.f * __builtin_fabsf((float)p[0]) <= 65504.f);
 }
 
 }  // namespace ql
