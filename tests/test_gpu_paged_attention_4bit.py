@@ -386,6 +386,22 @@ def test_cache_past_32_bit_offsets():
     assert torch.equal(small.run(), want)
 
 
+def test_groups_of_a_page_past_32_bits():
+    """The words of a page's 16 slots 300 MB apart (pages and heads next to each other)."""
+    hk, d, page = 2, 128, 16
+    small = Problem([(1, 300), (70, 290), (3, 40)], 8, hk, d, 32, page, BF, seed=15)
+    n_pages, per = small.cache[0].shape[0], 2 * d // 32
+    token, far = 150_000_006, []
+    assert n_pages * hk * per < token and 2 * 15 * token > 1 << 32
+    for x in small.cache[1::2]:
+        buf = torch.empty(15 * token + n_pages * hk * per, dtype=HF, device=DEV)
+        far.append(buf.as_strided(x.shape, (hk * per, token, per, 2, 1)))
+        far[-1].copy_(x)
+    want = small.run()
+    small.cache[1::2] = far
+    assert torch.equal(small.run(), want)
+
+
 def test_no_sequences_no_tokens_no_pages():
     cache = q.qlinear_paged_cache_4bit(2, 4, 2, 64, 32)
     i32 = dict(dtype=torch.int32, device=DEV)

@@ -1028,12 +1028,13 @@ ql_status qlinear_paged_attention_4bit(const ql_heads* q, const ql_heads* out, q
   a.page_stride = cache->page_stride;
   a.token_stride = cache->token_stride;
   a.head_stride = cache->head_stride;
-  a.page16 = cache->page_size % 16 == 0 && a.token_stride < (int64_t(1) << 27);
   a.kp = (const uint8_t*)cache->k_groups;
   a.vp = (const uint8_t*)cache->v_groups;
   a.p_page_stride = 4 * cache->group_page_stride;
   a.p_token_stride = 4 * cache->group_token_stride;
   a.p_head_stride = 4 * cache->group_head_stride;
+  // the places of 16 slots from the first fit in 32 bits
+  a.page16 = cache->page_size % 16 == 0 && a.token_stride < (int64_t(1) << 27) && a.p_token_stride < (int64_t(1) << 27);
   a.group_log2 = cache->group_size == 32 ? 5 : cache->group_size == 64 ? 6 : 7;
   a.io = dt(dtype);
   const hipStream_t s = (hipStream_t)stream;
