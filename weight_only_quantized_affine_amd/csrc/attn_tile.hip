@@ -28,9 +28,11 @@
 // leave the vector units free (all of it at the period's end: 1000 tokens at 32767 628 us, 577 so; by all
 // eight waves, half a tile each: 643; at 256 values a head, where the waves are in step, 882 and 757).  13
 // instructions decode a word of 8 values, once for 256 rows.  Measured, groups of 64: 4096 tokens 178 us, 1000
-// tokens at 32767 577 us, 920 TFLOP/s, 64 and 256 values a head 825 and 757 us.  It has the matrix cores'
-// floor over it by a third, since the vector units take a quarter more than for 16 bits.  (Decoding the
-// sequences to a 16-bit copy first would take a workspace four times their cache.)
+// tokens at 32767 577 us, 920 TFLOP/s, 64 and 256 values a head 825 and 757 us: a sixth more than from 16 bits,
+// for the vector units' share.  (Decoding the sequences to a 16-bit copy first would take a workspace four
+// times their cache.)  A decoded value rounds to fp16, which a matrix operand is: 2^-11 of it at most, where
+// the code itself stands for its value to some hundredths; fp16 outputs are then off by 0.0005 of their size,
+// where their own rounding is 0.0002 (bf16 outputs by their rounding, 0.0017).
 //
 // Work split.  With enough items (sequence, kv head, row tile) to fill the chip, one workgroup each,
 // the longest first, kv heads fastest so that a head's tiles run on one XCD and share its L2.  Else

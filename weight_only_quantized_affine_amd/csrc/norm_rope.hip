@@ -16,7 +16,11 @@
 //
 // Append to a cache in 4 bits: the rows of k (in 64 bits up to their rounding, since a code hangs on the last
 // bits) and of v are quantized where they are, 8 values and one word of codes a lane, a group's
-// smallest and largest value by DPP within its 4, 8 or 16 lanes.
+// smallest and largest value by DPP within its 4, 8 or 16 lanes.  Rows of k and v are taken token after token of
+// one head, so that neighbouring groups of lanes write neighbouring rows of a head-major page (head after
+// head: 4096 tokens 41 us, so 25).  Measured (bf16, 32 + 8 + 8 heads of 128, groups of 64): 64 tokens of 16 + 8 + 8
+// heads 4.4 us, 4096 tokens 25 us, 3.5 TB/s (17 of it memory, the rest the rows' work on the vector units);
+// reading 4096 tokens back 7.8 us.
 #include "head_common.hpp"
 
 namespace ql {

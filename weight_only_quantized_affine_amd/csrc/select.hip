@@ -16,7 +16,12 @@ namespace {
 // one token of ten thousand), and the vector units run fp64 at the rate of fp32 here.
 //
 // One wave a token, EPL neighbouring experts a lane, so that the lowest lane with the largest c holds the
-// lowest index: a round takes the lane's largest, the wave's by DPP, and a ballot.
+// lowest index: a round takes the lane's largest, the wave's by DPP, and a ballot.  Rounds compare fp32 keys and
+// look at 64 bits only where more than one lane has the largest.
+//
+// Measured: one token of 128 experts 4.2 us; 8192 tokens of 256 experts, sigmoid, 4 of 8 groups, 8 chosen, 18 us
+// against 2 of memory: bound by the vector units (four exponentials and inverses a lane in 64 bits, 260
+// instructions, and the rounds) and by the chain of each round.
 
 constexpr double kLowest = -1.7976931348623157e308;  // c of -infinity or NaN
 constexpr double kOut = -__builtin_inf();            // not to be chosen (again)
@@ -228,7 +233,8 @@ template <int EPL> __global__ __launch_bounds__(256) void select_kernel(const Se
 // ---------------------------------------------------------------- the combination
 //
 // out = residual + sum_j w_j y_j: k + 2 rows of memory traffic for k products a value, so memory bounds it.
-// A thread holds 16 bytes of a row and has the loads of all its token's positions in flight.
+// A thread holds 16 bytes of a row and has the loads of four positions in flight, ids or not (a load that waits
+// for its id: 4096 tokens of 8 x 4096 values 86 us, so 63, 5.3 TB/s; 16 tokens of 4 3.2 us).
 
 template <int DT> struct Elem;
 template <> struct Elem<DT_F32> {
