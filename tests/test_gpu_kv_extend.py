@@ -168,3 +168,14 @@ def test_a_captured_step_runs_on():
         host = (stack, 200)
         got = [x.tolist() for x in (bufs["cu_q"], bufs["positions"], bufs["slots"], lens, table, bufs["info"])]
         assert got == [cu, pos, slots, state[0], state[1], info] and free[:int(fc)].tolist() == stack
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("rows", [4000, 30000])
+def test_more_sequences_than_shared_memory_holds(in_place, rows):
+    r = np.random.default_rng(5)
+    counts = [int(x) for x in r.integers(-1, 2 if rows == 4000 else 6, 6001)]
+    if rows == 4000:
+        counts = [c if i % 3 else min(c, 0) for i, c in enumerate(counts)]
+    info = Step(counts, [int(x) for x in r.integers(0, 40, 6001)], 8, rows).run(in_place)
+    assert info[2] == 0 and info[0] > rows // 4
