@@ -578,32 +578,38 @@ def _paged_cache4(c: _PagedCache4, cache, d: Optional[int], device: int):
     if len(cache) != 4:
         raise QLError(2, "cache must be (k_codes, k_groups, v_codes, v_groups)")
     kc, kg, vc, vg = cache
-    if any(x.dtype is not torch.int32 for x in (kc, vc)) or any(x.dtype is not torch.float16 for x in (kg, vg)):
+    i32, f16 = torch.int32, torch.float16
+    if kc.dtype is not i32 or vc.dtype is not i32 or kg.dtype is not f16 or vg.dtype is not f16:
         raise QLError(3, "the cache's codes must be int32 and its groups float16")
     shape, groups = kc.shape, kg.shape
     if len(shape) != 4 or vc.shape != shape or (d is not None and shape[3] * 8 != d):
         raise QLError(2, f"the codes must both be [n_pages, page_size, heads, {d}/8]")
+    n_pages, page_size, heads, words = shape
     if len(groups) != 5 or vg.shape != groups or groups[:3] != shape[:3] or groups[3] < 1 or groups[4] != 2 or \
-            shape[3] * 8 % groups[3]:
+            words * 8 % groups[3]:
         raise QLError(2, f"the groups must both be {list(shape[:3])} + [groups of a row, 2]")
-    for a, b, inner, name in ((kc, vc, 1, "codes"), (kg, vg, 2, "groups")):
-        sa, sb = a.stride(), b.stride()
-        if sa != sb and any(x != y for x, y, n in zip(sa, sb, a.shape) if n > 1):
-            raise QLError(2, f"the {name} of k and v must have the same strides")
-        want = (1,) if inner == 1 else (2, 1)
-        if any(x != y for x, y, n in zip(sa[-inner:], want, a.shape[-inner:]) if n > 1):
-            raise QLError(2, f"the last dimension{'s' if inner > 1 else ''} of the {name} must be contiguous")
-    for x, name in zip(cache, ("k_codes", "k_groups", "v_codes", "v_groups")):
-        _same_device(x, name, device)
-    c.k_codes, c.k_groups, c.v_codes, c.v_groups = (x.data_ptr() for x in cache)
-    c.n_pages, c.page_size, c.hk, c.d = shape[0], shape[1], shape[2], shape[3] * 8
-    c.group_size = c.d // groups[3]
-    sk, sg = kc.stride(), kg.stride()
-    c.page_stride, c.token_stride, c.head_stride = (4 * x if n > 1 else 0 for x, n in zip(sk, shape[:3]))
-    steps = [x if n > 1 else 0 for x, n in zip(sg, shape[:3])]
-    if any(x % 2 for x in steps):
+    sk, sg, sv, sw = kc.stride(), kg.stride(), vc.stride(), vg.stride()
+    if sk != sv or sg != sw:
+        for a, b, x, name in ((sk, sv, shape, "codes"), (sg, sw, groups, "groups")):
+            if any(i != j for i, j, n in zip(a, b, x) if n > 1):
+                raise QLError(2, f"the {name} of k and v must have the same strides")
+    if sk[3] != 1 and words > 1:
+        raise QLError(2, "the last dimension of the codes must be contiguous")
+    if sg[4] != 1 or (sg[3] != 2 and groups[3] > 1):
+        raise QLError(2, "the last dimensions of the groups must be contiguous")
+    if not (kc.get_device() == kg.get_device() == vc.get_device() == vg.get_device() == device):
+        for x, name in zip(cache, ("k_codes", "k_groups", "v_codes", "v_groups")):
+            _same_device(x, name, device)
+    c.k_codes, c.k_groups, c.v_codes, c.v_groups = kc.data_ptr(), kg.data_ptr(), vc.data_ptr(), vg.data_ptr()
+    c.n_pages, c.page_size, c.hk, c.d = n_pages, page_size, heads, words * 8
+    c.group_size = words * 8 // groups[3]
+    # the stride of a dimension of one is free in torch
+    p, t, h = sk[0] if n_pages > 1 else 0, sk[1] if page_size > 1 else 0, sk[2] if heads > 1 else 0
+    c.page_stride, c.token_stride, c.head_stride = 4 * p, 4 * t, 4 * h
+    p, t, h = sg[0] if n_pages > 1 else 0, sg[1] if page_size > 1 else 0, sg[2] if heads > 1 else 0
+    if (p | t | h) & 1:
         raise QLError(4, "the strides of the groups must be whole words")
-    c.group_page_stride, c.group_token_stride, c.group_head_stride = (x // 2 for x in steps)
+    c.group_page_stride, c.group_token_stride, c.group_head_stride = p >> 1, t >> 1, h >> 1
 
 
 def _norm_rope(n: _NormRope, t: int, d: int, q_weight, k_weight, eps, positions, cos_sin, interleaved, device: int):
