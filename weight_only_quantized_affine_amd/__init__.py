@@ -540,6 +540,14 @@ def _array(x, name: str, dtype, shape, device: int):
     return x.data_ptr()
 
 
+def _result(x, name: str, dtype, shape, like, device: int):
+    """An output and its pointer: x, checked, or a new tensor where like is."""
+    if x is None:
+        x = _torch().empty(shape, dtype=dtype, device=like.device)
+        return x, x.data_ptr()
+    return x, _array(x, name, dtype, shape, device)
+
+
 def _paged_cache(c: _PagedCache, k_cache, v_cache, d: int, dtype, device: int):
     shape = k_cache.shape
     if len(shape) != 4 or v_cache.shape != shape or shape[3] != d:
@@ -863,7 +871,7 @@ def qlinear_kv_extend(counts, lens, block_table, *, page_size: int, rows: int, f
     free_count_out are given.  A step that cannot be done changes nothing (see qlinear.h for why)."""
     torch = _torch()
     lib = load_library()
-    device, i32 = counts.get_device(), dict(dtype=torch.int32, device=counts.device)
+    device, i32, i64 = counts.get_device(), torch.int32, torch.int64
     if counts.dim() != 1:
         raise QLError(2, "counts must be [n_seqs]")
     n_seqs, max_pages, row = _block_table(block_table, device)
@@ -872,22 +880,17 @@ def qlinear_kv_extend(counts, lens, block_table, *, page_size: int, rows: int, f
         if free_pages.dim() != 1:
             raise QLError(2, "free_pages must be [entries]")
         cap = free_pages.shape[0]
-    lens_out = lens if lens_out is None else lens_out
-    free_count_out = free_count if free_count_out is None else free_count_out
-    cu_q = torch.empty(n_seqs + 1, **i32) if cu_q is None else cu_q
-    info = torch.empty(4, **i32) if info is None else info
-    if positions is None:
-        positions = torch.empty(rows, dtype=torch.int64, device=counts.device)
-    if slots is None:
-        slots = torch.empty(rows, dtype=torch.int64, device=counts.device)
-    at = [_array(x, name, torch.int32, (n,), device)
-          for x, name, n in ((counts, "counts", n_seqs), (lens, "lens", n_seqs), (lens_out, "lens_out", n_seqs),
-                             (free_pages, "free_pages", cap), (free_count, "free_count", 1),
-                             (free_count_out, "free_count_out", 1), (cu_q, "cu_q", n_seqs + 1), (info, "info", 4))]
-    pos_at, slots_at = (_array(x, name, torch.int64, (rows,), device)
-                        for x, name in ((positions, "positions"), (slots, "slots")))
-    status = lib.qlinear_kv_extend(at[0], at[1], n_seqs, block_table.data_ptr(), row, max_pages, page_size, at[3], cap, at[4],
-                                   at[2], at[5], at[6], pos_at, slots_at, rows, at[7], _stream_on(device))
+    counts_at, lens_at = _array(counts, "counts", i32, (n_seqs,), device), _array(lens, "lens", i32, (n_seqs,), device)
+    list_at, count_at = _array(free_pages, "free_pages", i32, (cap,), device), _array(free_count, "free_count", i32, (1,), device)
+    lens_out_at = lens_at if lens_out is None else _array(lens_out, "lens_out", i32, (n_seqs,), device)
+    count_out_at = count_at if free_count_out is None else _array(free_count_out, "free_count_out", i32, (1,), device)
+    cu_q, cu_at = _result(cu_q, "cu_q", i32, (n_seqs + 1,), counts, device)
+    positions, pos_at = _result(positions, "positions", i64, (rows,), counts, device)
+    slots, slots_at = _result(slots, "slots", i64, (rows,), counts, device)
+    info, info_at = _result(info, "info", i32, (4,), counts, device)
+    status = lib.qlinear_kv_extend(counts_at, lens_at, n_seqs, block_table.data_ptr(), row, max_pages, page_size, list_at, cap,
+                                   count_at, lens_out_at, count_out_at, cu_at, pos_at, slots_at, rows, info_at,
+                                   _stream_on(device))
     if status:
         _check(status)
     return cu_q, positions, slots, info
@@ -909,16 +912,13 @@ def qlinear_select_experts(logits, k: int, *, sigmoid: bool = False, bias=None, 
     row, place = logits.stride()
     if place != 1 and e > 1:
         raise QLError(2, "the rows of logits must be contiguous")
-    if ids is None:
-        ids = torch.empty((t, k), dtype=torch.int64, device=logits.device)
-    if weights is None:
-        weights = torch.empty((t, k), dtype=torch.float32, device=logits.device)
+    ids, ids_at = _result(ids, "ids", torch.int64, (t, k), logits, device)
+    weights, weights_at = _result(weights, "weights", torch.float32, (t, k), logits, device)
     status = lib.qlinear_select_experts(logits.data_ptr(), _dt(logits), t, e, row if t > 1 else e,
                                         _array(bias, "bias", torch.float32, (e,), device), 1 if sigmoid else 0, n_groups,
                                         top_groups, group_top, k, 1 if renormalize else 0, scale,
-                                        _array(n_rows, "n_rows", torch.int32, (1,), device),
-                                        _array(ids, "ids", torch.int64, (t, k), device),
-                                        _array(weights, "weights", torch.float32, (t, k), device), _stream_on(device))
+                                        _array(n_rows, "n_rows", torch.int32, (1,), device), ids_at, weights_at,
+                                        _stream_on(device))
     if status:
         _check(status)
     return ids, weights
@@ -934,13 +934,12 @@ def qlinear_combine_experts(y, weights, *, ids=None, e: int = 0, residual=None, 
         raise QLError(2, "weights must be [tokens, k] and y [tokens * k, n]")
     (t, k), n = weights.shape, y.shape[1]
     device = y.get_device()
-    if out is None:
-        out = torch.empty((t, n), dtype=y.dtype, device=y.device)
+    out, out_at = _result(out, "out", y.dtype, (t, n), y, device)
     status = lib.qlinear_combine_experts(_array(y, "y", y.dtype, (t * k, n), device), _dt(y),
                                          _array(weights, "weights", torch.float32, (t, k), device),
                                          _array(ids, "ids", torch.int64, (t, k), device), e,
-                                         _array(residual, "residual", y.dtype, (t, n), device), t, k, n,
-                                         _array(out, "out", y.dtype, (t, n), device), _stream_on(device))
+                                         _array(residual, "residual", y.dtype, (t, n), device), t, k, n, out_at,
+                                         _stream_on(device))
     if status:
         _check(status)
     return out
