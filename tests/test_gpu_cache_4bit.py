@@ -231,3 +231,23 @@ def test_nothing_to_do():
     s = torch.arange(3, device=DEV)
     q.qlinear_kv_append_4bit(x, x, empty, s)
     assert (q.qlinear_kv_read_4bit(empty, s)[1] == 0).all()
+
+
+@pytest.mark.parametrize("magnitude,eps", [(1e25, 1e-6), (3e37, 0.0), (1e-25, 0.0), (1e-25, 1e-6), (1e-38, 0.0), (2.0 ** -126, 1e-30)])
+@pytest.mark.parametrize("rot", [0, 128])
+def test_norm_of_rows_whose_squares_leave_fp32(magnitude, eps, rot):
+    """bf16 rows of k with squares past fp32's range on either side: in 64 bits they are ordinary rows."""
+    t, hk, d, group = 9, 2, 128, 64
+    g = torch.Generator().manual_seed(17)
+    k = (torch.randn(t, hk, d, generator=g).double() * magnitude).to(BF)
+    k[1, :, 1:] = 0  # one value alone
+    k[2, :, ::2] = k[2, :, ::2] * 2.0 ** -8
+    k, v = k.to(DEV), torch.randn(t, hk, d, generator=g).to(BF).to(DEV)
+    w, cs = (1 + 0.3 * torch.randn(d, generator=g)).to(DEV), table(16, rot) if rot else None
+    slots, pos = torch.arange(t, device=DEV), torch.arange(t, device=DEV) if rot else None
+    cache = new_cache(1, 16, hk, d, group, "heads")
+    before = host(cache)
+    q.qlinear_kv_append_4bit(k, v, cache, slots, k_weight=w, eps=eps, positions=pos, cos_sin=cs)
+    rows = D.stored_rows(f64(k), f64(w), float(np.float32(eps)), np.arange(t), f64(cs) if rot else None, False, "bf16")
+    assert np.isfinite(rows).all() and np.abs(rows).max() < 32
+    check((magnitude, eps), cache, before, range(t), rows, f64(v).astype(np.float32), group)

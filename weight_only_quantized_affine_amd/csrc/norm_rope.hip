@@ -335,7 +335,7 @@ __device__ __forceinline__ void quantized_row(const Append4Args& a, int64_t tok,
       if (on) weights8(a.k_weight, a.wdt, c, w);
       double ss = 0.;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss += (double)(f[j] * f[j]);  // 22 bits: exact
+      for (int j = 0; j < 8; ++j) ss = __builtin_fma((double)f[j], (double)f[j], ss);  // exact squares: bf16's leave fp32
       const double r = rsqrt64(__builtin_fma(group_sum<L>(ss), a.inv_d, (double)a.eps));
 #pragma unroll
       for (int j = 0; j < 8; ++j) y[j] = y[j] * r * w[j];
