@@ -1,0 +1,77 @@
+"""How exact the few-row 4-bit attention is, against the definition in 64 bits: its root mean square error over many
+outputs is that of its stated roundings, so that a sum which loses more shows, however far below the largest
+error that the roundings allow.
+
+With weights w_j (they sum to one), v_j = s_j (c_j - 8) + m_j, m_j = b_j + 8 s_j, f = 2^-11 and h half a step of out's
+type relative to the value, an output o errs by
+  w_j s_j    rounds once to fp16 in its product with c_j - 8:                f w_j |s_j (c_j - 8)|
+  w_j        rounds once to fp16 in its product with m_j and in the sum of the weights:       f w_j |m_j - o|
+  o          rounds once:                                                    h |o|
+each at most so, independent of the others, and spread evenly over their range: a third of the squares on average.
+Sums: a product of the matrix cores takes a subnormal half as if its exponent were that of the smallest normal one, 2^-14,
+and drops what lies below 2^-24 of the largest term so taken.  Codes are subnormal, c 2^-24, so that a product over 32
+keys loses at most 2^-24 2^10 of its largest w_j s_j: the sum of these is counted whole, and the same, of
+|q_i| s_j, for each of a row's d / 32 products of a score.
+"""
+import numpy as np
+import pytest
+import torch
+
+import weight_only_quantized_affine_amd as q
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF, HF = torch.bfloat16, torch.float16
+F = 2.0 ** -11
+LOST = 2.0 ** -14
+
+
+def parts(words, params):
+    """Codes, scales and biases of rows [.., d / 8], each [.., d] in 64 bits."""
+    c = ((words[..., None] >> (4 * torch.arange(8, device=DEV))) & 15).flatten(-2).double()
+    s, b = (params[..., i].double().repeat_interleave(c.shape[-1] // params.shape[-2], -1) for i in (0, 1))
+    return c, s, b
+
+
+def row(p, cache, pages, n, scale):
+    """One kv head's n positions and its query rows p [rows, d] -> outputs and their mean square error."""
+    kc, ks, kb = (x.flatten(0, 1)[:n] for x in parts(cache[0][pages], cache[1][pages]))
+    c, s, b = (x.flatten(0, 1)[:n] for x in parts(cache[2][pages], cache[3][pages]))
+    x = p @ (kc * ks + kb).T * scale
+    w = x.softmax(-1)
+    o = w @ (c * s + b)
+    e = scale * LOST * p.abs().amax(-1, keepdim=True) * ks.amax() * (p.shape[1] // 32) + 64 * 2.0 ** -24 * x.abs().amax(-1, keepdim=True)
+    m = b + 8 * s
+    w2 = w * w
+    spread = lambda y: w2 @ (y * y) - 2 * (w2 @ y) * o + w2.sum(-1, keepdim=True) * o * o  # noqa: E731  sum w^2 (y - o)^2
+    var = F * F / 3 * (w2 @ (s * (c - 8)) ** 2 + spread(m)) + e * e * spread(c * s + b)
+    pad = torch.nn.functional.pad(w, (0, -n % 32)).unflatten(-1, (-1, 32)).amax(-1)  # 32 keys' largest weight
+    return o, var, LOST * s.amax() * pad.sum(-1, keepdim=True).expand_as(o)
+
+
+@pytest.mark.parametrize("d,group,tokens,q_scale", [(128, 64, 1, 1.0), (128, 64, 1, 4.0), (64, 32, 1, 1.0), (128, 128, 1, 1.0), (64, 64, 1, 1.0),
+                                                    (256, 128, 1, 1.0), (256, 32, 1, 1.0), (128, 32, 1, 1.0), (128, 64, 5, 1.0)])
+@pytest.mark.parametrize("n", [500, 16000])
+def test_errors_are_those_of_the_roundings(d, group, tokens, q_scale, n):
+    seqs, hk, g, page, scale = 4, 4, 4, 16, d ** -0.5
+    gen = torch.Generator(device=DEV).manual_seed(n + d)
+    per = -(-n // page)
+    cache = q.qlinear_paged_cache_4bit(per * seqs, page, hk, d, group)
+    k, v = (torch.randn(per * seqs * page, hk, d, generator=gen, device=DEV).to(HF) for _ in range(2))
+    q.qlinear_kv_append_4bit(k, v, cache, torch.arange(per * seqs * page, device=DEV))
+    table = torch.arange(per * seqs, device=DEV, dtype=torch.int32).view(seqs, per)
+    cu = torch.arange(seqs + 1, device=DEV, dtype=torch.int32) * tokens
+    x = (torch.randn(seqs * tokens, hk * g, d, generator=gen, device=DEV) * q_scale).to(HF)
+    out = q.qlinear_paged_attention_4bit(x, cache, table, cu, torch.full((seqs,), n, device=DEV, dtype=torch.int32), max_q=tokens)
+    err = stat = lost = 0.0
+    for s in range(seqs):
+        for i in range(tokens):
+            for h in range(hk):
+                rows = x[s * tokens + i, h * g:(h + 1) * g].double()
+                o, var, low = row(rows, [y[:, :, h] for y in cache], table[s].long(), n - tokens + i + 1, scale)
+                got = out[s * tokens + i, h * g:(h + 1) * g].double()
+                err += float((got - o).pow(2).sum())
+                stat += float((var + (torch.finfo(HF).eps / 2) ** 2 / 3 * o * o).sum())
+                lost += float(low.pow(2).sum())
+    # thousands of outputs: their mean square is within a tenth of its expectation
+    assert np.sqrt(err) <= 1.1 * np.sqrt(stat) + np.sqrt(lost), (np.sqrt(err), np.sqrt(stat), np.sqrt(lost))
