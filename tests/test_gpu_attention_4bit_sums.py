@@ -75,3 +75,43 @@ def test_errors_are_those_of_the_roundings(d, group, tokens, q_scale, n):
                 lost += float(low.pow(2).sum())
     # thousands of outputs: their mean square is within a tenth of its expectation
     assert np.sqrt(err) <= 1.1 * np.sqrt(stat) + np.sqrt(lost), (np.sqrt(err), np.sqrt(stat), np.sqrt(lost))
+
+
+@pytest.mark.parametrize("d,group", [(64, 32), (64, 64), (128, 32), (128, 64), (128, 128), (256, 32), (256, 64), (256, 128)])
+@pytest.mark.parametrize("tokens,n", [(1, 700), (4, 300), (40, 300)])
+@pytest.mark.parametrize("large", [64.0, 4096.0])
+def test_biases_meet_the_whole_sum_of_a_row(d, group, tokens, n, large):
+    """Queries whose values nearly cancel in each group, over keys that are their biases alone (scale 0): a score is a
+    small sum of large values times a bias, every term and partial sum of it exact in fp32.  What is left is the scores' own
+    scaling and exponential, |score| (2^-22 + 2^-24) and 2^-22, and the roundings of weights, values and output."""
+    hk, g, page, scale = 2, 2, 16, 0.25
+    gen = torch.Generator(device=DEV).manual_seed(d + group + n)
+    per = -(-n // page)
+    cache = q.qlinear_paged_cache_4bit(per, page, hk, d, group)
+    k, v = torch.zeros(per * page, hk, d, device=DEV), torch.randn(per * page, hk, d, generator=gen, device=DEV)
+    bias = torch.randint(-48, 49, (per * page, hk, d // group, 1), generator=gen, device=DEV) / 8
+    k = (k.unflatten(-1, (-1, group)) + bias).flatten(-2).to(BF)  # exact
+    q.qlinear_kv_append_4bit(k, v.to(BF), cache, torch.arange(per * page, device=DEV))
+    assert torch.equal(cache[1][..., 0], torch.zeros_like(cache[1][..., 0]))
+    sign = torch.tensor([1.0, -1.0], device=DEV).repeat(group // 2)
+    x = torch.zeros(tokens, hk * g, d // group, group, device=DEV) + large * sign
+    # one pair of a group holds other values: what the group sums to
+    x[..., 6] = torch.randint(64, 255, x.shape[:3], generator=gen, device=DEV) / 128
+    x[..., 11] = torch.randint(-255, -64, x.shape[:3], generator=gen, device=DEV) / 256
+    x = x.flatten(-2).to(BF)
+    table = torch.arange(per, device=DEV, dtype=torch.int32)[None]
+    cu, lens = (torch.tensor(y, device=DEV, dtype=torch.int32) for y in ([0, tokens], [n]))
+    out = q.qlinear_paged_attention_4bit(x, cache, table, cu, lens, max_q=tokens, scale=scale)
+    for i in range(tokens):
+        m = n - tokens + i + 1
+        for h in range(hk):
+            kc, ks, kb = (y.flatten(0, 1)[:m] for y in parts(cache[0][:, :, h], cache[1][:, :, h]))
+            c, s, b = (y.flatten(0, 1)[:m] for y in parts(cache[2][:, :, h], cache[3][:, :, h]))
+            sc = x[i, h * g:(h + 1) * g].double() @ kb.T * scale
+            w = sc.softmax(-1)
+            o, big = w @ (c * s + b), w @ (c * s + b).abs()
+            e = sc.abs().amax(-1, keepdim=True) * (2.0 ** -22 + 2.0 ** -24) * 2 + 2.0 ** -22
+            # 16-bit roundings: a weight and a value (or w s and w), the sum's weights; a code's sum, a third as much
+            tol = 3 * F * (big + 8 * (w @ s)) * (1 + F) + (F + torch.finfo(BF).eps / 2) * o.abs() + 2 * e * big + 2 * (m + 8) * 2.0 ** -24 * big + 2.0 ** -24
+            bad = (out[i, h * g:(h + 1) * g].double() - o).abs() > tol
+            assert not bad.any(), (i, h, float((out[i, h * g:(h + 1) * g].double() - o).abs().max()), float(tol.max()))

@@ -311,7 +311,10 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few4_kernel(const 
     const int g = lane >> 4, col = lane & 15;
     // The wave's queries: column c of tile n is row 16 n + c; a lane holds the values that meet its part
     // of the keys' rows, word by word; and, for the keys' biases, the sums of each group's values as two fp16
-    // numbers a group (four groups a lane; every lane group takes part, with its share of the sum).
+    // numbers a group (four groups a lane; every lane group takes part, with its share of the sum), held 2^16 times
+    // larger than the codes' products: both together keep 22 bits, or 2^-29 of the row's largest value (at the
+    // products' size the second one would be subnormal and keep 2^-13 of that; taking the 2^16 out costs 62.2 -> 63.2
+    // us of 64 ragged sequences).
     u32x4_t qf[NC][GP * WPL];
     u32x4_t qb[NC];
     int qpos[NC];
@@ -349,7 +352,7 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few4_kernel(const 
           qf[n][x] = w;
       }
 #pragma unroll
-      for (int x = 0; x < GP; ++x) qs[x] = join32(join16(qs[x], SumF()), SumF()) * (GP == 8 ? 0x1p-25f : 0x1p-26f);
+      for (int x = 0; x < GP; ++x) qs[x] = join32(join16(qs[x], SumF()), SumF()) * (GP == 8 ? 0x1p-9f : 0x1p-10f);
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         float v = x < GP ? qs[x % GP] : 0.f;
@@ -456,7 +459,8 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attn_few4_kernel(const 
           for (int r = 0; r < 4; ++r) {
             const float ks = (float)h2(w[x][r])[0];
 #pragma unroll
-            for (int n = 0; n < NC; ++n) sc[n][kt][r] = __builtin_fmaf(ks, acc[n][x][r], sc[n][kt][r]);
+            for (int n = 0; n < NC; ++n)
+              sc[n][kt][r] = __builtin_fmaf(ks, acc[n][x][r], x == 0 ? sc[n][kt][r] * 0x1p-16f : sc[n][kt][r]);
           }
         __builtin_amdgcn_sched_barrier(0);  // one key tile at a time: its words and sums fit in the registers
       }
