@@ -497,7 +497,7 @@ ql_status qlinear_select_experts(const void* logits, ql_dtype dtype, int64_t t, 
  * qlinear_apply_experts with a token's k positions side by side), weights fp32 [t, k] and residual [t, n] or NULL,
  *   out[i, :] = residual[i, :] + sum_j weights[i, j] y[i * k + j, :]
  * in fp32, residual first and j in order, rounded once.  Where ids (int64 [t, k], or NULL) lies outside [0, e) the
- * position adds nothing, whatever y and weights hold.  y, residual and out share dtype (any ql_dtype) and are
+ * position adds nothing, whatever y and weights hold; e >= 1 with ids.  y, residual and out share dtype (any ql_dtype) and are
  * contiguous, aligned to their type; out may be residual and overlaps nothing else.  1 <= k <= 64. */
 ql_status qlinear_combine_experts(const void* y, ql_dtype dtype, const float* weights, const int64_t* ids, int64_t e,
                                   const void* residual, int64_t t, int64_t k, int64_t n, void* out, void* stream);

@@ -195,6 +195,20 @@ def test_combine_refusals(lib):
     assert combine(t=0, y=None) == OK and combine(n=0, out=None) == OK
 
 
+def test_combine_takes_ids_only_with_their_number(lib):
+    """Without e every id would lie outside [0, e) and no expert be counted."""
+    args = lambda ids, e, t=3, n=64: (FAKE, BF16, FAKE, ids, e, None, t, 2, n, FAKE, None)  # noqa: E731
+    for t, n in ((3, 64), (0, 64), (3, 0)):
+        assert lib.qlinear_combine_experts(*args(FAKE, 0, t, n)) == SHAPE
+        assert b"e must be >= 1" in lib.qlinear_last_error()
+    assert lib.qlinear_combine_experts(*args(None, 0, 0)) == OK
+    assert lib.qlinear_combine_experts(*args(FAKE, 1, 0)) == OK
+    for t in (0, 2):
+        y, w, ids = torch.zeros(t * 2, 8), torch.zeros(t, 2), torch.zeros(t, 2, dtype=torch.int64)
+        with pytest.raises(q.QLError, match="must be given with ids"):
+            q.qlinear_combine_experts(y, w, ids=ids, residual=torch.zeros(t, 8))
+
+
 def test_binding_refuses_wrong_tensors():
     bf, i32 = torch.bfloat16, dict(dtype=torch.int32)
     k = torch.zeros(2, 4, 64, dtype=bf)

@@ -927,11 +927,13 @@ def qlinear_select_experts(logits, k: int, *, sigmoid: bool = False, bias=None, 
 def qlinear_combine_experts(y, weights, *, ids=None, e: int = 0, residual=None, out=None):
     """residual [t, n] + the sum of y's k rows of each token (y [t * k, n], as qlinear_apply_experts gives them)
     times weights (fp32 [t, k]) -> out [t, n] in y's dtype.  Positions whose id (int64 [t, k]) lies outside
-    [0, e) add nothing.  out may be residual."""
+    [0, e) add nothing: ids and e, the number of experts, are given together.  out may be residual."""
     torch = _torch()
     lib = load_library()
     if weights.dim() != 2 or y.dim() != 2:
         raise QLError(2, "weights must be [tokens, k] and y [tokens * k, n]")
+    if ids is not None and e < 1:
+        raise QLError(2, "e, the number of experts, must be given with ids")
     (t, k), n = weights.shape, y.shape[1]
     device = y.get_device()
     out, out_at = _result(out, "out", y.dtype, (t, n), y, device)

@@ -1196,6 +1196,7 @@ ql_status qlinear_combine_experts(const void* y, ql_dtype dtype, const float* we
   const char* fn = "qlinear_combine_experts";
   CHECK(is_out(dtype), QL_ERR_DTYPE, "%s: dtype must be QL_F32, QL_F16 or QL_BF16", fn);
   CHECK(t >= 0 && n >= 0 && e >= 0, QL_ERR_SHAPE, "%s: t, n and e must be >= 0", fn);
+  CHECK(!ids || e >= 1, QL_ERR_SHAPE, "%s: e must be >= 1 with ids", fn);
   CHECK(k >= 1 && k <= 64, QL_ERR_SHAPE, "%s: k=%lld must be in [1, 64]", fn, (long long)k);
   if (t == 0 || n == 0) return ok();
   CHECK(t < (int64_t(1) << 31) && n < (int64_t(1) << 31) && t * n < (int64_t(1) << 31) - 256, QL_ERR_UNSUPPORTED,
