@@ -179,3 +179,17 @@ def test_more_sequences_than_shared_memory_holds(in_place, rows):
         counts = [c if i % 3 else min(c, 0) for i, c in enumerate(counts)]
     info = Step(counts, [int(x) for x in r.integers(0, 40, 6001)], 8, rows).run(in_place)
     assert info[2] == 0 and info[0] > rows // 4
+
+
+def test_a_list_without_entries():
+    """An empty tensor of free pages is a list that gives nothing and takes nothing, not the absence of one."""
+    for counts, lens, why in (([1, 0], [3, 4], 0), ([1, 0], [4, 4], 2), ([-1, 0], [0, 4], 0), ([-1, 0], [3, 4], 8)):
+        step = Step(counts, lens, 4, 2, spare=0)
+        step.free, step.cap = [], 0
+        assert step.run()[2] == why and step.run(in_place=True)[2] == why
+    table, free = i32([[0, 1]]), i32([])
+    for kw in (dict(free_pages=free), dict(free_pages=i32([5])), dict(free_count=i32([0]))):
+        with pytest.raises(q.QLError, match="free_pages and free_count"):
+            q.qlinear_kv_extend(i32([1]), i32([1]), table, page_size=4, rows=1, **kw)
+    with pytest.raises(q.QLError):
+        q.qlinear_kv_extend(i32([1]), i32([1]), table, page_size=4, rows=1, free_count_out=i32([0]))

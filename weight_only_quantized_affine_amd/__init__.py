@@ -876,12 +876,16 @@ def qlinear_kv_extend(counts, lens, block_table, *, page_size: int, rows: int, f
         raise QLError(2, "counts must be [n_seqs]")
     n_seqs, max_pages, row = _block_table(block_table, device)
     cap = 0
+    if (free_pages is None) != (free_count is None):
+        raise QLError(1, "free_pages and free_count must be given together")
     if free_pages is not None:
         if free_pages.dim() != 1:
             raise QLError(2, "free_pages must be [entries]")
         cap = free_pages.shape[0]
     counts_at, lens_at = _array(counts, "counts", i32, (n_seqs,), device), _array(lens, "lens", i32, (n_seqs,), device)
     list_at, count_at = _array(free_pages, "free_pages", i32, (cap,), device), _array(free_count, "free_count", i32, (1,), device)
+    if cap == 0 and free_pages is not None:
+        list_at = count_at  # an empty tensor has no address: any that is not NULL, since no entry is touched
     lens_out_at = lens_at if lens_out is None else _array(lens_out, "lens_out", i32, (n_seqs,), device)
     count_out_at = count_at if free_count_out is None else _array(free_count_out, "free_count_out", i32, (1,), device)
     cu_q, cu_at = _result(cu_q, "cu_q", i32, (n_seqs + 1,), counts, device)
