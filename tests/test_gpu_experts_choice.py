@@ -217,3 +217,21 @@ def test_captured_with_the_routed_experts():
             assert ((got[i].double() - want).abs() <= 2.0 ** -7 * mag + 2.0 ** -8 * want.abs()).all()
         layer()
         assert torch.equal(out, got)
+
+
+@pytest.mark.parametrize("renormalize", [False, True])
+@pytest.mark.parametrize("low", [-700.0, -709.0, -709.75, -720.0, -740.0])
+def test_sigmoids_next_to_the_smallest_numbers(low, renormalize):
+    """Logits whose sigmoid, e^x there, lies around and below the smallest normal number of 64 bits: they are still in
+    order, and the k largest of a row of nothing else share the weight by their ratios."""
+    x = (low - torch.arange(9.0) / 4)[None, [3, 0, 7, 5, 1, 8, 2, 6, 4]]
+    ids, w = q.qlinear_select_experts(x.to(DEV), 4, sigmoid=True, renormalize=renormalize, scale=2.0)
+    order = [1, 4, 6, 0]
+    assert ids.tolist() == [order]
+    if renormalize:
+        e = np.exp(f64(x[0, order]) - low)
+        # a p is off by the smallest number, 2^-1074, which is up to 2^-1074 / e^x of it; twice for its share
+        off = 2.0 ** -23 + 4 * np.exp(-1074 * np.log(2.0) - f64(x[0, order]).min())
+        assert (np.abs(f64(w[0]) - 2 * e / e.sum()) <= off * 2).all()
+    else:
+        assert (w == 0).all()

@@ -86,7 +86,7 @@ __device__ __forceinline__ double exp64(double x) {
   p = __builtin_fma(p, r, 1.);
   return __builtin_ldexp(p, (int)fmax(k, -1100.));
 }
-// 1 / x for 1 <= x < 2^1023, by Newton's steps.
+// 1 / x for 1 <= x < 2^1020, by Newton's steps.
 __device__ __forceinline__ double inverse64(double x) {
   double r = __builtin_amdgcn_rcp(x);
   r = __builtin_fma(__builtin_fma(-x, r, 1.), r, r);
@@ -124,7 +124,12 @@ template <int EPL> __global__ __launch_bounds__(256) void select_kernel(const Se
   double p[EPL], c[EPL];
   if (a.sigmoid) {
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) p[j] = x[j] < -709.5f ? 0. : inverse64(1. + exp64(-(double)fminf(x[j], 800.f)));
+    for (int j = 0; j < EPL; ++j) {
+      // far below 0 it is e^x itself (next to it, 1 + e^-x and its inverse leave the normal numbers)
+      const bool far = x[j] < -700.f;
+      const double e = exp64(far ? fmaxf(x[j], -800.f) : -fminf(x[j], 800.f));
+      p[j] = far ? e : inverse64(1. + e);
+    }
   } else {
     float mx = x[0];
 #pragma unroll
@@ -224,8 +229,9 @@ template <int EPL> __global__ __launch_bounds__(256) void select_kernel(const Se
     sum += chosen;
   }
   if (lane < a.k) {
-    double w = my_p * (double)a.scale;
+    double w = my_p;
     if (a.renormalize) w = sum > 0. ? w / sum : 0.;
+    w *= (double)a.scale;
     ids[lane] = my_id;
     weights[lane] = (float)w;
   }
