@@ -428,7 +428,7 @@ ql_status qlinear_kv_append_4bit(const ql_heads* q, const ql_heads* q_out, const
 
 /* The values of cached rows: k_out[i] and v_out[i] [t, hk, d] in dtype (16 bits) get the rows at slots[i], each
  * value code * scale + bias in fp32 rounded once; a slot outside [0, n_pages * page_size) gives zeros.  Slots
- * may repeat.  d as in qlinear_kv_append_4bit. */
+ * may repeat.  d as in qlinear_kv_append_4bit; at most 2^34 - 2^11 values of k and v in all. */
 ql_status qlinear_kv_read_4bit(const ql_paged_cache4* cache, const int64_t* slots, int64_t t, const ql_heads* k_out,
                                const ql_heads* v_out, ql_dtype dtype, void* stream);
 

@@ -251,3 +251,17 @@ def test_norm_of_rows_whose_squares_leave_fp32(magnitude, eps, rot):
     rows = D.stored_rows(f64(k), f64(w), float(np.float32(eps)), np.arange(t), f64(cs) if rot else None, False, "bf16")
     assert np.isfinite(rows).all() and np.abs(rows).max() < 32
     check((magnitude, eps), cache, before, range(t), rows, f64(v).astype(np.float32), group)
+
+
+def test_more_heads_than_tokens_have_room_for():
+    """One token of very many heads: 2^31 chunks of 8 values are the limit, not heads."""
+    t, hk, d = 2, 70000, 512
+    g = torch.Generator(device=DEV).manual_seed(2)
+    k = torch.randn(t, hk, d, generator=g, device=DEV).to(BF)
+    cache = q.qlinear_paged_cache_4bit(1, 3, hk, d, 128)
+    few = q.qlinear_paged_cache_4bit(1, 3, 7, d, 128)
+    q.qlinear_kv_append_4bit(k, k, cache, torch.tensor([2, 0], device=DEV))
+    q.qlinear_kv_append_4bit(k[:, -7:], k[:, -7:], few, torch.tensor([2, 0], device=DEV))
+    slots = torch.tensor([0, 1, 2], device=DEV)
+    for a, b in zip(q.qlinear_kv_read_4bit(cache, slots), q.qlinear_kv_read_4bit(few, slots)):
+        assert torch.equal(a[:, -7:], b) and b[0].abs().sum() > 0

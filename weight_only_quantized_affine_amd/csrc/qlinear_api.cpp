@@ -1086,7 +1086,8 @@ ql_status qlinear_kv_read_4bit(const ql_paged_cache4* cache, const int64_t* slot
   if (t == 0) return ok();
   CHECK(slots && k_out->p && v_out->p, QL_ERR_NULL, "%s: slots, k_out and v_out must not be NULL", fn);
   CHECK(aligned(slots, 8), QL_ERR_ALIGN, "%s: slots must be 8-byte aligned", fn);
-  CHECK(t < (int64_t(1) << 31) / (2 * cache->hk * (cache->d / 8)) - 256, QL_ERR_UNSUPPORTED, "%s: 2^34 values or more", fn);
+  CHECK(t <= ((int64_t(1) << 31) - 256) / (2 * cache->hk * (cache->d / 8)), QL_ERR_UNSUPPORTED,
+        "%s: more than 2^34 - 2^11 values of k and v", fn);
   ql::Read4Args a{};
   a.k = (const uint8_t*)cache->k_codes;
   a.v = (const uint8_t*)cache->v_codes;
