@@ -421,7 +421,8 @@ typedef struct {
  * of qlinear_quantize (fp32, fp16 parameters) and stored.  A row of k is worked out in 64 bits and
  * rounded to fp32 and from there to dtype, so that its codes do not hang on the order of a sum.  A group
  * that holds a NaN or a magnitude past 2^15 is stored with scale 0 and bias NaN.  d a multiple of
- * group_size up to 512; the other arguments as qlinear_kv_append. */
+ * group_size up to 512; t (ceil(hq / 4) + 2 hk) rows of d values, d rounded up to 64, 128, 256 or 512, hold fewer
+ * than 2^35 - 2^12 values; the other arguments as qlinear_kv_append. */
 ql_status qlinear_kv_append_4bit(const ql_heads* q, const ql_heads* q_out, const ql_heads* k, const ql_heads* v,
                                  const ql_paged_cache4* cache, const int64_t* slots, ql_dtype dtype, int64_t t,
                                  const ql_norm_rope* nr, void* stream);
@@ -467,7 +468,7 @@ ql_status qlinear_paged_attention_4bit(const ql_heads* q, const ql_heads* out, q
  * counts, lens int32 [n_seqs], block_table int32 rows of max_pages table_stride apart, free_pages int32 [free_cap],
  * free_count int32 [1]: DEVICE memory.  lens_out may be lens and free_count_out may be free_count; nothing else
  * overlaps.  Entries of free_pages and block_table are not looked at, only moved.  n_seqs < 2^24,
- * rows < 2^31, max_pages * page_size < 2^31. */
+ * rows < 2^31 - 4096, max_pages * page_size < 2^31. */
 ql_status qlinear_kv_extend(const int32_t* counts, const int32_t* lens, int64_t n_seqs, int32_t* block_table,
                             int64_t table_stride, int64_t max_pages, int64_t page_size, int32_t* free_pages,
                             int64_t free_cap, const int32_t* free_count, int32_t* lens_out, int32_t* free_count_out,
@@ -486,8 +487,8 @@ ql_status qlinear_kv_extend(const int32_t* counts, const int32_t* lens, int64_t 
  * ones share the softmax; a row of nothing but -infinity has p = 0.  ids int64 [t, k] are what
  * qlinear_apply_experts takes, weights fp32 [t, k].  n_rows: NULL, or a DEVICE int32: the rows from *n_rows on get
  * ids -1 and weights 0 (the padding of a captured batch).
- * 1 <= e <= 1024, 1 <= k <= min(64, the experts of top_groups groups), n_groups divides e and is at most 64; with
- * one group top_groups must be 1.  logits aligned to their type, ids 8-byte, the others 4-byte. */
+ * t <= 2^26 - 4, 1 <= e <= 1024, 1 <= k <= min(64, the experts of top_groups groups), n_groups divides e and is at
+ * most 64; with one group top_groups must be 1.  logits aligned to their type, ids 8-byte, the others 4-byte. */
 ql_status qlinear_select_experts(const void* logits, ql_dtype dtype, int64_t t, int64_t e, int64_t row_stride,
                                  const float* bias, int sigmoid, int64_t n_groups, int64_t top_groups, int group_top,
                                  int64_t k, int renormalize, float scale, const int32_t* n_rows, int64_t* ids,
@@ -497,8 +498,9 @@ ql_status qlinear_select_experts(const void* logits, ql_dtype dtype, int64_t t, 
  * qlinear_apply_experts with a token's k positions side by side), weights fp32 [t, k] and residual [t, n] or NULL,
  *   out[i, :] = residual[i, :] + sum_j weights[i, j] y[i * k + j, :]
  * in fp32, residual first and j in order, rounded once.  Where ids (int64 [t, k], or NULL) lies outside [0, e) the
- * position adds nothing, whatever y and weights hold; e >= 1 with ids.  y, residual and out share dtype (any ql_dtype) and are
- * contiguous, aligned to their type; out may be residual and overlaps nothing else.  1 <= k <= 64. */
+ * position adds nothing, whatever y and weights hold; e >= 1 with ids.  y, residual and out share dtype (any
+ * ql_dtype) and are contiguous, aligned to their type; out may be residual and overlaps nothing else.
+ * 1 <= k <= 64, t n < 2^31 - 256. */
 ql_status qlinear_combine_experts(const void* y, ql_dtype dtype, const float* weights, const int64_t* ids, int64_t e,
                                   const void* residual, int64_t t, int64_t k, int64_t n, void* out, void* stream);
 

@@ -195,6 +195,18 @@ def test_combine_refusals(lib):
     assert combine(t=0, y=None) == OK and combine(n=0, out=None) == OK
 
 
+def test_launches_of_2_32_threads_are_refused(lib):
+    """The largest launch has 2^32 - 1 threads: 64 a token of a choice, 8 to 64 a row of an append."""
+    for t in ((1 << 26) - 3, 1 << 26, (1 << 31) - 1):
+        assert lib.qlinear_select_experts(FAKE, F32, t, 8, 8, None, 0, 1, 1, 1, 2, 1, 1.0, None, FAKE, FAKE, None) == UNSUPPORTED
+        assert b"2^26" in lib.qlinear_last_error()
+    # 8 + 8 rows of 16 lanes a token, and with 8 heads of q, four a lane, two more; 64 lanes at 512 values
+    for t, d, qh in ((1 << 24, 128, None), (1 << 24, 128, heads()), (15_000_000, 128, heads()), (1 << 22, 512, None)):
+        n, c, k = nrope(), cache(d=d, group_size=64), heads()
+        assert append(lib, qh=qh, qo=qh, k=k, v=k, c=c, t=t, nr=n) == UNSUPPORTED, (t, d)
+        assert b"threads" in lib.qlinear_last_error()
+
+
 def test_combine_takes_ids_only_with_their_number(lib):
     """Without e every id would lie outside [0, e) and no expert be counted."""
     args = lambda ids, e, t=3, n=64: (FAKE, BF16, FAKE, ids, e, None, t, 2, n, FAKE, None)  # noqa: E731

@@ -1055,6 +1055,10 @@ ql_status qlinear_kv_append_4bit(const ql_heads* q, const ql_heads* q_out, const
   ql::Append4Args a{};
   st = append_args(fn, q, q_out, k, v, cache->n_pages, cache->page_size, cache->hk, cache->d, slots, t, nr, a);
   if (st != QL_OK || t == 0) return st;
+  // a row's lanes; at this size a lane holds four rows of q
+  const int64_t lanes = cache->d <= 64 ? 8 : cache->d <= 128 ? 16 : cache->d <= 256 ? 32 : 64;
+  CHECK(t * ((a.hq + 3) / 4 + 2 * cache->hk) * lanes < (int64_t(1) << 32) - 512, QL_ERR_UNSUPPORTED,
+        "%s: 2^32 threads or more (t=%lld)", fn, (long long)t);
   a.k_out = (uint8_t*)cache->k_codes;
   a.v_out = (uint8_t*)cache->v_codes;
   a.ko_ts = a.vo_ts = cache->token_stride;
@@ -1173,6 +1177,7 @@ ql_status qlinear_select_experts(const void* logits, ql_dtype dtype, int64_t t, 
   const char* fn = "qlinear_select_experts";
   CHECK(is_out(dtype), QL_ERR_DTYPE, "%s: dtype must be QL_F32, QL_F16 or QL_BF16", fn);
   CHECK(t >= 0 && t < (int64_t(1) << 31), QL_ERR_SHAPE, "%s: t=%lld must be in [0, 2^31)", fn, (long long)t);
+  CHECK(t <= (int64_t(1) << 26) - 4, QL_ERR_UNSUPPORTED, "%s: t=%lld must be at most 2^26 - 4", fn, (long long)t);
   CHECK(e >= 1 && e <= 1024, QL_ERR_UNSUPPORTED, "%s: e=%lld not supported (1 to 1024)", fn, (long long)e);
   CHECK(n_groups >= 1 && n_groups <= 64 && e % n_groups == 0, QL_ERR_SHAPE,
         "%s: n_groups=%lld must be in [1, 64] and divide e=%lld", fn, (long long)n_groups, (long long)e);
