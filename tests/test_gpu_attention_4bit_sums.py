@@ -18,6 +18,7 @@ import pytest
 import torch
 
 import weight_only_quantized_affine_amd as q
+from test_gpu_paged_attention_4bit import LENS, Problem
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -115,3 +116,72 @@ def test_biases_meet_the_whole_sum_of_a_row(d, group, tokens, n, large):
             tol = 3 * F * (big + 8 * (w @ s)) * (1 + F) + (F + torch.finfo(BF).eps / 2) * o.abs() + 2 * e * big + 2 * (m + 8) * 2.0 ** -24 * big + 2.0 ** -24
             bad = (out[i, h * g:(h + 1) * g].double() - o).abs() > tol
             assert not bad.any(), (i, h, float((out[i, h * g:(h + 1) * g].double() - o).abs().max()), float(tol.max()))
+
+
+def few_rows_tolerance(p, x, n, first, last, cache, scale, sink):
+    """Query rows x [rows, d] that see the positions [first, last) of `cache` (codes and parameters of one kv head, n rows) ->
+    outputs and what each may be off by: every rounding above at its largest, and
+      a weight's relative error e (numerator and sum): what a product over codes drops, d / 32 times LOST max|q| s; the
+                 fp32 sums, (d + 8) u of g = sum |q| (15 s + |b|) (u = 2^-24), and the two halves of the sums of q, 4 u
+                 of it; its scaling and difference, 8 u |score|; the exponential, 2 u
+      2 (n + 8) u sum w (24 s + |b|)    the fp32 sums over the keys and the quotient
+      LOST sum w s                      what the products over codes drop
+      2^-25 |v| a key                   weights below 2^-14, where the largest weighs 2^-8 at least."""
+    u = 2.0 ** -24
+    kc, ks, kb = (y[first:last] for y in parts(cache[0], cache[1]))
+    c, s, b = (y[first:last] for y in parts(cache[2], cache[3]))
+    sc = x @ (kc * ks + kb).T * scale
+    top = sc.amax(-1, keepdim=True)
+    ex = (sc - top).exp()
+    z = ex.sum(-1, keepdim=True) + (0 if sink is None else (sink[:, None] - top).exp())
+    w = ex / z
+    o = w @ (c * s + b)
+    g = (x.abs() @ (15 * ks + kb.abs()).T * scale).amax(-1, keepdim=True)
+    e = scale * LOST * x.abs().amax(-1, keepdim=True) * ks.amax() * (x.shape[1] / 32) + (x.shape[1] + 12) * u * g + 8 * u * sc.abs().amax(-1, keepdim=True) + 2 * u
+    count = last - first
+    tol = F * (1 + F) * (w @ (s * (c - 8)).abs() + w @ (b + 8 * s).abs()) + (F + torch.finfo(p.dtype).eps / 2) * o.abs()
+    tol = tol + 2 * e * (w @ (c * s + b).abs()) + 2 * (count + 8) * u * (w @ (24 * s + b.abs())) + LOST * (w @ s)
+    tol = tol + 2.0 ** -25 * count * (c * s + b).abs().amax() / (ex.sum(-1, keepdim=True) * 2.0 ** -8).clamp(min=1) + 2.0 ** -25
+    return o, tol * (1 + 2.0 ** -6)
+
+
+def check_few(p, got, scale=None, window=0, sinks=None):
+    hk, page, d = p.cache[0].shape[2], p.cache[0].shape[1], p.q.shape[2]
+    g = p.q.shape[1] // hk
+    for s, (n, kv) in enumerate(p.lens):
+        pages = p.table[s, :-(-kv // page)].long().to(DEV)
+        for h in range(hk):
+            cache = [y[pages, :, h].flatten(0, 1)[:kv] for y in p.cache]
+            for i in range(n):
+                at, last = int(p.cu[s]) + i, kv - n + i + 1
+                first = max(0, last - window) if window else 0
+                out = got[at, h * g:(h + 1) * g].double()
+                if last <= first:
+                    assert (out == 0).all()
+                    continue
+                o, tol = few_rows_tolerance(p, p.q[at, h * g:(h + 1) * g].double(), n, first, last, cache, d ** -0.5 if scale is None else scale,
+                                            None if sinks is None else sinks[h * g:(h + 1) * g].double())
+                bad = ~((out - o).abs() <= tol)
+                assert not bad.any(), (s, i, h, float((out - o).abs().max()), float(tol.max()), torch.argwhere(bad)[:4].tolist())
+
+
+@pytest.mark.parametrize("lens", ["tokens", "one", "drafts", "empty"])
+@pytest.mark.parametrize("dtype,hq,hk,d,group,page,heads_first", [
+    (BF, 8, 4, 128, 64, 16, True), (HF, 6, 2, 64, 32, 7, False), (BF, 4, 1, 256, 128, 64, True), (HF, 3, 3, 128, 128, 1, False),
+    (BF, 8, 2, 64, 64, 200, False), (HF, 8, 2, 256, 32, 48, False), (BF, 4, 4, 128, 32, 24, True), (HF, 4, 2, 256, 64, 16, True),
+    (HF, 16, 2, 128, 64, 16, True), (BF, 16, 2, 64, 32, 48, True), (HF, 14, 2, 128, 32, 5, False)])
+def test_every_output_is_within_the_few_row_kernels_own_roundings(lens, dtype, hq, hk, d, group, page, heads_first):
+    """Four tokens of at most eight heads a kv head (four at 256 values) are the few-row kernel's: nothing is allowed for
+    values or keys that round."""
+    p = Problem(LENS[lens], hq, hk, d, group, page, dtype, heads_first=heads_first, seed=31)
+    check_few(p, p.run())
+    check_few(p, p.run(window=60, sinks=p.sinks, scale=0.15), 0.15, 60, p.sinks)
+
+
+@pytest.mark.parametrize("magnitude", [0.02, 1.0, 12.0])
+def test_keys_with_large_biases(magnitude):
+    """Channels of k far from zero, as keys have them: a group's bias is many times its scale."""
+    p = Problem([(1, 900), (4, 350), (2, 64), (1, 1)], 8, 2, 128, 64, 16, BF, seed=32)
+    p.cache[1][..., 1] += torch.randn(p.cache[1].shape[2:4], device=DEV, generator=torch.Generator(device=DEV).manual_seed(1)).to(HF) * 20
+    p.q *= magnitude
+    check_few(p, p.run())
