@@ -434,9 +434,12 @@ ql_status qlinear_kv_read_4bit(const ql_paged_cache4* cache, const int64_t* slot
                                const ql_heads* v_out, ql_dtype dtype, void* stream);
 
 /* qlinear_paged_attention over such a cache; arguments, masks, sinks, limits and workspace as there, dtype that of
- * q and out.  Keys enter as they are or rounded to fp16 (below 2^-14 an absolute 2^-25), q with 11 significant bits
- * (bf16: exact); values, weights, or products of a weight and a scale, round to fp16 before they are summed in fp32.
- * A cached value past 65504 may be taken as infinite. */
+ * q and out.  A sequence of few rows (new tokens times hq / hk at most 16, in calls without longer ones up to 32) is
+ * worked out from the codes: keys and values enter as they are, but a product of 32 terms drops up to 2^-14 of the
+ * largest |q| times scale of a key, or weight times scale of a value, among them; weights, and products of a weight and
+ * a scale, round to fp16.  For other sequences cached keys and values round to fp16 (below 2^-14 an absolute 2^-25), and
+ * so do the weights.  q enters with 11 significant bits (bf16: exact; values below 2^-24 of their row's largest with an
+ * absolute 2^-35 of that).  Sums are in fp32.  A cached value past 65504 may be taken as infinite. */
 size_t qlinear_paged_attention_4bit_workspace_size(int64_t t, int64_t n_seqs, int64_t hq, int64_t hk, int64_t d,
                                                    int64_t max_q, int64_t max_pages, int64_t page_size, int64_t window);
 ql_status qlinear_paged_attention_4bit(const ql_heads* q, const ql_heads* out, ql_dtype dtype, int64_t t,

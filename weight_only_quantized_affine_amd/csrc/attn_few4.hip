@@ -3,8 +3,8 @@
 //
 // No value is decoded.  A code masked into the low bits of a half is the fp16 subnormal c 2^-24, or 16 c 2^-24
 // four bits further up, so a word of eight codes becomes an operand of the 16x16x32 product by one shift and
-// four masks, and scales and biases enter in fp32:
-//   scores   q.k = sum over groups of s (q.c) + b sum(q), one accumulator a group;
+// four masks, and scales and biases enter as they are:
+//   scores   q.k = sum over groups of s (q.c) + b sum(q), one accumulator a group, sum(q) as two fp16 numbers;
 //   output   sum_j w_j v_j = sum_j (w_j s_j) (c_j - 8) + sum_j w_j (b_j + 8 s_j), the products w s and the weights
 //            of the second sum rounded to fp16 (as large as a rounding of w in w v, since a group's middle is
 //            taken out), the sum of the w s taken out 8 times.
@@ -19,16 +19,16 @@
 // of the keys that the reading lanes' addresses give: the order in which the lane holds the scores.
 // (Decoding every code to fp16 by 13 instructions a word: 131071 tokens 54 us, 64 ragged sequences 105.)
 //
-// Bound by the vector units next to memory: a tile of 64 positions takes some 520 vector instructions a wave, the
-// ragged batch 700 with its items' starts and ends.  Two workgroups a compute unit share its registers (three,
+// Bound by the vector units next to memory: a tile of 64 positions takes some 540 vector instructions a wave, the
+// ragged batch 730 with its items' starts and ends.  Two workgroups a compute unit share its registers (three,
 // with fewer each: 131071 tokens 53 us against 46).  V of two tiles lies in LDS and K of one, whose codes are in
 // registers before the next K is copied; sums of weight times bias and of the codes' middles are extra rows of
 // the products where registers allow (kSumInRow; both steps together: 64 ragged sequences 71 -> 61 us).
 //
 // Measured (bf16, 32 heads on 8 of 128, groups of 64): 64 ragged sequences of 100 to 16000 tokens, pages of 16,
-// 58 to 62 us, 3.5 TB/s with the joining; one of 131071 tokens, pages of 64, 45 us; 64 sequences of 5 drafted
-// tokens 106.  64 values a head 75, 256 values 87, groups of 32 94, of 128 59; token-major pages 102, pages of 24
-// 75.  (The 16-bit cache: 139 and 97 us.)
+// 59 to 63 us, 3.4 TB/s with the joining; one of 131071 tokens, pages of 64, 47 us; 64 sequences of 5 drafted
+// tokens 107.  64 values a head 79, 256 values 87, groups of 32 89, of 128 59; token-major pages 103, pages of 24
+// 73.  (The 16-bit cache: 139 and 97 us.)
 #include "attn_common4.hpp"
 #include "attn_few.hpp"
 

@@ -27,12 +27,13 @@
 // in registers and decodes a word of them between every two products of the scores, whose matrix instructions
 // leave the vector units free (all of it at the period's end: 1000 tokens at 32767 628 us, 577 so; by all
 // eight waves, half a tile each: 643; at 256 values a head, where the waves are in step, 882 and 757).  13
-// instructions decode a word of 8 values, once for 256 rows.  Measured, groups of 64: 4096 tokens 178 us, 1000
-// tokens at 32767 577 us, 920 TFLOP/s, 64 and 256 values a head 825 and 757 us: a sixth more than from 16 bits,
-// for the vector units' share.  (Decoding the sequences to a 16-bit copy first would take a workspace four
+// instructions decode a word of 8 values, once for 256 rows.  Measured with the joining, one call after the other,
+// groups of 64: 4096 tokens 181 us, 1000 tokens at 32767 577 to 585 us, 910 TFLOP/s, 64 and 256 values a head 825 and
+// 759 us: 17 to 29 % more than from 16 bits, for the vector units' share.  (Decoding the sequences to a 16-bit copy first would take a workspace four
 // times their cache.)  A decoded value rounds to fp16, which a matrix operand is: 2^-11 of it at most, where
-// the code itself stands for its value to some hundredths; fp16 outputs are then off by 0.0005 of their size,
-// where their own rounding is 0.0002 (bf16 outputs by their rounding, 0.0017).
+// the code itself stands for its value to some hundredths; fp16 outputs are then off by 0.0004 to 0.0008 of
+// their size (the larger the scores, the more), as the roundings alone would have it, where their own rounding is
+// 0.0002 (bf16 outputs by their rounding, 0.0017).
 //
 // Work split.  With enough items (sequence, kv head, row tile) to fill the chip, one workgroup each,
 // the longest first, kv heads fastest so that a head's tiles run on one XCD and share its L2.  Else

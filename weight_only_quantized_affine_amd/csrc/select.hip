@@ -19,8 +19,8 @@ namespace {
 // lowest index: a round takes the lane's largest, the wave's by DPP, and a ballot.  Rounds compare fp32 keys and
 // look at 64 bits only where more than one lane has the largest.
 //
-// Measured: one token of 128 experts 4.2 us; 8192 tokens of 256 experts, sigmoid, 4 of 8 groups, 8 chosen, 18 us
-// against 2 of memory: bound by the vector units, 1000 instructions a token, issue 86 % busy (the coefficients of
+// Measured: one token of 128 experts 4.2 us; 8192 tokens of 256 experts, sigmoid, 4 of 8 groups, 8 chosen, 17 to 18 us
+// against 2 of memory: bound by the vector units, 950 instructions a token, issue 82 % busy (the coefficients of
 // the exponential as scalar operands, a sixth fewer instructions: 17.9 against 17.9; each lane's experts in
 // order before the rounds, which then only shift them: 18.9).
 
