@@ -241,7 +241,10 @@ template <int EPL> __global__ __launch_bounds__(256) void select_kernel(const Se
 //
 // out = residual + sum_j w_j y_j: k + 2 rows of memory traffic for k products a value, so memory bounds it.
 // A thread holds 16 bytes of a row and has the loads of four positions in flight, ids or not (a load that waits
-// for its id: 4096 tokens of 8 x 4096 values 86 us, so 63, 5.3 TB/s; 16 tokens of 4 3.2 us).
+// for its id: 4096 tokens of 8 x 4096 values 86 us, so 63, 5.3 TB/s; 16 tokens of 4 3.2 us).  Rows that are no
+// multiples of 16 bytes go one value a thread: 8 x 4095 values in bf16 83 us, in fp32, whose 4 bytes a lane suffice, 117
+// against 124 of 4096.  A token of fewer positions than are in flight loads its last one again, out of the cache: one
+// position of 4096 values 17 us, 5.9 TB/s, but of 4095, with 8 in flight, 60.
 
 template <int DT> struct Elem;
 template <> struct Elem<DT_F32> {
